@@ -13,7 +13,9 @@ Low-level names mirror ``include/gemm.h``: ``gemm_create``, ``gemm_run``,
 ``gemm_host_io_enable``, ``gemm_run_host_batch``, ``gemm_pair_schedule``,
 ``gemm_cta_schedule``, ``gemm_decode_ring``, ``gemm_run_splitk_noalloc``,
 ``gemm_noalloc_status``, ``gemm_run_mx``, ``gemm_trace_set``.
-``Gemm`` wraps a handle for torch tensors.
+``Gemm`` wraps a handle for torch tensors.  The operators of
+mixture-of-experts layers and of 4-bit weights (``Route``, ``Permute``,
+``GroupedGemm``, ``W4Gemm``) are in ``experts.py``.
 """
 from __future__ import annotations
 
@@ -40,7 +42,12 @@ EXPORTED = ["gemm_create", "gemm_run", "gemm_get_status", "gemm_destroy", "gemm_
             "gemm_plan_string", "gemm_workspace_bytes", "gemm_raster_tile", "gemm_debug_set",
             "gemm_run_splitk_noalloc", "gemm_noalloc_status", "gemm_timing_enable", "gemm_timing_read",
             "gemm_host_io_enable", "gemm_run_host_batch", "gemm_pair_schedule",
-            "gemm_cta_schedule", "gemm_decode_ring", "gemm_run_mx", "gemm_trace_set"]
+            "gemm_cta_schedule", "gemm_decode_ring", "gemm_run_mx", "gemm_trace_set",
+            "gemm_op_status", "gemm_op_destroy", "gemm_op_workspace_bytes", "gemm_op_plan_string",
+            "gemm_op_debug_set", "gemm_route_create", "gemm_route_run", "gemm_route_backward",
+            "gemm_permute_create", "gemm_permute_gather", "gemm_permute_combine",
+            "gemm_permute_combine_backward", "gemm_grouped_create", "gemm_grouped_run",
+            "gemm_w4_create", "gemm_w4_run"]
 GEMM_TRACE_EVENTS = 32
 GEMM_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -52,6 +59,32 @@ class GemmDesc(ctypes.Structure):
                 ("layout_c", ctypes.c_int), ("layout_d", ctypes.c_int),
                 ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64), ("ldc", ctypes.c_int64),
                 ("ldd", ctypes.c_int64)]
+
+
+class RouteDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("type", ctypes.c_int), ("normalize", ctypes.c_int32), ("ld", ctypes.c_int64)]
+
+
+class PermuteDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("k", ctypes.c_int32),
+                ("type", ctypes.c_int), ("ld_tokens", ctypes.c_int64),
+                ("ld_rows", ctypes.c_int64)]
+
+
+class GroupedDesc(ctypes.Structure):
+    _fields_ = [("form", ctypes.c_int), ("E", ctypes.c_int32), ("R", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("ab_type", ctypes.c_int),
+                ("c_type", ctypes.c_int), ("d_type", ctypes.c_int), ("layout_b", ctypes.c_int),
+                ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64), ("ldc", ctypes.c_int64),
+                ("ldd", ctypes.c_int64)]
+
+
+class W4Desc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("group", ctypes.c_int32), ("has_zeros", ctypes.c_int32),
+                ("R", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("x_type", ctypes.c_int), ("scale_type", ctypes.c_int), ("d_type", ctypes.c_int),
+                ("ldx", ctypes.c_int64), ("ldd", ctypes.c_int64)]
 
 
 class GemmError(RuntimeError):
@@ -119,6 +152,22 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
     lib.gemm_run_host_batch.argtypes = [vp, ci, ctypes.POINTER(vp), ctypes.POINTER(vp),
                                         ctypes.POINTER(vp), ctypes.POINTER(vp), vp]
     lib.gemm_run_host_batch.restype = ci
+    for name, desc in (("gemm_route_create", RouteDesc), ("gemm_permute_create", PermuteDesc),
+                       ("gemm_grouped_create", GroupedDesc), ("gemm_w4_create", W4Desc)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(vp), ctypes.POINTER(desc)]
+    for name, pointers in (("gemm_route_run", 6), ("gemm_route_backward", 5),
+                           ("gemm_permute_gather", 4), ("gemm_permute_combine", 4),
+                           ("gemm_permute_combine_backward", 7), ("gemm_grouped_run", 5),
+                           ("gemm_w4_run", 6)):
+        # handle, operands, stream
+        getattr(lib, name).argtypes = [vp] * (pointers + 2)
+        getattr(lib, name).restype = ci
+    lib.gemm_op_status.argtypes = [vp, vp]
+    lib.gemm_op_destroy.argtypes = [vp]
+    lib.gemm_op_workspace_bytes.argtypes = [vp]
+    lib.gemm_op_workspace_bytes.restype = i64
+    lib.gemm_op_plan_string.argtypes = [vp, ctypes.c_char_p, ctypes.c_size_t]
+    lib.gemm_op_debug_set.argtypes = [vp, ci, ctypes.c_uint64]
     _lib = lib
     return lib
 
@@ -411,3 +460,14 @@ def matmul_add(A, B, C=None, out_dtype=None, D=None, stream=None):
     finally:
         g.close()
     return D
+
+
+_EXPERTS = ("GroupedGemm", "Permute", "Route", "W4Gemm", "grouped_matmul", "pack_w4", "w4_matmul")
+
+
+def __getattr__(name):
+    # experts.py needs torch at import; this module does not
+    if name in _EXPERTS:
+        from . import experts
+        return getattr(experts, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -37,6 +37,11 @@ UNITS = [
     ("decode.cu", [], "decode.o"),
     ("decode_mma.cu", [], "decode_mma.o"),
     ("i8_mma.cu", [], "i8_mma.o"),
+    ("moe_host.cu", [], "moe_host.o"),
+    ("route.cu", [], "route.o"),
+    ("permute.cu", [], "permute.o"),
+    ("grouped.cu", [], "grouped.o"),
+    ("w4.cu", [], "w4.o"),
 ]
 
 

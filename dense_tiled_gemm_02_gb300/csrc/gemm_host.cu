@@ -14,6 +14,7 @@
 
 #include "common.h"
 #include "gemm.h"
+#include "moe.h"
 #include "plan_table.h"
 #include "tc_launch.h"
 
@@ -72,6 +73,14 @@ EncodeFn get_encode() {
   });
   return fn;
 }
+
+}  // namespace
+
+namespace gb300 {
+void* tensor_map_encoder() { return reinterpret_cast<void*>(get_encode()); }
+}  // namespace gb300
+
+namespace {
 
 // cluster = 0: a variant without cluster split-K; cluster >= 2: the one
 // with the smallest cluster capacity that holds `cluster` splits.

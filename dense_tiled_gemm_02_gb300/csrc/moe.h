@@ -1,0 +1,116 @@
+// moe.h -- parameters and launches of the mixture-of-experts and 4-bit-weight
+// kernels (route.cu, permute.cu, grouped.cu, w4.cu), used by moe_host.cu.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "common.h"
+
+namespace gb300 {
+
+// The driver's cuTensorMapEncodeTiled, or null (gemm_host.cu).
+void* tensor_map_encoder();
+
+// Status bit beside STATUS_TIMEOUT: offsets or row indices out of range.
+constexpr uint32_t STATUS_BAD_INDEX = 2u;
+
+// The rows [lo, hi) of expert e; empty, with the status set, when the offsets
+// decrease or leave [0, R].
+__device__ __forceinline__ int2 expert_rows(const int* offsets, int e, int R, uint32_t* status) {
+  int2 r = make_int2(offsets[e], offsets[e + 1]);
+  if (r.x < 0 || r.y < r.x || r.y > R) {
+    atomicOr(status, STATUS_BAD_INDEX);
+    r.y = r.x = 0;
+  }
+  return r;
+}
+
+// ---------------------------------------------------------------- routing (route.cu)
+struct RouteParams {
+  int T, E, k, type, normalize;
+  long long ld;
+  const void* logits;
+  int* experts;
+  float* gates;
+  int* offsets;
+  int* row_slot;
+  int* slot_row;
+  int blocks, tokens_per_block;  // several-block form
+  int* hist;                     // [blocks][E]: counts, then each block's first row per expert
+  unsigned* ticket;              // zero between calls
+};
+// Blocks of the forward kernel; 1: one block does the whole call.
+int route_blocks(long long T, int k, int num_sms);
+cudaError_t launch_route(const RouteParams& p, cudaStream_t st);
+
+struct RouteBackwardParams {
+  int T, E, k, type, normalize;
+  long long ld;
+  const void* logits;
+  const int* experts;
+  const float* gates;
+  const float* dgates;
+  void* dlogits;
+};
+cudaError_t launch_route_backward(const RouteBackwardParams& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- row movement (permute.cu)
+struct PermuteParams {
+  long long T, H;
+  int k, type;
+  long long ld_tokens, ld_rows;
+  const void* tokens;  // X, or dY
+  void* tokens_out;    // Y
+  const void* rows;    // Ys
+  void* rows_out;      // Xs, or dYs
+  const int* row_slot;
+  const int* slot_row;
+  const float* gates;
+  float* dgates;
+  uint32_t* status;
+};
+cudaError_t launch_gather(const PermuteParams& p, cudaStream_t st);
+cudaError_t launch_combine(const PermuteParams& p, cudaStream_t st);
+cudaError_t launch_combine_backward(const PermuteParams& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- grouped products (grouped.cu)
+// The tensor cores' M dimension is D's columns ("features", contiguous in
+// D), their N dimension D's rows: a row tile takes any multiple of 32 rows
+// up to 256, so that a ragged group costs about its own length.
+struct GroupedParams {
+  int grad;            // GEMM_GROUPED_GRAD: the sum runs over an expert's rows
+  int E, R, K, N;
+  int f_mn;            // features operand MN-major (B row-major)
+  uint32_t idesc;      // instruction descriptor without its N field
+  const int* offsets;
+  const void* C;
+  int d_type;          // also C's
+  long long ldc, ldd;
+  void* D;
+  uint32_t* status;
+  unsigned long long timeout_ns;
+  int debug_flags;
+};
+// Tensor maps: the features operand; the rows operand in boxes of 128 rows
+// and of 32 (rows form; both 64 x 64 boxes of the MN-major operand in grad).
+cudaError_t launch_grouped(const CUtensorMap& f, const CUtensorMap& x128, const CUtensorMap& x32,
+                           const GroupedParams& p, int grid, cudaStream_t st);
+cudaError_t prepare_grouped();
+
+// ---------------------------------------------------------------- 4-bit weights (w4.cu)
+struct W4Params {
+  int E, R, K, N, group, groups;
+  int x_type, scale_type, d_type;
+  long long ldx, ldd;
+  const void* X;
+  const uint8_t* W;
+  const void* scales;
+  const uint8_t* zeros;  // null: 8
+  const int* offsets;    // null: all rows to expert 0
+  void* D;
+  uint32_t* status;
+};
+cudaError_t launch_w4(const W4Params& p, int num_sms, cudaStream_t st);
+
+}  // namespace gb300

@@ -392,6 +392,181 @@ GEMM_API int gemm_debug_set(gemm_handle_t h, int flags, uint64_t timeout_ns);
 #define GEMM_TRACE_EVENTS 32
 GEMM_API int gemm_trace_set(gemm_handle_t h, uint64_t* dev_buf);
 
+/*
+ * Operators of mixture-of-experts layers and of 4-bit weights.  The source
+ * pages have no counterpart; these are the products and row movements a
+ * language model needs around the GEMM above.  All follow its conventions:
+ * a handle (gemm_op_t) is created for fixed sizes and types, holds any
+ * workspace and a device status word, and its run calls only enqueue on the
+ * caller's stream (no allocation, no synchronisation, nothing read back).
+ * One handle must not be used by two streams at the same time.  Run calls
+ * return GEMM_OK, GEMM_ERR_INVALID_ARG (a null pointer, a handle of another
+ * operator or of another device than the current one),
+ * GEMM_ERR_MISALIGNED or GEMM_ERR_CUDA.
+ *
+ * Experts are numbered 0 .. E-1, E <= GEMM_MAX_EXPERTS.  Rows sorted by
+ * expert are described by `offsets`, E + 1 int32 values in device memory:
+ * the rows of expert e are offsets[e] <= r < offsets[e + 1]; a group may be
+ * empty, and rows at or past offsets[E] belong to no expert.  The kernels
+ * read the offsets on the device, so a call never waits for the host to see
+ * them.  Offsets that decrease or leave [0, R] are not followed: the groups
+ * they bound count as empty and gemm_op_status reports
+ * GEMM_ERR_INVALID_ARG (the outputs are then undefined, but nothing outside
+ * the operands is read or written).
+ */
+#define GEMM_MAX_EXPERTS 1024
+#define GEMM_MAX_TOP_K 32
+
+typedef struct gemm_op* gemm_op_t;
+
+/* gemm_op_status: synchronise stream, then return and clear the handle's
+ * device status word: GEMM_OK, GEMM_ERR_DEVICE_TIMEOUT (a bounded device-side
+ * wait of a grouped product expired) or GEMM_ERR_INVALID_ARG (offsets or row
+ * indices out of range); GEMM_ERR_CUDA if the synchronisation fails. */
+GEMM_API int gemm_op_status(gemm_op_t op, gemm_stream_t stream);
+
+/* gemm_op_destroy: synchronise the device and free the handle; NULL is a no-op. */
+GEMM_API int gemm_op_destroy(gemm_op_t op);
+
+/* gemm_op_workspace_bytes: device workspace held by the handle, or -1. */
+GEMM_API int64_t gemm_op_workspace_bytes(gemm_op_t op);
+
+/* gemm_op_plan_string: one line naming the operator and the kernel variant
+ * chosen, written to buf (at most n bytes with the terminator); returns its
+ * full length. */
+GEMM_API int gemm_op_plan_string(gemm_op_t op, char* buf, size_t n);
+
+/* gemm_op_debug_set: the test hook of gemm_debug_set, for the grouped
+ * product's ring (the other operators wait for nothing and ignore it). */
+GEMM_API int gemm_op_debug_set(gemm_op_t op, int flags, uint64_t timeout_ns);
+
+/*
+ * Token routing.  logits: T rows of E values (ld elements apart, 0 = E) of
+ * type F16, BF16 or F32.  Each token t chooses the k largest of its logits,
+ * in falling order; equal logits go to the lower expert, NaN counts as above
+ * every number, and a logit of -inf is never chosen.  Outputs:
+ *   experts  T x k int32: the chosen experts, -1 where fewer than k logits
+ *            of the token are above -inf
+ *   gates    T x k fp32: the softmax of the chosen logits over the chosen
+ *            ones (normalize != 0) or over all E; 0 where experts is -1
+ *   offsets  E + 1 int32: the groups of the slots t * k + j sorted by expert,
+ *            slots of one expert in rising order (a stable sort)
+ *   row_slot T * k int32: the slot of each sorted row, -1 at or past
+ *            offsets[E]
+ *   slot_row T x k int32: the sorted row of each slot, -1 where unrouted
+ * The result does not depend on how threads are scheduled.  1 <= k <=
+ * min(E, GEMM_MAX_TOP_K).  T zero sets offsets to zero.
+ * gemm_route_backward: dlogits (laid out like logits, of their type) from
+ * dgates (T x k fp32) and the forward pass's logits, experts and gates: with
+ * s = sum_j gates_j dgates_j of the token, gates_j (dgates_j - s) at the
+ * chosen experts (and -p_e s elsewhere, p the softmax over all E, when
+ * normalize is 0); zero at logits of -inf.  Sums and exponentials are fp32.
+ */
+typedef struct {
+  int64_t T;
+  int32_t E, k;
+  gemm_dtype_t type;
+  int32_t normalize;
+  int64_t ld;
+} gemm_route_desc_t;
+GEMM_API int gemm_route_create(gemm_op_t* out, const gemm_route_desc_t* desc);
+GEMM_API int gemm_route_run(gemm_op_t op, const void* logits, int32_t* experts, float* gates,
+                            int32_t* offsets, int32_t* row_slot, int32_t* slot_row,
+                            gemm_stream_t stream);
+GEMM_API int gemm_route_backward(gemm_op_t op, const void* logits, const int32_t* experts,
+                                 const float* gates, const float* dgates, void* dlogits,
+                                 gemm_stream_t stream);
+
+/*
+ * Rows of tokens into expert order and back.  Token arrays have T rows of H
+ * elements (ld_tokens apart), sorted arrays T * k rows (ld_rows apart); type
+ * F16, BF16 or F32; row_slot and slot_row as gemm_route_run writes them.
+ *   gather:   Xs[slot_row[t, j]] = X[t]
+ *   combine:  Y[t] = sum_j gates[t, j] Ys[slot_row[t, j]]   (gates NULL: 1;
+ *             the gradient of gather is combine without gates)
+ *   combine_backward:  dYs[slot_row[t, j]] = gates[t, j] dY[t] and
+ *             dgates[t, j] = <dY[t], Ys[slot_row[t, j]]> (fp32)
+ * Unrouted slots add nothing and get dgates 0; rows whose row_slot is
+ * negative are set to zero by gather and combine_backward.  Sums are fp32 in
+ * a fixed order, rounded once.  Indices outside [-1, T * k) count as -1 and
+ * set the status.  Outputs must not overlap inputs.
+ */
+typedef struct {
+  int64_t T, H;
+  int32_t k;
+  gemm_dtype_t type;
+  int64_t ld_tokens, ld_rows;
+} gemm_permute_desc_t;
+GEMM_API int gemm_permute_create(gemm_op_t* out, const gemm_permute_desc_t* desc);
+GEMM_API int gemm_permute_gather(gemm_op_t op, const void* X, const int32_t* row_slot,
+                                 const int32_t* slot_row, void* Xs, gemm_stream_t stream);
+GEMM_API int gemm_permute_combine(gemm_op_t op, const void* Ys, const int32_t* slot_row,
+                                  const float* gates, void* Y, gemm_stream_t stream);
+GEMM_API int gemm_permute_combine_backward(gemm_op_t op, const void* dY, const void* Ys,
+                                           const int32_t* row_slot, const int32_t* slot_row,
+                                           const float* gates, void* dYs, float* dgates,
+                                           gemm_stream_t stream);
+
+/*
+ * Products grouped by expert.  A is R x K, row-major (lda).
+ *   GEMM_GROUPED_ROWS: D[r, n] = sum_k A[r, k] B_e[k, n] (+ C[r, n]) for the
+ *     rows r of expert e.  B holds E matrices K x N one after another:
+ *     layout_b GEMM_ROW_MAJOR E * K rows of N (ldb apart), GEMM_COL_MAJOR
+ *     E * N rows of K.  C and D are R x N, row-major; rows of no expert are
+ *     not written.  (The input gradient dX = dY B^T is the same form with
+ *     the other layout and K and N exchanged.)
+ *   GEMM_GROUPED_GRAD: D_e[k, n] = sum over the rows r of expert e of
+ *     A[r, k] B[r, n] (+ C_e[k, n]).  B is R x N, row-major; C and D hold
+ *     E matrices K x N as E * K rows of N.  An expert without rows gets C_e,
+ *     or zeros.  (The weight gradient, A the layer's input and B the output's
+ *     gradient.)
+ * ab_type F16 or BF16, d_type F16, BF16 or F32; c_type 0 (no C) or d_type.
+ * fp32 accumulation, C added in fp32, one rounding.  C may be D.  lda, ldb,
+ * ldc, ldd: 0 = packed.  A and B are read by TMA: rows that are not 16-byte
+ * multiples are copied to aligned workspace rows first, and a base pointer
+ * that is not 16-byte aligned while its rows are is GEMM_ERR_MISALIGNED.
+ * C and D need only their element's alignment.  A value of one expert never
+ * reaches another's output, not even as a NaN.
+ */
+typedef enum { GEMM_GROUPED_ROWS = 0, GEMM_GROUPED_GRAD = 1 } gemm_grouped_form_t;
+typedef struct {
+  gemm_grouped_form_t form;
+  int32_t E;
+  int64_t R, K, N;
+  gemm_dtype_t ab_type, c_type, d_type;
+  gemm_layout_t layout_b;
+  int64_t lda, ldb, ldc, ldd;
+} gemm_grouped_desc_t;
+GEMM_API int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc);
+GEMM_API int gemm_grouped_run(gemm_op_t op, const void* A, const void* B, const int32_t* offsets,
+                              const void* C, void* D, gemm_stream_t stream);
+
+/*
+ * Rows times 4-bit weights.  D[r, n] = sum_k X[r, k] w_e[n, k], with
+ * w_e[n, k] = (q - z) * s: q the 4-bit value of weight (n, k), W holding E
+ * matrices of N rows of K / 2 bytes, weight k in the low half of byte k / 2
+ * when k is even and in the high half when it is odd; s = scales[e, n,
+ * k / group] (scale_type F16, BF16 or F32) and z = zeros[e, n, k / group]
+ * (bytes 0..15, has_zeros != 0) or 8.  scales
+ * and zeros hold E x N x ceil(K / group) values.  X is R x K (ldx), type F16
+ * or BF16; D R x N (ldd), F16, BF16 or F32.  With E = 1 offsets may be NULL
+ * (all R rows); otherwise they group the rows as above, and rows of no expert
+ * are not written.  K and group are multiples of 32, W is 16-byte aligned and
+ * so are X's rows.  Products of X with the integers q - z are summed in fp32 per
+ * group, scaled in fp32, and rounded once.  Made for the few rows of a
+ * decode step: the weights are read once for every 32 rows of an expert.
+ */
+typedef struct {
+  int32_t E, group, has_zeros;
+  int64_t R, K, N;
+  gemm_dtype_t x_type, scale_type, d_type;
+  int64_t ldx, ldd;
+} gemm_w4_desc_t;
+GEMM_API int gemm_w4_create(gemm_op_t* out, const gemm_w4_desc_t* desc);
+GEMM_API int gemm_w4_run(gemm_op_t op, const void* X, const uint8_t* W, const void* scales,
+                         const uint8_t* zeros, const int32_t* offsets, void* D,
+                         gemm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
