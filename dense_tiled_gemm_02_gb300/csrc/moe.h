@@ -70,9 +70,9 @@ struct PermuteParams {
   float* dgates;
   uint32_t* status;
 };
-cudaError_t launch_gather(const PermuteParams& p, cudaStream_t st);
-cudaError_t launch_combine(const PermuteParams& p, cudaStream_t st);
-cudaError_t launch_combine_backward(const PermuteParams& p, cudaStream_t st);
+cudaError_t launch_gather(const PermuteParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_combine(const PermuteParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_combine_backward(const PermuteParams& p, int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- grouped products (grouped.cu)
 // The tensor cores' M dimension is D's columns ("features", contiguous in

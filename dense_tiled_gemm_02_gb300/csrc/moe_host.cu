@@ -304,7 +304,7 @@ int gemm_permute_gather(gemm_op_t op, const void* X, const int32_t* row_slot,
   p.rows_out = Xs;
   p.row_slot = row_slot;
   p.slot_row = slot_row;
-  return launched(launch_gather(p, static_cast<cudaStream_t>(stream)));
+  return launched(launch_gather(p, op->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int gemm_permute_combine(gemm_op_t op, const void* Ys, const int32_t* slot_row, const float* gates,
@@ -320,7 +320,7 @@ int gemm_permute_combine(gemm_op_t op, const void* Ys, const int32_t* slot_row, 
   p.tokens_out = Y;
   p.slot_row = slot_row;
   p.gates = gates;
-  return launched(launch_combine(p, static_cast<cudaStream_t>(stream)));
+  return launched(launch_combine(p, op->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int gemm_permute_combine_backward(gemm_op_t op, const void* dY, const void* Ys,
@@ -341,7 +341,7 @@ int gemm_permute_combine_backward(gemm_op_t op, const void* dY, const void* Ys,
   p.slot_row = slot_row;
   p.gates = gates;
   p.dgates = dgates;
-  return launched(launch_combine_backward(p, static_cast<cudaStream_t>(stream)));
+  return launched(launch_combine_backward(p, op->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 // ---------------------------------------------------------------- grouped products
