@@ -3,17 +3,29 @@
 //   rows:  D[r,n]   = sum_k A[r,k] B_e[k,n] (+ C)         for the rows r of e
 //   grad:  D_e[k,n] = sum over e's rows r of A[r,k] B[r,n] (+ C)
 //
-// tcgen05 with D's columns ("features") as the M dimension, 128 to a tile,
+// tcgen05 with D's columns ("features") as the M dimension, 128 to a CTA,
 // and D's rows as the N dimension.  The M of an MMA is fixed while its N is
 // any multiple of 32 up to 256, so the ragged side goes to N: a group of m
-// rows is cut into ceil(m / 256) tiles of equal width and costs about m rows
+// rows is cut into ceil(m / QT) tiles of equal width and costs about m rows
 // of tensor time, not m rounded up to a tile; a decode step's one or two rows
-// cost a 32-wide MMA while the weights stream.  An accumulator's lanes are
-// then consecutive features: lane-consecutive stores run along D's rows.
+// cost a 32-wide MMA while the weights stream.
 //
-// Every CTA reads the offsets and counts the tiles of each expert into a
-// prefix sum in shared memory; tile t of the persistent loop finds its expert
-// by bisection.  No host knowledge of the groups, one launch.
+// Two forms of one kernel:
+//   wide    CTA pairs (cta_group::2), 256 features x up to 256 rows; each CTA
+//           stages its 128 features and half of the rows, six 32 KB stages.
+//           Bound by the tensor pipe.
+//   narrow  single CTAs, 128 features x up to 64 rows, eight 24 KB stages: for
+//           groups of few rows, where reading the weights is the bound and
+//           bytes in flight count.
+//
+// Every CTA reads the offsets and counts the row tiles of each expert into a
+// prefix sum in shared memory, from which any tile or K slice finds its
+// expert by bisection: no host knowledge of the groups, one launch.  Tiles
+// are dealt round-robin; what would be a partial last wave (with one full
+// wave before it) is dealt as equal runs of K slices instead.  The pieces of
+// a tile that several units then share leave fp32 partial sums, and whichever
+// of them finishes last adds them up in K order and stores D: no unit waits
+// for another, and the result does not depend on who is last.
 //
 // Nothing of another expert enters a sum, not even as 0 * NaN: rows past a
 // group's end are columns of the accumulator that are not stored (rows), and
@@ -25,6 +37,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "gemm.h"
 #include "moe.h"
 #include "ptx.cuh"
@@ -34,99 +48,310 @@ namespace gb300 {
 
 namespace {
 
-constexpr int FT = 128;              // features of a tile
-constexpr int QT = 256;              // most D rows of a tile
-constexpr int STAGES = 4;
+constexpr int FT = 128;                       // features of a CTA
 constexpr uint32_t F_BYTES = FT * BK * 2;
-constexpr uint32_t X_BYTES = QT * BK * 2;
-constexpr int RASTER = 8;            // row tiles that share a features tile in L2
+constexpr int RASTER = 8;                     // row tiles that share a features tile in L2
+constexpr int MIN_RUN = 8;                    // K slices: a shorter run costs more than it saves
+constexpr uint32_t EPI_BYTES = 32 * 64;       // staged 32 rows x 32 features of 16 bits
+// warp 0: TMA loads, 1: MMA issue, 2-5: epilogue, 6: schedule, 7: clears the
+// rows past a group (grad)
+constexpr int GROUPED_THREADS = 256;
+constexpr int QUEUE = 4;                      // pieces the schedule runs ahead
 
-constexpr uint32_t grouped_smem() {
-  return STAGES * (F_BYTES + X_BYTES) + 1024 /* alignment */ + 256 /* barriers */;
+template <int CG, int QT, int STAGES>
+struct Cfg {
+  static constexpr uint32_t X_BYTES = (QT / CG) * BK * 2;
+  static constexpr uint32_t STAGE_BYTES = F_BYTES + X_BYTES;
+  static constexpr uint32_t TMEM_COLS = 2 * QT;
+  static constexpr uint32_t BAR_BYTES = 768;  // barriers, flags, queue of pieces
+  static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + 8 * EPI_BYTES + BAR_BYTES +
+                                   4 * (3 * GEMM_MAX_EXPERTS + 1);
+  static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
+};
+
+// ---------------------------------------------------------------- PTX this kernel adds
+template <int CG>
+__device__ __forceinline__ void load_2d(uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                        uint32_t bar) {
+  if constexpr (CG == 2)
+    tma_load_2d_pair(dst, tmap, x, y, bar);
+  else
+    tma_load_2d(dst, tmap, x, y, bar);
 }
-// after the barriers: first and end row of each expert, tile prefix
-constexpr uint32_t smem_total() { return grouped_smem() + 4 * (3 * GEMM_MAX_EXPERTS + 1); }
 
 // x, y, z: coordinates from the innermost dimension.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int32_t x, int32_t y,
-                                            int32_t z, uint32_t bar) {
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                        int32_t z, uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t f, uint64_t x, uint32_t idesc,
+                                    uint32_t accumulate) {
+  if constexpr (CG == 2)
+    mma_f16_ss_pair(d, f, x, idesc, accumulate);
+  else
+    mma_f16_ss(d, f, x, idesc, accumulate);
+}
+
+// Arrive on `bar` (of both CTAs of a pair) when the MMAs so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 2)
+    mma_commit_pair_both(bar);
+  else
+    mma_commit(bar);
+}
+
+// bounded_wait for a barrier that another CTA arrives on after writing its own
+// shared memory: acquires at cluster scope.
+__device__ __forceinline__ bool bounded_wait_cluster(uint32_t bar, uint32_t parity,
+                                                     volatile int* abort, uint32_t* status,
+                                                     uint64_t timeout_ns) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t n = 1;; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((n & 31u) == 0u) {
+      if (*abort) return false;
+      if (global_timer_ns() - t0 > timeout_ns) {
+        *abort = 1;
+        atomicOr(status, STATUS_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// 16 lanes x 32 columns as 16 x 8 fragments: of columns 8 i .. 8 i + 7, thread
+// t receives lane t / 4, columns 2 (t % 4) and + 1 in r[4 i], r[4 i + 1], and
+// lane t / 4 + 8 in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 
-struct Tile {
-  int e;
-  int f0;         // first feature
-  int q0, nq;     // first D row (rows: of all rows; grad: of the expert's K) and how many
-  int k0, klen;   // the sum's range (rows: 0, K; grad: the expert's rows)
-};
+// Four 8 x 8 16-bit matrices, each stored transposed: lane 8 m + i gives the
+// address of the 16-byte row that takes column i of matrix m.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                  uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 
+// ---------------------------------------------------------------- schedule
 // Row tiles of an expert with m D rows, and their common width.
-__device__ __forceinline__ int row_tiles(int m) { return (m + QT - 1) / QT; }
+template <int QT>
+__device__ __forceinline__ int row_tiles(int m) {
+  return (m + QT - 1) / QT;
+}
 __device__ __forceinline__ int tile_width(int m, int tiles) {
   return ((m + tiles - 1) / tiles + 31) & ~31;
 }
 
-__device__ __forceinline__ Tile find_tile(const GroupedParams& p, const int* lo, const int* prefix,
-                                          int t) {
-  int a = 0, b = p.E;  // prefix[a] <= t < prefix[b]
-  while (b - a > 1) {
-    const int m = (a + b) >> 1;
-    if (prefix[m] <= t)
-      a = m;
-    else
-      b = m;
+// K slices of a sum over len; an empty one counts as a slice without MMAs, so
+// that its zeros (or C) are stored like any tile.
+__device__ __forceinline__ int slices_of(int len) { return max(1, (len + BK - 1) / BK); }
+
+// A piece of work: a tile of D and the range [k, kend) of its sum.
+struct alignas(16) Piece {
+  int e, f0;         // expert, first feature
+  int q0, nq;        // first D row (rows: of all rows; grad: of the expert's K) and how many
+  int base, k, kend; // the sum's first row (grad) and this piece's range of it
+  int pieces, first; // pieces of the tile and the unit that has its first
+  int slot;          // partial sums: 1 for a tile's first piece, 0 for a later one
+  int more;          // 0: the end of the work
+};
+
+// The work of unit c of `units`.  prefix[e]: rows form, row tiles of the
+// experts before e; grad, K slices of one tile of each of them.
+template <int CG, int QT>
+struct Schedule {
+  const GroupedParams& p;
+  const int* lo;      // [E] first row, [E] end row
+  const int* prefix;  // [E + 1]
+  int c, units;
+  int ft, tiles_e, kb;      // feature tiles; grad: tiles of an expert; rows: slices of a tile
+  int tiles, whole;         // all tiles; how many are dealt whole, round-robin
+  int runs;
+  int64_t s0, len;          // slices before the runs, and in them
+  int i;                    // whole tiles taken
+  int64_t at, end;          // this unit's run
+
+  __device__ __forceinline__ Schedule(const GroupedParams& p_, const int* lo_, const int* prefix_,
+                                      int c_, int units_)
+      : p(p_), lo(lo_), prefix(prefix_), c(c_), units(units_) {
+    ft = (p.N + FT * CG - 1) / (FT * CG);
+    tiles_e = row_tiles<QT>(p.K) * ft;
+    kb = slices_of(p.K);
+    tiles = p.grad ? p.E * tiles_e : prefix[p.E] * ft;
+    const int waves = tiles / units;
+    const bool split = tiles % units != 0 && waves < p.split_waves;
+    whole = !split ? tiles : (waves > 1 ? waves - 1 : 0) * units;
+    s0 = p.grad ? slices_before(whole) : static_cast<int64_t>(whole) * kb;
+    const int64_t all = p.grad ? static_cast<int64_t>(prefix[p.E]) * tiles_e
+                               : static_cast<int64_t>(tiles) * kb;
+    len = all - s0;
+    const int64_t most = min(static_cast<int64_t>(units), len / MIN_RUN);
+    runs = static_cast<int>(max(static_cast<int64_t>(min(tiles - whole, units)), most));
+    i = 0;
+    at = c < runs ? len * c / runs : 0;
+    end = c < runs ? len * (c + 1) / runs : 0;
   }
-  const int i = t - prefix[a];
-  const int ft = (p.N + FT - 1) / FT;
-  const int rows = lo[a + p.E] - lo[a];
-  const int m = p.grad ? p.K : rows;
-  const int rt = row_tiles(m), w = tile_width(m, rt);
-  int64_t ri, fi;
-  raster_tile(i, rt, ft, RASTER, ri, fi);
-  Tile x;
-  x.e = a;
-  x.f0 = static_cast<int>(fi) * FT;
-  const int q = static_cast<int>(ri) * w;
-  x.nq = min(w, m - q);
-  x.q0 = p.grad ? q : lo[a] + q;
-  x.k0 = p.grad ? lo[a] : 0;
-  x.klen = p.grad ? rows : p.K;
-  return x;
-}
 
-__device__ __forceinline__ float load_c(const GroupedParams& p, long long i) {
-  if (p.d_type == T_F32) return static_cast<const float*>(p.C)[i];
-  if (p.d_type == T_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[i]);
-  return __half2float(static_cast<const __half*>(p.C)[i]);
+  // grad: slices of all tiles before tile t
+  __device__ __forceinline__ int64_t slices_before(int t) const {
+    const int e = t / tiles_e;
+    if (e >= p.E) return static_cast<int64_t>(prefix[p.E]) * tiles_e;
+    return static_cast<int64_t>(prefix[e]) * tiles_e +
+           static_cast<int64_t>(t - e * tiles_e) * (prefix[e + 1] - prefix[e]);
+  }
+
+  // The e with prefix[e] * scale <= v < prefix[e + 1] * scale.
+  __device__ __forceinline__ int find(int64_t v, int scale) const {
+    int a = 0, b = p.E;
+    while (b - a > 1) {
+      const int m = (a + b) >> 1;
+      if (static_cast<int64_t>(prefix[m]) * scale <= v)
+        a = m;
+      else
+        b = m;
+    }
+    return a;
+  }
+
+  __device__ __forceinline__ void place(Piece& x, int e, int tile_in_e) const {
+    const int rows = lo[e + p.E] - lo[e];
+    const int m = p.grad ? p.K : rows;
+    const int rt = row_tiles<QT>(m), w = tile_width(m, rt);
+    int64_t ri, fi;
+    raster_tile(tile_in_e, rt, ft, RASTER, ri, fi);
+    const int q = static_cast<int>(ri) * w;
+    x.e = e;
+    x.f0 = static_cast<int>(fi) * FT * CG;
+    x.nq = min(w, m - q);
+    x.q0 = p.grad ? q : lo[e] + q;
+    x.base = p.grad ? lo[e] : 0;
+    x.kend = p.grad ? rows : p.K;
+  }
+
+  __device__ __forceinline__ bool next(Piece& x) {
+    const int64_t t = c + static_cast<int64_t>(i) * units;
+    if (t < whole) {
+      ++i;
+      const int e = p.grad ? static_cast<int>(t) / tiles_e : find(t, ft);
+      place(x, e, static_cast<int>(t) - (p.grad ? e * tiles_e : prefix[e] * ft));
+      x.k = 0;
+      x.pieces = 1;
+      x.first = c;
+      x.slot = 0;
+      return true;
+    }
+    if (at >= end) return false;
+    const int64_t s = s0 + at;
+    int64_t tile_s;  // the tile's first slice
+    int n;           // its slices
+    if (p.grad) {
+      const int e = find(s, tiles_e);
+      n = prefix[e + 1] - prefix[e];
+      const int64_t before = static_cast<int64_t>(prefix[e]) * tiles_e;
+      const int j = static_cast<int>((s - before) / n);
+      tile_s = before + static_cast<int64_t>(j) * n;
+      place(x, e, j);
+    } else {
+      n = kb;
+      const int64_t tile = s / kb;
+      tile_s = tile * kb;
+      const int e = find(tile, ft);
+      place(x, e, static_cast<int>(tile) - prefix[e] * ft);
+    }
+    const int64_t stop = min(end, tile_s - s0 + n);
+    x.k = static_cast<int>(s - tile_s) * BK;
+    x.kend = min(x.kend, static_cast<int>(stop + s0 - tile_s) * BK);
+    const int64_t r0 = tile_s - s0, r1 = r0 + n - 1;
+    x.first = static_cast<int>(((r0 + 1) * runs - 1) / len);
+    x.pieces = static_cast<int>(((r1 + 1) * runs - 1) / len) - x.first + 1;
+    x.slot = c == x.first ? 1 : 0;
+    at = stop;
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- element types
+template <int DT>
+__device__ __forceinline__ float load_c(const void* c, long long i) {
+  if constexpr (DT == T_F32) return static_cast<const float*>(c)[i];
+  if constexpr (DT == T_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(c)[i]);
+  return __half2float(static_cast<const __half*>(c)[i]);
 }
-__device__ __forceinline__ void store_d(const GroupedParams& p, long long i, float v) {
-  if (p.d_type == T_F32)
-    static_cast<float*>(p.D)[i] = v;
-  else if (p.d_type == T_BF16)
-    static_cast<__nv_bfloat16*>(p.D)[i] = __float2bfloat16_rn(v);
+template <int DT>
+__device__ __forceinline__ void store_d(void* d, long long i, float v) {
+  if constexpr (DT == T_F32)
+    static_cast<float*>(d)[i] = v;
+  else if constexpr (DT == T_BF16)
+    static_cast<__nv_bfloat16*>(d)[i] = __float2bfloat16_rn(v);
   else
-    static_cast<__half*>(p.D)[i] = __float2half_rn(v);
+    static_cast<__half*>(d)[i] = __float2half_rn(v);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) {
+  if constexpr (DT == T_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(__uint_as_float(lo), __uint_as_float(hi));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
 }
 
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+// ---------------------------------------------------------------- kernel
+template <int CG, int QT, int STAGES, int DT>
+__global__ void __launch_bounds__(GROUPED_THREADS, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmX128,
                    const __grid_constant__ CUtensorMap tmX32, const GroupedParams p) {
+  using C = Cfg<CG, QT, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sF = smem;
   uint8_t* const sX = smem + STAGES * F_BYTES;
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(sX + STAGES * X_BYTES);
-  constexpr int NBARS = 2 * STAGES + 5;
+  uint8_t* const sE = sX + STAGES * C::X_BYTES;  // epilogue: two buffers a warp
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(sE + 8 * EPI_BYTES);
+  constexpr int NBARS = 4 * STAGES + 5 + 2 * QUEUE;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* const ep_go = abort_flag + 1;
-  int* const lo = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [2E]: first, end
-  int* const prefix = lo + 2 * p.E;  // [E + 1]
+  volatile int* const ep_last = abort_flag + 2;
+  Piece* const queue = reinterpret_cast<Piece*>(reinterpret_cast<uint8_t*>(bars) + 512);
+  static_assert(8 * NBARS + 16 <= 512 && 512 + QUEUE * sizeof(Piece) <= C::BAR_BYTES, "layout");
+  int* const lo = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + C::BAR_BYTES);
+  int* const prefix = lo + 2 * p.E;
 
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](uint32_t s) { return bar0 + 8u * s; };
@@ -134,39 +359,68 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto acc_full = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
   auto acc_empty = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
   const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
+  // grad, per ring place: a slice that ends inside 16 rows has landed in this
+  // CTA; both CTAs' rows past the group are cleared (on the even CTA).  One
+  // each per place: with groups of a slice or less the clearing runs up to a
+  // ring ahead of the MMA.
+  auto tail_full = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
+  auto tail_clear = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + 5 + s); };
+  auto q_full = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + i); };
+  auto q_empty = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + QUEUE + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
+      mbar_init(tail_full(s), 1);
+      mbar_init(tail_clear(s), CG);
+    }
+    for (int i = 0; i < QUEUE; ++i) {
+      mbar_init(q_full(i), 1);
+      mbar_init(q_empty(i), p.grad ? 7 : 6);  // one arrival per warp that reads a piece
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 4);
+      mbar_init(acc_empty(b), 4 * CG);
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmF);
+    tma_prefetch_desc(&tmX128);
+    if (!p.grad) tma_prefetch_desc(&tmX32);
+  }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_holder), 512);
-    tmem_relinquish();
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(smem_u32(tmem_holder), C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   pdl_wait();
   pdl_trigger();
-  const int ft = (p.N + FT - 1) / FT;
-  for (int e = threadIdx.x; e < p.E; e += NUM_THREADS) {
+  for (int e = threadIdx.x; e < p.E; e += GROUPED_THREADS) {
     const int2 r = expert_rows(p.offsets, e, p.R, p.status);
     lo[e] = r.x;
     lo[e + p.E] = r.y;
   }
   __syncthreads();
-  if (warp == 2) {  // the tile prefix: each lane a run of experts, then a warp scan
+  if (warp == 2) {  // the prefix: each lane a run of experts, then a warp scan
+    auto count = [&](int e) {
+      const int rows = lo[e + p.E] - lo[e];
+      return p.grad ? slices_of(rows) : row_tiles<QT>(rows);
+    };
     const int len = (p.E + 31) / 32, b = min(p.E, lane * len), e1 = min(p.E, b + len);
     int sum = 0;
-    for (int e = b; e < e1; ++e) sum += row_tiles(p.grad ? p.K : lo[e + p.E] - lo[e]) * ft;
+    for (int e = b; e < e1; ++e) sum += count(e);
     int inc = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -176,55 +430,112 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int at = inc - sum;
     for (int e = b; e < e1; ++e) {
       prefix[e] = at;
-      at += row_tiles(p.grad ? p.K : lo[e + p.E] - lo[e]) * ft;
+      at += count(e);
     }
     if (lane == 31) prefix[p.E] = inc;
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();  // both CTAs' barriers exist
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int tiles = prefix[p.E];
   const uint64_t tmo = p.timeout_ns;
-  const int grid = gridDim.x;
+  // The next piece of this CTA's work; false at its end or after a timeout.
+  uint32_t q_at = 0, q_ph = 0;
+  auto next_piece = [&](Piece& x) {
+    bool ok = true;
+    if (lane == 0)
+      ok = bounded_wait(q_full(q_at), q_ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    if (!ok) return false;
+    __syncwarp();
+    x = queue[q_at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_empty(q_at));
+    if (++q_at == QUEUE) {
+      q_at = 0;
+      q_ph ^= 1u;
+    }
+    return x.more != 0;
+  };
+  // The piece's last slice ends inside 16 rows of another expert's.
+  auto is_ragged = [&](const Piece& x) { return p.grad && (x.kend - x.k) % 16 != 0; };
+  Piece x;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+  if (warp == 6) {
+    // ------------------------------------------------------------ schedule (each CTA)
+    // A piece costs a few hundred instructions (bisection, divisions); taken
+    // by the MMA warp itself they held the tensor pipe up at every tile.
+    Schedule<CG, QT> work(p, lo, prefix, blockIdx.x / CG, gridDim.x / CG);
     if (lane == 0) {
-      uint32_t it = 0, s = 0, ph = 0;
-      bool stop = false, skipped = false;
-      for (int t = blockIdx.x; t < tiles && !stop; t += grid) {
-        const Tile x = find_tile(p, lo, prefix, t);
-        for (int k = 0; k < x.klen; k += BK) {
+      for (bool more = true; more;) {
+        more = work.next(x);
+        x.more = more;
+        if (!bounded_wait(q_empty(q_at), q_ph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo)) break;
+        queue[q_at] = x;
+        mbar_arrive(q_full(q_at));
+        if (++q_at == QUEUE) {
+          q_at = 0;
+          q_ph ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (each CTA)
+    uint32_t it = 0, s = 0, ph = 0;
+    uint32_t tail_used = 0, tail_ph = 0;  // bit s: used; parity of the next use
+    bool stop = false, skipped = false;
+    while (next_piece(x)) {
+      if (lane == 0 && !stop) {
+        const int half = ((x.nq + 31) & ~31) / CG;  // this CTA's rows of the tile
+        const int q0 = x.q0 + static_cast<int>(rank) * half, f0 = x.f0 + static_cast<int>(rank) * FT;
+        const bool big = half > 64;
+        const int boxes = p.grad ? (half + 63) / 64 : (big ? (half + 127) / 128 : (half + 31) / 32);
+        const uint32_t bytes = F_BYTES + boxes * (p.grad ? 8192u : (big ? 16384u : 4096u));
+        for (int k = x.k; k < x.kend; k += BK) {
           if (!bounded_wait(empty(s), ph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo)) {
             stop = true;
             break;
           }
-          const uint32_t fd = smem_u32(sF + s * F_BYTES), xd = smem_u32(sX + s * X_BYTES);
-          if ((p.debug_flags & DBG_SKIP_FIRST_FILL) && it == 0) {
+          const uint32_t fd = smem_u32(sF + s * F_BYTES), xd = smem_u32(sX + s * C::X_BYTES);
+          // both CTAs' copies are counted by the even CTA, but for a slice
+          // whose rows past the group are to be cleared before the MMA
+          const bool tail = k + BK > x.kend && is_ragged(x);
+          uint32_t fb = full(s);
+          if (tail)
+            fb = tail_full(s);
+          else if constexpr (CG == 2)
+            fb = map_shared_rank(full(s), 0);
+          if ((p.debug_flags & DBG_SKIP_FIRST_FILL) && it == 0 && leader) {
             skipped = true;  // test hook: the MMA's wait on the first stage expires
-          } else if (p.grad) {
-            const int xb = (x.nq + 63) / 64;
-            mbar_arrive_expect_tx(full(s), F_BYTES + xb * 8192u);
-            for (int i = 0; i < FT / 64; ++i)
-              tma_load_2d(fd + i * 8192u, &tmF, x.f0 + 64 * i, x.k0 + k, full(s));
-            for (int i = 0; i < xb; ++i)
-              tma_load_2d(xd + i * 8192u, &tmX128, x.q0 + 64 * i, x.k0 + k, full(s));
           } else {
-            const bool wide = x.nq > 64;
-            const int xb = wide ? (x.nq + 127) / 128 : (x.nq + 31) / 32;
-            mbar_arrive_expect_tx(full(s), F_BYTES + xb * (wide ? 16384u : 4096u));
-            if (p.f_mn) {
-              for (int i = 0; i < FT / 64; ++i)
-                tma_load_3d(fd + i * 8192u, &tmF, x.f0 + 64 * i, k, x.e, full(s));
-            } else {
-              tma_load_2d(fd, &tmF, k, x.e * p.N + x.f0, full(s));
+            if (tail) {
+              mbar_arrive_expect_tx(tail_full(s), bytes);
+              tail_used |= 1u << s;
+              tail_ph ^= 1u << s;
+              if (leader) mbar_arrive(full(s));  // this use of the place, in step
+            } else if (leader) {
+              mbar_arrive_expect_tx(full(s), CG * bytes);
             }
-            for (int i = 0; i < xb; ++i) {
-              if (wide)
-                tma_load_2d(xd + i * 16384u, &tmX128, k, x.q0 + 128 * i, full(s));
-              else
-                tma_load_2d(xd + i * 4096u, &tmX32, k, x.q0 + 32 * i, full(s));
+            if (p.grad) {
+              for (int i = 0; i < FT / 64; ++i)
+                load_2d<CG>(fd + i * 8192u, &tmF, f0 + 64 * i, x.base + k, fb);
+              for (int i = 0; i < boxes; ++i)
+                load_2d<CG>(xd + i * 8192u, &tmX128, q0 + 64 * i, x.base + k, fb);
+            } else {
+              if (p.f_mn) {
+                for (int i = 0; i < FT / 64; ++i)
+                  load_3d<CG>(fd + i * 8192u, &tmF, f0 + 64 * i, k, x.e, fb);
+              } else {
+                load_2d<CG>(fd, &tmF, k, x.e * p.N + f0, fb);
+              }
+              for (int i = 0; i < boxes; ++i) {
+                if (big)
+                  load_2d<CG>(xd + i * 16384u, &tmX128, k, q0 + 128 * i, fb);
+                else
+                  load_2d<CG>(xd + i * 4096u, &tmX32, k, q0 + 32 * i, fb);
+              }
             }
           }
           ++it;
@@ -234,90 +545,137 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
-      // copies in flight land before the CTA leaves
-      for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j) {
-        if (skipped && j == 0) continue;
-        drain_wait(full(j % STAGES), (j / STAGES) & 1u, 200000000ull);
+      __syncwarp();
+    }
+    if (lane == 0) {
+      // Copies in flight land before the CTA leaves.  The even CTA's barriers
+      // count both CTAs' (after giving up, the odd CTA gives its own time).
+      for (uint32_t j = 0; j < STAGES; ++j)
+        if ((tail_used >> j) & 1u)
+          drain_wait(tail_full(j), ((tail_ph >> j) & 1u) ^ 1u, 200000000ull);
+      if (leader) {
+        for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j) {
+          if (skipped && j == 0) continue;
+          drain_wait(full(j % STAGES), (j / STAGES) & 1u, 200000000ull);
+        }
+      } else if (*abort_flag) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // All lanes walk the loop (they clear rows past a group together); lane 0
-    // waits and issues.
-    const bool x_mn = p.grad != 0;
+    // ------------------------------------------------------------ MMA issuer (even CTA)
     const uint32_t f_lo0 = sdesc_lo(smem_u32(sF), p.f_mn ? 8192u : 16u);
-    const uint32_t x_lo0 = sdesc_lo(smem_u32(sX), x_mn ? 8192u : 16u);
+    const uint32_t x_lo0 = sdesc_lo(smem_u32(sX), p.grad ? 8192u : 16u);
     const uint32_t dhi = sdesc_hi_sw128(1024u);
-    const uint32_t f_step = p.f_mn ? 128u : 2u, x_step = x_mn ? 128u : 2u;
+    const uint32_t f_step = p.f_mn ? 128u : 2u, x_step = p.grad ? 128u : 2u;
     uint32_t s = 0, ph = 0, acc_it = 0;
+    uint32_t tail_ph = 0;  // bit s: parity of the next ragged slice in place s
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += grid) {
-      const Tile x = find_tile(p, lo, prefix, t);
-      if (x.klen == 0) continue;
-      const uint32_t buf = acc_it & 1u;
-      const uint32_t d_tmem = tmem_base + buf * QT;
-      const uint32_t idesc = p.idesc | (static_cast<uint32_t>(((x.nq + 31) & ~31) >> 3) << 17);
-      if (lane == 0)
+    while (next_piece(x)) {
+      if (leader && lane == 0 && ok && x.k < x.kend) {
+        const uint32_t buf = acc_it & 1u;
+        const uint32_t d_tmem = tmem_base + buf * QT;
+        const uint32_t idesc = p.idesc | (static_cast<uint32_t>(((x.nq + 31) & ~31) >> 3) << 17);
         ok = bounded_wait(acc_empty(buf), ((acc_it >> 1) & 1u) ^ 1u, abort_flag, p.status,
                           STATUS_TIMEOUT, tmo);
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      if (!ok) break;
-      tc_fence_after();
-      for (int k = 0; k < x.klen; k += BK) {
-        if (lane == 0)
+        tc_fence_after();
+        const int nfull = (x.kend - x.k) / BK;
+        uint32_t accumulate = 0;
+        for (int i = 0; ok && i < nfull; ++i) {
           ok = bounded_wait(full(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        if (!ok) break;
-        const int left = min(BK, x.klen - k);
-        const int chunks = (left + 15) / 16;
-        if (p.grad && left < 16 * chunks) {
-          // rows [left, 16 chunks) of the slice belong to another expert (or
-          // to nobody): zero them in every 64-wide box of both operands
-          const int n16 = (16 * chunks - left) * 8;  // 16-byte units per box
-          const int boxes = FT / 64 + (x.nq + 63) / 64;
-          for (int i = lane; i < n16 * boxes; i += 32) {
-            const int b = i / n16, u = i - b * n16;
-            uint8_t* const base = b < FT / 64 ? sF + s * F_BYTES + b * 8192
-                                              : sX + s * X_BYTES + (b - FT / 64) * 8192;
-            *reinterpret_cast<uint4*>(base + left * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+          if (!ok) break;
+          const uint32_t f_lo = f_lo0 + s * (F_BYTES >> 4), x_lo = x_lo0 + s * (C::X_BYTES >> 4);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            mma<CG>(d_tmem, sdesc(dhi, f_lo + c * f_step), sdesc(dhi, x_lo + c * x_step), idesc,
+                    accumulate | c);
+          accumulate = 1;
+          commit<CG>(empty(s));
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
           }
-          fence_proxy_async_smem();
-          __syncwarp();
         }
-        if (lane == 0) {
-          const uint32_t f_lo = f_lo0 + s * (F_BYTES >> 4), x_lo = x_lo0 + s * (X_BYTES >> 4);
-          for (int c = 0; c < chunks; ++c)
-            mma_f16_ss(d_tmem, sdesc(dhi, f_lo + c * f_step), sdesc(dhi, x_lo + c * x_step), idesc,
-                       (k | c) != 0);
-          mma_commit(empty(s));
+        const int left = x.kend - x.k - nfull * BK;  // a last slice that is not whole
+        if (ok && left > 0) {
+          ok = bounded_wait(full(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
+          if (ok && is_ragged(x)) {
+            ok = bounded_wait_cluster(tail_clear(s), (tail_ph >> s) & 1u, abort_flag, p.status, tmo);
+            tail_ph ^= 1u << s;
+          }
+          if (ok) {
+            const uint32_t f_lo = f_lo0 + s * (F_BYTES >> 4), x_lo = x_lo0 + s * (C::X_BYTES >> 4);
+            for (int c = 0; c < (left + 15) / 16; ++c)
+              mma<CG>(d_tmem, sdesc(dhi, f_lo + c * f_step), sdesc(dhi, x_lo + c * x_step), idesc,
+                      accumulate | c);
+            commit<CG>(empty(s));
+          }
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
-        __syncwarp();
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1u;
-        }
+        if (ok) commit<CG>(acc_full(buf));
+        ++acc_it;
       }
-      if (!ok) break;
-      if (lane == 0) mma_commit(acc_full(buf));
-      ++acc_it;
+      __syncwarp();
     }
-    if (lane == 0) {
-      mma_commit(done_bar);
+    if (leader && lane == 0) {
+      commit<CG>(done_bar);
       drain_wait(done_bar, 0, 200000000ull);
     }
     __syncwarp();
+  } else if (warp == 7) {
+    // ------------------------------------------------------------ rows past a group (each CTA)
+    // Zeros over the rows [left, 16 chunks) of a ragged slice, which belong to
+    // another expert (or to nobody), in every 64-wide box of both operands.
+    uint32_t s = 0, tail_ph = 0;
+    bool ok = p.grad != 0;
+    while (ok && next_piece(x)) {
+      const int n = x.kend - x.k;
+      if (n > 0 && is_ragged(x)) {
+        const uint32_t at = (s + n / BK) % STAGES;  // the place of the piece's last slice
+        const int left = n % BK;
+        if (lane == 0)
+          ok = bounded_wait(tail_full(at), (tail_ph >> at) & 1u, abort_flag, p.status,
+                            STATUS_TIMEOUT, tmo);
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (!ok) break;
+        tail_ph ^= 1u << at;
+        const int n16 = ((left + 15) / 16 * 16 - left) * 8;  // 16-byte units per box
+        const int boxes = FT / 64 + (((x.nq + 31) & ~31) / CG + 63) / 64;
+        for (int i = lane; i < n16 * boxes; i += 32) {
+          const int b = i / n16, u = i - b * n16;
+          uint8_t* const base = b < FT / 64 ? sF + at * F_BYTES + b * 8192
+                                            : sX + at * C::X_BYTES + (b - FT / 64) * 8192;
+          *reinterpret_cast<uint4*>(base + left * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            mbar_arrive_cluster(map_shared_rank(tail_clear(at), 0));
+          else
+            mbar_arrive(tail_clear(at));
+        }
+      }
+      s = (s + static_cast<uint32_t>((max(n, 0) + BK - 1) / BK)) % STAGES;
+    }
   } else {
-    // ------------------------------------------------------------ epilogue
+    // ------------------------------------------------------------ epilogue (each CTA)
     const int q = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    const bool leader = threadIdx.x == 64;
-    uint32_t acc_it = 0;
-    for (int t = blockIdx.x; t < tiles; t += grid) {
-      const Tile x = find_tile(p, lo, prefix, t);
+    const bool ep_leader = threadIdx.x == 64;
+    uint8_t* const stage = sE + q * 2 * EPI_BYTES;
+    uint32_t acc_it = 0, staged = 0;
+    const int unit = blockIdx.x / CG;
+    while (next_piece(x)) {
       const uint32_t buf = acc_it & 1u;
-      if (x.klen != 0) {
-        if (leader)
+      const bool sum = x.k < x.kend;
+      if (sum) {
+        if (ep_leader)
           *ep_go = bounded_wait(acc_full(buf), (acc_it >> 1) & 1u, abort_flag, p.status,
                                 STATUS_TIMEOUT, tmo) ? 1 : 0;
         named_barrier_sync(1, 128);
@@ -326,55 +684,255 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!go) break;
         tc_fence_after();
       }
-      const int f = x.f0 + q * 32 + lane;
-      const long long row0 = p.grad ? static_cast<long long>(x.e) * p.K + x.q0 : x.q0;
-#pragma unroll 1
-      for (int c = 0; c < x.nq; c += 32) {
-        uint32_t v[32];
-        if (x.klen != 0) {
-          tmem_ld_32x32b_x32(tmem_base + lane_base + buf * QT + c, v);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0u;
-        }
-        if (f < p.N) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (c + j >= x.nq) break;
-            float d = __uint_as_float(v[j]);
-            if (p.C) d += load_c(p, (row0 + c + j) * p.ldc + f);
-            store_d(p, (row0 + c + j) * p.ldd + f, d);
-          }
-        }
-        __syncwarp();
-      }
-      if (x.klen != 0) {
+      auto release = [&] {  // the accumulator has been read
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty(buf));
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            mbar_arrive_cluster(map_shared_rank(acc_empty(buf), 0));
+          else
+            mbar_arrive(acc_empty(buf));
+        }
+      };
+      const int f32 = x.f0 + static_cast<int>(rank) * FT + q * 32;  // this warp's features
+      const int f = f32 + lane;
+      const long long row0 = p.grad ? static_cast<long long>(x.e) * p.K + x.q0 : x.q0;
+      const uint32_t taddr = tmem_base + lane_base + buf * QT;
+      if (sum && x.pieces == 1 && p.d_vec && !p.C) {
+        // 16-bit D, 16-byte rows: the fragments of 32 rows x 32 features are
+        // transposed into rows by stmatrix (16-byte units, unit u of row r at
+        // u ^ (r / 2) % 4 against bank conflicts) and leave as 16-byte stores
+        if constexpr (DT != T_F32) {
+#pragma unroll 1
+          for (int c = 0; c < x.nq; c += 32) {
+            uint32_t r[32];
+            tmem_ld_16x256b_x4(taddr + c, r);
+            tmem_ld_16x256b_x4(taddr + c + (16u << 16), r + 16);
+            tmem_ld_wait();
+            if (c + 32 >= x.nq) release();
+            uint8_t* const out = stage + (staged++ & 1u) * EPI_BYTES;
+            const int m = lane >> 3;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                const uint32_t* const v = r + 16 * h + 4 * i;
+                const int row = 8 * (i + (m >> 1)) + (lane & 7);
+                const int u = (2 * h + (m & 1)) ^ ((row >> 1) & 3);
+                stmatrix_x4_trans(smem_u32(out + row * 64 + u * 16), pack2<DT>(v[0], v[1]),
+                                  pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
+                                  pack2<DT>(v[6], v[7]));
+              }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 8 * i + (lane >> 2), u = lane & 3;
+              const uint4 v =
+                  *reinterpret_cast<const uint4*>(out + row * 64 + ((u ^ ((row >> 1) & 3)) << 4));
+              const int f8 = f32 + 8 * u;
+              if (c + row < x.nq && f8 < p.N) {
+                uint16_t* const d =
+                    static_cast<uint16_t*>(p.D) + (row0 + c + row) * p.ldd + f8;
+                if (f8 + 8 <= p.N) {
+                  *reinterpret_cast<uint4*>(d) = v;
+                } else {
+                  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                  for (int j = 0; j < p.N - f8; ++j)
+                    d[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+                }
+              }
+            }
+          }
+        }
         ++acc_it;
+        continue;
       }
+      // Everything else: lane = feature, one D row at a time.  Partial sums of
+      // a shared tile: float4 of four D rows of a feature, features adjacent.
+      auto partial = [&](int piece_unit, int slot) {
+        return reinterpret_cast<float4*>(
+                   p.partial + (static_cast<size_t>(2 * piece_unit + slot) * CG + rank) * (QT * FT)) +
+               q * 32 + lane;
+      };
+      if (x.pieces > 1) {
+        // leave the sums, see who is last
+        float4* const mine = partial(unit, x.slot);
+#pragma unroll 1
+        for (int c = 0; c < x.nq; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(taddr + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            mine[(c / 4 + j) * FT] =
+                make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                            __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+        }
+        __threadfence();
+        named_barrier_sync(1, 128);
+        if (ep_leader) {
+          unsigned* const count = p.counters + x.first * CG + rank;
+          const bool last = atomicAdd(count, 1u) == static_cast<unsigned>(x.pieces) - 1u;
+          if (last) *count = 0u;  // ready for the next call
+          __threadfence();
+          *ep_last = last ? 1 : 0;
+        }
+        named_barrier_sync(1, 128);
+        const bool last = *ep_last != 0;
+        named_barrier_sync(1, 128);
+        if (!last) {
+          release();
+          ++acc_it;
+          continue;
+        }
+        __threadfence();
+      }
+#pragma unroll 1
+      for (int c = 0; c < x.nq; c += 32) {
+        float v[32];
+        if (sum) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(taddr + c, r);
+          tmem_ld_wait();
+          if (c + 32 >= x.nq) release();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        }
+        if (x.pieces > 1) {
+          // in K order, this unit's own sums among them: the same bits
+          // whoever is last
+          float t[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) t[j] = 0.f;
+#pragma unroll 1
+          for (int i = 0; i < x.pieces; ++i) {
+            if (x.first + i == unit) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) t[j] += v[j];
+              continue;
+            }
+            const float4* const src = partial(x.first + i, i == 0 ? 1 : 0) + c / 4 * FT;
+            float4 w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __ldcg(src + j * FT);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              t[4 * j] += w[j].x;
+              t[4 * j + 1] += w[j].y;
+              t[4 * j + 2] += w[j].z;
+              t[4 * j + 3] += w[j].w;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = t[j];
+        }
+        if (f < p.N) {
+          if (p.C) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < x.nq) v[j] += load_c<DT>(p.C, (row0 + c + j) * p.ldc + f);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c + j < x.nq) store_d<DT>(p.D, (row0 + c + j) * p.ldd + f, v[j]);
+        }
+        __syncwarp();
+      }
+      if (sum) ++acc_it;
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2)
+    cluster_sync_all();
+  else
+    __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    if constexpr (CG == 2)
+      tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
+}
+
+// ---------------------------------------------------------------- launches
+constexpr int WIDE_QT = 256, WIDE_STAGES = 6;
+constexpr int NARROW_QT = 64, NARROW_STAGES = 8;
+
+template <int CG, int QT, int STAGES, int DT>
+cudaLaunchConfig_t config(int units, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * CG));
+  cfg.blockDim = dim3(GROUPED_THREADS);
+  cfg.dynamicSmemBytes = Cfg<CG, QT, STAGES>::SMEM;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cfg;
+}
+
+// Sets the kernel's shared memory limit; how many units run at once.
+template <int CG, int QT, int STAGES, int DT>
+int prepare(int num_sms) {
+  auto* kernel = grouped_kernel<CG, QT, STAGES, DT>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Cfg<CG, QT, STAGES>::SMEM) != cudaSuccess)
+    return 0;
+  if (CG == 1) return num_sms;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = config<CG, QT, STAGES, DT>(1, nullptr, attr);
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+
+template <int CG, int QT, int STAGES, int DT>
+cudaError_t launch(const CUtensorMap& f, const CUtensorMap& x128, const CUtensorMap& x32,
+                   const GroupedParams& p, int units, cudaStream_t st) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = config<CG, QT, STAGES, DT>(units, st, attr);
+  return cudaLaunchKernelEx(&cfg, grouped_kernel<CG, QT, STAGES, DT>, f, x128, x32, p);
+}
+
+template <int DT>
+int prepare_typed(bool wide, int num_sms) {
+  return wide ? prepare<2, WIDE_QT, WIDE_STAGES, DT>(num_sms)
+              : prepare<1, NARROW_QT, NARROW_STAGES, DT>(num_sms);
+}
+template <int DT>
+cudaError_t launch_typed(bool wide, const CUtensorMap& f, const CUtensorMap& x128,
+                         const CUtensorMap& x32, const GroupedParams& p, int units,
+                         cudaStream_t st) {
+  return wide ? launch<2, WIDE_QT, WIDE_STAGES, DT>(f, x128, x32, p, units, st)
+              : launch<1, NARROW_QT, NARROW_STAGES, DT>(f, x128, x32, p, units, st);
 }
 
 }  // namespace
 
-cudaError_t prepare_grouped() {
-  return cudaFuncSetAttribute(grouped_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smem_total());
+int prepare_grouped(bool wide, int d_type, int num_sms) {
+  return d_type == T_F32    ? prepare_typed<T_F32>(wide, num_sms)
+         : d_type == T_BF16 ? prepare_typed<T_BF16>(wide, num_sms)
+                            : prepare_typed<T_F16>(wide, num_sms);
 }
 
-cudaError_t launch_grouped(const CUtensorMap& f, const CUtensorMap& x128, const CUtensorMap& x32,
-                           const GroupedParams& p, int grid, cudaStream_t st) {
-  return launch_pdl(grouped_kernel, dim3(grid), dim3(NUM_THREADS), smem_total(), st, f, x128, x32, p);
+size_t grouped_partial_bytes(bool wide, int units) {
+  return sizeof(float) * 2 * units * FT * (wide ? 2 * WIDE_QT : NARROW_QT);
+}
+
+cudaError_t launch_grouped(bool wide, const CUtensorMap& f, const CUtensorMap& x128,
+                           const CUtensorMap& x32, const GroupedParams& p, int units,
+                           cudaStream_t st) {
+  return p.d_type == T_F32    ? launch_typed<T_F32>(wide, f, x128, x32, p, units, st)
+         : p.d_type == T_BF16 ? launch_typed<T_BF16>(wide, f, x128, x32, p, units, st)
+                              : launch_typed<T_F16>(wide, f, x128, x32, p, units, st);
 }
 
 }  // namespace gb300

@@ -75,9 +75,6 @@ cudaError_t launch_combine(const PermuteParams& p, int num_sms, cudaStream_t st)
 cudaError_t launch_combine_backward(const PermuteParams& p, int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- grouped products (grouped.cu)
-// The tensor cores' M dimension is D's columns ("features", contiguous in
-// D), their N dimension D's rows: a row tile takes any multiple of 32 rows
-// up to 256, so that a ragged group costs about its own length.
 struct GroupedParams {
   int grad;            // GEMM_GROUPED_GRAD: the sum runs over an expert's rows
   int E, R, K, N;
@@ -86,17 +83,26 @@ struct GroupedParams {
   const int* offsets;
   const void* C;
   int d_type;          // also C's
+  int d_vec;           // 16-bit D whose rows start on 16-byte boundaries
   long long ldc, ldd;
   void* D;
+  // Fewer full waves than this: the partial last wave is dealt by K slices.
+  int split_waves;
+  float* partial;      // grouped_partial_bytes()
+  unsigned* counters;  // one per CTA, zero between calls
   uint32_t* status;
   unsigned long long timeout_ns;
   int debug_flags;
 };
+// Sets the kernel up on the current device; how many of its units (CTA pairs
+// when wide, else CTAs) run at once, 0 on failure.
+int prepare_grouped(bool wide, int d_type, int num_sms);
+size_t grouped_partial_bytes(bool wide, int units);
 // Tensor maps: the features operand; the rows operand in boxes of 128 rows
-// and of 32 (rows form; both 64 x 64 boxes of the MN-major operand in grad).
-cudaError_t launch_grouped(const CUtensorMap& f, const CUtensorMap& x128, const CUtensorMap& x32,
-                           const GroupedParams& p, int grid, cudaStream_t st);
-cudaError_t prepare_grouped();
+// and of 32 (rows form; in grad x128 has 64 x 64 boxes and x32 is not read).
+cudaError_t launch_grouped(bool wide, const CUtensorMap& f, const CUtensorMap& x128,
+                           const CUtensorMap& x32, const GroupedParams& p, int units,
+                           cudaStream_t st);
 
 // ---------------------------------------------------------------- 4-bit weights (w4.cu)
 struct W4Params {

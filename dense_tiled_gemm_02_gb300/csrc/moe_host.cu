@@ -49,8 +49,10 @@ struct gemm_op {
   bool copy_a = false, copy_b = false;
   int64_t a_rows = 0, a_cols = 0, b_rows = 0, b_cols = 0;
   int64_t ws_lda = 0, ws_ldb = 0;
-  size_t ws_b_off = 0;
-  int grid = 0;
+  size_t ws_b_off = 0, ws_partial_off = 0, ws_counters_off = 0;
+  bool wide = false;
+  int units = 0;
+  int grid = 0;  // route: blocks
 };
 
 namespace {
@@ -370,7 +372,7 @@ int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc) {
   // tile numbers are 32-bit: the most there can be (each expert may add a
   // partial tile to the rows')
   const int64_t ft = (d.N + 127) / 128;
-  const int64_t qt = grad ? d.E * ((d.K + 255) / 256) : d.R / 256 + d.E;
+  const int64_t qt = grad ? d.E * ((d.K + 63) / 64) : d.R / 64 + d.E;
   if (ft > 0 && qt > INT_MAX / ft) return GEMM_ERR_INVALID_ARG;
 
   const bool copy_a = d.lda % 8 != 0 && d.R > 0 && d.K > 0;
@@ -378,14 +380,30 @@ int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc) {
   const int64_t ws_lda = up(d.K, 64), ws_ldb = up(b_cols, 64);
   const size_t a_bytes = copy_a ? static_cast<size_t>(d.R) * ws_lda * 2 : 0;
   const size_t b_bytes = copy_b ? static_cast<size_t>(b_rows) * ws_ldb * 2 : 0;
+  int sms = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    cudaGetLastError();
+  // The wide form needs D rows to fill a tile's columns (more than 64 an
+  // expert, on average) and a wave of tiles.
+  const int64_t m = grad ? d.K : d.R / d.E;
+  const bool wide = m > 64 && d.E * ((m + 255) / 256) * ((d.N + 255) / 256) >= sms / 2;
+  const int most_units = std::max(1, wide ? sms / 2 : sms);
+  const size_t partial = grouped_partial_bytes(wide, most_units);
+  const size_t counters = 4 * static_cast<size_t>(most_units) * (wide ? 2 : 1);
+  const size_t p_off = static_cast<size_t>(up(static_cast<int64_t>(a_bytes + b_bytes), 256));
   gemm_op* op = nullptr;
-  const int rc = make_op(Kind::kGrouped, a_bytes + b_bytes, &op);
+  const int rc = make_op(Kind::kGrouped, p_off + partial + counters, &op);
   if (rc != GEMM_OK) return rc;
-  if (prepare_grouped() != cudaSuccess) {
+  op->units = std::min(most_units, prepare_grouped(wide, d.d_type, op->num_sms));
+  if (op->units <= 0) {
     cudaGetLastError();
     gemm_op_destroy(op);
     return GEMM_ERR_CUDA;
   }
+  op->wide = wide;
+  op->ws_partial_off = p_off;
+  op->ws_counters_off = p_off + partial;
   op->grouped = d;
   op->copy_a = copy_a;
   op->copy_b = copy_b;
@@ -396,11 +414,11 @@ int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc) {
   op->ws_lda = copy_a ? ws_lda : d.lda;
   op->ws_ldb = copy_b ? ws_ldb : d.ldb;
   op->ws_b_off = a_bytes;
-  op->grid = static_cast<int>(std::min<int64_t>(op->num_sms, std::max<int64_t>(qt * ft, 1)));
   char buf[160];
-  std::snprintf(buf, sizeof buf, "grouped form=%s E=%d R=%lld K=%lld N=%lld copy=%d%d grid=%d",
+  std::snprintf(buf, sizeof buf, "grouped form=%s E=%d R=%lld K=%lld N=%lld wide=%d copy=%d%d units=%d",
                 grad ? "grad" : "rows", d.E, static_cast<long long>(d.R),
-                static_cast<long long>(d.K), static_cast<long long>(d.N), copy_a, copy_b, op->grid);
+                static_cast<long long>(d.K), static_cast<long long>(d.N), wide, copy_a, copy_b,
+                op->units);
   op->plan = buf;
   *out = op;
   return GEMM_OK;
@@ -459,18 +477,23 @@ int gemm_grouped_run(gemm_op_t op, const void* A, const void* B, const int32_t* 
   p.K = static_cast<int>(d.K);
   p.N = static_cast<int>(d.N);
   p.f_mn = grad || d.layout_b == GEMM_ROW_MAJOR;
-  p.idesc = idesc_f16(d.ab_type == GEMM_BF16, p.f_mn, grad, 128, 0);
+  p.idesc = idesc_f16(d.ab_type == GEMM_BF16, p.f_mn, grad, op->wide ? 256 : 128, 0);
   p.offsets = offsets;
   p.C = C;
   p.d_type = d.d_type;
+  p.d_vec = is_16bit(d.d_type) && d.ldd % 8 == 0 && aligned(D, 16);
   p.ldc = d.ldc;
   p.ldd = d.ldd;
   p.D = D;
+  p.split_waves = 8;
+  uint8_t* const ws = static_cast<uint8_t*>(op->ws);
+  p.partial = reinterpret_cast<float*>(ws + op->ws_partial_off);
+  p.counters = reinterpret_cast<unsigned*>(ws + op->ws_counters_off);
   p.status = op->status;
   p.timeout_ns = op->timeout_ns;
   p.debug_flags = op->debug_flags;
   op->debug_flags = 0;
-  return launched(launch_grouped(f, x128, x32, p, op->grid, st));
+  return launched(launch_grouped(op->wide, f, x128, x32, p, op->units, st));
 }
 
 // ---------------------------------------------------------------- 4-bit weights
