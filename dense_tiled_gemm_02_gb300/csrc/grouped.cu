@@ -31,8 +31,12 @@
 // group's end are columns of the accumulator that are not stored (rows), and
 // K past its end is read as zeros on both sides because the tensor maps end
 // there (an N-contiguous B gets a dimension per expert).  In grad the sum
-// itself is ragged: the last slice's rows past the group are overwritten
-// with zeros in shared memory, on both operands, before the MMA reads them.
+// itself is ragged: a small kernel before this one writes, per expert, copies
+// of both operands' tensor maps whose rows end where the group does, so that
+// rows past it are read as zeros too.  (Overwriting them with zeros in shared
+// memory instead put the clearing, and the odd CTA's word that it had been
+// done, between the last copy and the last MMA of every tile: 1.6 us a tile,
+// 338 us against 254 for 32 experts of 513 and of 528 rows, 2048 x 4096.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -52,10 +56,14 @@ constexpr int FT = 128;                       // features of a CTA
 constexpr uint32_t F_BYTES = FT * BK * 2;
 constexpr int RASTER = 8;                     // row tiles that share a features tile in L2
 constexpr int MIN_RUN = 8;                    // K slices: a shorter run costs more than it saves
-constexpr uint32_t EPI_BYTES = 32 * 64;       // staged 32 rows x 32 features of 16 bits
-// warp 0: TMA loads, 1: MMA issue, 2-5: epilogue, 6: schedule, 7: clears the
-// rows past a group (grad)
-constexpr int GROUPED_THREADS = 256;
+constexpr uint32_t EPI_BYTES = 32 * 256;      // staged 32 rows x 128 features of 16 bits
+// K slices by which a split must shorten the busiest unit's work: what the
+// exchange of partial sums costs (about 4 us at a quarter us a slice).
+constexpr int SPLIT_GAIN = 16;
+// warp 0: TMA loads, 1: MMA issue, 2-9: epilogue (two groups of four, taking
+// 32-row chunks of a tile in turn), 10: schedule
+constexpr int GROUPED_THREADS = 352;
+constexpr int EPI_WARPS = 8;
 constexpr int QUEUE = 4;                      // pieces the schedule runs ahead
 
 template <int CG, int QT, int STAGES>
@@ -64,8 +72,8 @@ struct Cfg {
   static constexpr uint32_t STAGE_BYTES = F_BYTES + X_BYTES;
   static constexpr uint32_t TMEM_COLS = 2 * QT;
   static constexpr uint32_t BAR_BYTES = 768;  // barriers, flags, queue of pieces
-  static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + 8 * EPI_BYTES + BAR_BYTES +
-                                   4 * (3 * GEMM_MAX_EXPERTS + 1);
+  static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + 2 * EPI_BYTES + BAR_BYTES +
+                                   4 * (2 * GEMM_MAX_EXPERTS + 2);
   static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -115,31 +123,19 @@ __device__ __forceinline__ void commit(uint32_t bar) {
     mma_commit(bar);
 }
 
-// bounded_wait for a barrier that another CTA arrives on after writing its own
-// shared memory: acquires at cluster scope.
-__device__ __forceinline__ bool bounded_wait_cluster(uint32_t bar, uint32_t parity,
-                                                     volatile int* abort, uint32_t* status,
-                                                     uint64_t timeout_ns) {
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t n = 1;; ++n) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((n & 31u) == 0u) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > timeout_ns) {
-        *abort = 1;
-        atomicOr(status, STATUS_TIMEOUT);
-        return false;
-      }
-    }
-  }
+// A tensor map that an earlier kernel wrote: before this thread's first copy by it.
+__device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+}
+
+// Store of a shared-memory box at (x, y, z), elements outside the tensor left
+// out; tracked as a bulk group of this thread.
+__device__ __forceinline__ void store_3d(const void* tmap, uint32_t src, int32_t x, int32_t y,
+                                         int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
 }
 
 // 16 lanes x 32 columns as 16 x 8 fragments: of columns 8 i .. 8 i + 7, thread
@@ -175,6 +171,11 @@ __device__ __forceinline__ int tile_width(int m, int tiles) {
   return ((m + tiles - 1) / tiles + 31) & ~31;
 }
 
+// Rows of expert e; offsets that decrease or leave [0, R] bound none.
+__device__ __forceinline__ int rows_of(const GroupedParams& p, const int* lo, int e) {
+  return lo[e] < 0 || lo[e + 1] < lo[e] || lo[e + 1] > p.R ? 0 : lo[e + 1] - lo[e];
+}
+
 // K slices of a sum over len; an empty one counts as a slice without MMAs, so
 // that its zeros (or C) are stored like any tile.
 __device__ __forceinline__ int slices_of(int len) { return max(1, (len + BK - 1) / BK); }
@@ -194,7 +195,7 @@ struct alignas(16) Piece {
 template <int CG, int QT>
 struct Schedule {
   const GroupedParams& p;
-  const int* lo;      // [E] first row, [E] end row
+  const int* lo;      // [E + 1] offsets
   const int* prefix;  // [E + 1]
   int c, units;
   int ft, tiles_e, kb;      // feature tiles; grad: tiles of an expert; rows: slices of a tile
@@ -212,11 +213,14 @@ struct Schedule {
     kb = slices_of(p.K);
     tiles = p.grad ? p.E * tiles_e : prefix[p.E] * ft;
     const int waves = tiles / units;
-    const bool split = tiles % units != 0 && waves < p.split_waves;
-    whole = !split ? tiles : (waves > 1 ? waves - 1 : 0) * units;
-    s0 = p.grad ? slices_before(whole) : static_cast<int64_t>(whole) * kb;
     const int64_t all = p.grad ? static_cast<int64_t>(prefix[p.E]) * tiles_e
                                : static_cast<int64_t>(tiles) * kb;
+    // whole tiles take waves + 1 tiles of the busiest unit's time, equal runs
+    // all / units slices
+    const int64_t tile_kb = tiles > 0 ? all / tiles : 0;
+    const bool split = tiles % units != 0 && (waves + 1) * tile_kb - all / units >= SPLIT_GAIN;
+    whole = !split ? tiles : (waves > 1 ? waves - 1 : 0) * units;
+    s0 = p.grad ? slices_before(whole) : static_cast<int64_t>(whole) * kb;
     len = all - s0;
     const int64_t most = min(static_cast<int64_t>(units), len / MIN_RUN);
     runs = static_cast<int>(max(static_cast<int64_t>(min(tiles - whole, units)), most));
@@ -247,7 +251,7 @@ struct Schedule {
   }
 
   __device__ __forceinline__ void place(Piece& x, int e, int tile_in_e) const {
-    const int rows = lo[e + p.E] - lo[e];
+    const int rows = rows_of(p, lo, e);
     const int m = p.grad ? p.K : rows;
     const int rt = row_tiles<QT>(m), w = tile_width(m, rt);
     int64_t ri, fi;
@@ -334,16 +338,17 @@ __device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) {
 template <int CG, int QT, int STAGES, int DT>
 __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmX128,
-                   const __grid_constant__ CUtensorMap tmX32, const GroupedParams p) {
+                   const __grid_constant__ CUtensorMap tmX32,
+                   const __grid_constant__ CUtensorMap tmD, const GroupedParams p) {
   using C = Cfg<CG, QT, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sF = smem;
   uint8_t* const sX = smem + STAGES * F_BYTES;
-  uint8_t* const sE = sX + STAGES * C::X_BYTES;  // epilogue: two buffers a warp
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(sE + 8 * EPI_BYTES);
-  constexpr int NBARS = 4 * STAGES + 5 + 2 * QUEUE;
+  uint8_t* const sE = sX + STAGES * C::X_BYTES;  // epilogue: two buffers
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(sE + 2 * EPI_BYTES);
+  constexpr int NBARS = 2 * STAGES + 5 + 2 * QUEUE;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* const ep_go = abort_flag + 1;
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
   Piece* const queue = reinterpret_cast<Piece*>(reinterpret_cast<uint8_t*>(bars) + 512);
   static_assert(8 * NBARS + 16 <= 512 && 512 + QUEUE * sizeof(Piece) <= C::BAR_BYTES, "layout");
   int* const lo = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + C::BAR_BYTES);
-  int* const prefix = lo + 2 * p.E;
+  int* const prefix = lo + p.E + 1;
 
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](uint32_t s) { return bar0 + 8u * s; };
@@ -359,14 +364,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
   auto acc_full = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
   auto acc_empty = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
   const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
-  // grad, per ring place: a slice that ends inside 16 rows has landed in this
-  // CTA; both CTAs' rows past the group are cleared (on the even CTA).  One
-  // each per place: with groups of a slice or less the clearing runs up to a
-  // ring ahead of the MMA.
-  auto tail_full = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
-  auto tail_clear = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + 5 + s); };
-  auto q_full = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + i); };
-  auto q_empty = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + QUEUE + i); };
+  auto q_full = [&](uint32_t i) { return bar0 + 8u * (2 * STAGES + 5 + i); };
+  auto q_empty = [&](uint32_t i) { return bar0 + 8u * (2 * STAGES + 5 + QUEUE + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
@@ -375,16 +374,14 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
-      mbar_init(tail_full(s), 1);
-      mbar_init(tail_clear(s), CG);
     }
     for (int i = 0; i < QUEUE; ++i) {
       mbar_init(q_full(i), 1);
-      mbar_init(q_empty(i), p.grad ? 7 : 6);  // one arrival per warp that reads a piece
+      mbar_init(q_empty(i), 2 + EPI_WARPS);  // one arrival per warp that reads a piece
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 4 * CG);
+      mbar_init(acc_empty(b), EPI_WARPS * CG);
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -392,9 +389,12 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     fence_proxy_async_smem();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmF);
-    tma_prefetch_desc(&tmX128);
-    if (!p.grad) tma_prefetch_desc(&tmX32);
+    if (!p.grad) {
+      tma_prefetch_desc(&tmF);
+      tma_prefetch_desc(&tmX128);
+      tma_prefetch_desc(&tmX32);
+    }
+    if (p.d_tma) tma_prefetch_desc(&tmD);
   }
   if (warp == 1) {
     if constexpr (CG == 2) {
@@ -407,15 +407,14 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
   }
   pdl_wait();
   pdl_trigger();
-  for (int e = threadIdx.x; e < p.E; e += GROUPED_THREADS) {
-    const int2 r = expert_rows(p.offsets, e, p.R, p.status);
-    lo[e] = r.x;
-    lo[e + p.E] = r.y;
+  for (int e = threadIdx.x; e <= p.E; e += GROUPED_THREADS) {
+    lo[e] = p.offsets[e];
+    if (e < p.E) expert_rows(p.offsets, e, p.R, p.status);
   }
   __syncthreads();
   if (warp == 2) {  // the prefix: each lane a run of experts, then a warp scan
     auto count = [&](int e) {
-      const int rows = lo[e + p.E] - lo[e];
+      const int rows = rows_of(p, lo, e);
       return p.grad ? slices_of(rows) : row_tiles<QT>(rows);
     };
     const int len = (p.E + 31) / 32, b = min(p.E, lane * len), e1 = min(p.E, b + len);
@@ -458,11 +457,9 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     }
     return x.more != 0;
   };
-  // The piece's last slice ends inside 16 rows of another expert's.
-  auto is_ragged = [&](const Piece& x) { return p.grad && (x.kend - x.k) % 16 != 0; };
   Piece x;
 
-  if (warp == 6) {
+  if (warp == 10) {
     // ------------------------------------------------------------ schedule (each CTA)
     // A piece costs a few hundred instructions (bisection, divisions); taken
     // by the MMA warp itself they held the tensor pipe up at every tile.
@@ -483,66 +480,86 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     __syncwarp();
   } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (each CTA)
+    // The slice loop is kept tight, one copy of it per kind of operand: at
+    // 512 tensor cycles a slice, the 650 that a general loop took to issue
+    // one (branches and box loops inside) set the speed of the whole kernel.
     uint32_t it = 0, s = 0, ph = 0;
-    uint32_t tail_used = 0, tail_ph = 0;  // bit s: used; parity of the next use
+    int mapped = -1;  // grad: the expert whose tensor maps have been acquired
     bool stop = false, skipped = false;
+    const uint32_t sF0 = smem_u32(sF), sX0 = smem_u32(sX);
+    const uint32_t full0 = CG == 2 ? map_shared_rank(full(0), 0) : full(0);
     while (next_piece(x)) {
       if (lane == 0 && !stop) {
         const int half = ((x.nq + 31) & ~31) / CG;  // this CTA's rows of the tile
         const int q0 = x.q0 + static_cast<int>(rank) * half, f0 = x.f0 + static_cast<int>(rank) * FT;
         const bool big = half > 64;
-        const int boxes = p.grad ? (half + 63) / 64 : (big ? (half + 127) / 128 : (half + 31) / 32);
+        const int boxes = p.grad ? (half + 63) / 64 : (big ? 1 : (half + 31) / 32);
         const uint32_t bytes = F_BYTES + boxes * (p.grad ? 8192u : (big ? 16384u : 4096u));
-        for (int k = x.k; k < x.kend; k += BK) {
-          if (!bounded_wait(empty(s), ph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo)) {
-            stop = true;
-            break;
-          }
-          const uint32_t fd = smem_u32(sF + s * F_BYTES), xd = smem_u32(sX + s * C::X_BYTES);
-          // both CTAs' copies are counted by the even CTA, but for a slice
-          // whose rows past the group are to be cleared before the MMA
-          const bool tail = k + BK > x.kend && is_ragged(x);
-          uint32_t fb = full(s);
-          if (tail)
-            fb = tail_full(s);
-          else if constexpr (CG == 2)
-            fb = map_shared_rank(full(s), 0);
-          if ((p.debug_flags & DBG_SKIP_FIRST_FILL) && it == 0 && leader) {
-            skipped = true;  // test hook: the MMA's wait on the first stage expires
-          } else {
-            if (tail) {
-              mbar_arrive_expect_tx(tail_full(s), bytes);
-              tail_used |= 1u << s;
-              tail_ph ^= 1u << s;
-              if (leader) mbar_arrive(full(s));  // this use of the place, in step
-            } else if (leader) {
-              mbar_arrive_expect_tx(full(s), CG * bytes);
+        const uint32_t both = CG * bytes;
+        const int frow = x.e * p.N + f0;
+        auto slices = [&](auto copies) {
+          for (int k = x.k; k < x.kend; k += BK) {
+            if (!bounded_wait(empty(s), ph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo)) {
+              stop = true;
+              return;
             }
-            if (p.grad) {
-              for (int i = 0; i < FT / 64; ++i)
-                load_2d<CG>(fd + i * 8192u, &tmF, f0 + 64 * i, x.base + k, fb);
-              for (int i = 0; i < boxes; ++i)
-                load_2d<CG>(xd + i * 8192u, &tmX128, q0 + 64 * i, x.base + k, fb);
+            if (it == 0 && leader && (p.debug_flags & DBG_SKIP_FIRST_FILL)) {
+              skipped = true;  // test hook: the MMA's wait on the first stage expires
             } else {
-              if (p.f_mn) {
-                for (int i = 0; i < FT / 64; ++i)
-                  load_3d<CG>(fd + i * 8192u, &tmF, f0 + 64 * i, k, x.e, fb);
-              } else {
-                load_2d<CG>(fd, &tmF, k, x.e * p.N + f0, fb);
-              }
-              for (int i = 0; i < boxes; ++i) {
-                if (big)
-                  load_2d<CG>(xd + i * 16384u, &tmX128, k, q0 + 128 * i, fb);
-                else
-                  load_2d<CG>(xd + i * 4096u, &tmX32, k, q0 + 32 * i, fb);
-              }
+              if (leader) mbar_arrive_expect_tx(full(s), both);
+              copies(k, sF0 + s * F_BYTES, sX0 + s * C::X_BYTES, full0 + 8u * s);
+            }
+            ++it;
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1u;
             }
           }
-          ++it;
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
+        };
+        const CUtensorMap* const mf = p.maps + x.e;  // grad: the maps that end with the group
+        const CUtensorMap* const mx = mf + p.E;
+        if (p.grad && x.k < x.kend && mapped != x.e) {
+          acquire_map(mf);
+          acquire_map(mx);
+          mapped = x.e;
+        }
+        auto grad_copies = [&](int k, uint32_t fd, uint32_t xd, uint32_t bar) {
+          const int r = x.base + k;
+          load_2d<CG>(fd, mf, f0, r, bar);
+          load_2d<CG>(fd + 8192u, mf, f0 + 64, r, bar);
+          load_2d<CG>(xd, mx, q0, r, bar);
+          if (boxes > 1) load_2d<CG>(xd + 8192u, mx, q0 + 64, r, bar);
+        };
+        auto f_copies = [&](int k, uint32_t fd, uint32_t bar) {  // N-contiguous B
+          load_3d<CG>(fd, &tmF, f0, k, x.e, bar);
+          load_3d<CG>(fd + 8192u, &tmF, f0 + 64, k, x.e, bar);
+        };
+        auto x_copies = [&](int k, uint32_t xd, uint32_t bar) {  // up to 64 rows
+          load_2d<CG>(xd, &tmX32, k, q0, bar);
+          if (boxes > 1) load_2d<CG>(xd + 4096u, &tmX32, k, q0 + 32, bar);
+        };
+        if (p.grad) {
+          slices(grad_copies);
+        } else if (p.f_mn && big) {
+          slices([&](int k, uint32_t fd, uint32_t xd, uint32_t bar) {
+            f_copies(k, fd, bar);
+            load_2d<CG>(xd, &tmX128, k, q0, bar);
+          });
+        } else if (p.f_mn) {
+          slices([&](int k, uint32_t fd, uint32_t xd, uint32_t bar) {
+            f_copies(k, fd, bar);
+            x_copies(k, xd, bar);
+          });
+        } else if (big) {
+          slices([&](int k, uint32_t fd, uint32_t xd, uint32_t bar) {
+            load_2d<CG>(fd, &tmF, k, frow, bar);
+            load_2d<CG>(xd, &tmX128, k, q0, bar);
+          });
+        } else {
+          slices([&](int k, uint32_t fd, uint32_t xd, uint32_t bar) {
+            load_2d<CG>(fd, &tmF, k, frow, bar);
+            x_copies(k, xd, bar);
+          });
         }
       }
       __syncwarp();
@@ -550,9 +567,6 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     if (lane == 0) {
       // Copies in flight land before the CTA leaves.  The even CTA's barriers
       // count both CTAs' (after giving up, the odd CTA gives its own time).
-      for (uint32_t j = 0; j < STAGES; ++j)
-        if ((tail_used >> j) & 1u)
-          drain_wait(tail_full(j), ((tail_ph >> j) & 1u) ^ 1u, 200000000ull);
       if (leader) {
         for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j) {
           if (skipped && j == 0) continue;
@@ -569,9 +583,12 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     const uint32_t f_lo0 = sdesc_lo(smem_u32(sF), p.f_mn ? 8192u : 16u);
     const uint32_t x_lo0 = sdesc_lo(smem_u32(sX), p.grad ? 8192u : 16u);
     const uint32_t dhi = sdesc_hi_sw128(1024u);
+    // K steps of a slice, in 16-byte units: 32 bytes along a K-major row, 16
+    // rows of an MN-major tile
     const uint32_t f_step = p.f_mn ? 128u : 2u, x_step = p.grad ? 128u : 2u;
+    const uint32_t f_off[4] = {0u, f_step, 2 * f_step, 3 * f_step};
+    const uint32_t x_off[4] = {0u, x_step, 2 * x_step, 3 * x_step};
     uint32_t s = 0, ph = 0, acc_it = 0;
-    uint32_t tail_ph = 0;  // bit s: parity of the next ragged slice in place s
     bool ok = true;
     while (next_piece(x)) {
       if (leader && lane == 0 && ok && x.k < x.kend) {
@@ -589,7 +606,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
           const uint32_t f_lo = f_lo0 + s * (F_BYTES >> 4), x_lo = x_lo0 + s * (C::X_BYTES >> 4);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            mma<CG>(d_tmem, sdesc(dhi, f_lo + c * f_step), sdesc(dhi, x_lo + c * x_step), idesc,
+            mma<CG>(d_tmem, sdesc(dhi, f_lo + f_off[c]), sdesc(dhi, x_lo + x_off[c]), idesc,
                     accumulate | c);
           accumulate = 1;
           commit<CG>(empty(s));
@@ -601,10 +618,6 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         const int left = x.kend - x.k - nfull * BK;  // a last slice that is not whole
         if (ok && left > 0) {
           ok = bounded_wait(full(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
-          if (ok && is_ragged(x)) {
-            ok = bounded_wait_cluster(tail_clear(s), (tail_ph >> s) & 1u, abort_flag, p.status, tmo);
-            tail_ph ^= 1u << s;
-          }
           if (ok) {
             const uint32_t f_lo = f_lo0 + s * (F_BYTES >> 4), x_lo = x_lo0 + s * (C::X_BYTES >> 4);
             for (int c = 0; c < (left + 15) / 16; ++c)
@@ -627,49 +640,12 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       drain_wait(done_bar, 0, 200000000ull);
     }
     __syncwarp();
-  } else if (warp == 7) {
-    // ------------------------------------------------------------ rows past a group (each CTA)
-    // Zeros over the rows [left, 16 chunks) of a ragged slice, which belong to
-    // another expert (or to nobody), in every 64-wide box of both operands.
-    uint32_t s = 0, tail_ph = 0;
-    bool ok = p.grad != 0;
-    while (ok && next_piece(x)) {
-      const int n = x.kend - x.k;
-      if (n > 0 && is_ragged(x)) {
-        const uint32_t at = (s + n / BK) % STAGES;  // the place of the piece's last slice
-        const int left = n % BK;
-        if (lane == 0)
-          ok = bounded_wait(tail_full(at), (tail_ph >> at) & 1u, abort_flag, p.status,
-                            STATUS_TIMEOUT, tmo);
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        if (!ok) break;
-        tail_ph ^= 1u << at;
-        const int n16 = ((left + 15) / 16 * 16 - left) * 8;  // 16-byte units per box
-        const int boxes = FT / 64 + (((x.nq + 31) & ~31) / CG + 63) / 64;
-        for (int i = lane; i < n16 * boxes; i += 32) {
-          const int b = i / n16, u = i - b * n16;
-          uint8_t* const base = b < FT / 64 ? sF + at * F_BYTES + b * 8192
-                                            : sX + at * C::X_BYTES + (b - FT / 64) * 8192;
-          *reinterpret_cast<uint4*>(base + left * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 2)
-            mbar_arrive_cluster(map_shared_rank(tail_clear(at), 0));
-          else
-            mbar_arrive(tail_clear(at));
-        }
-      }
-      s = (s + static_cast<uint32_t>((max(n, 0) + BK - 1) / BK)) % STAGES;
-    }
   } else {
     // ------------------------------------------------------------ epilogue (each CTA)
-    const int q = warp & 3;
+    const int q = warp & 3, group = (warp - 2) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    const bool ep_leader = threadIdx.x == 64;
-    uint8_t* const stage = sE + q * 2 * EPI_BYTES;
-    uint32_t acc_it = 0, staged = 0;
+    const bool ep_leader = threadIdx.x == 64, group_leader = threadIdx.x == 64 + 128 * group;
+    uint32_t acc_it = 0;
     const int unit = blockIdx.x / CG;
     while (next_piece(x)) {
       const uint32_t buf = acc_it & 1u;
@@ -678,9 +654,9 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         if (ep_leader)
           *ep_go = bounded_wait(acc_full(buf), (acc_it >> 1) & 1u, abort_flag, p.status,
                                 STATUS_TIMEOUT, tmo) ? 1 : 0;
-        named_barrier_sync(1, 128);
+        named_barrier_sync(1, 32 * EPI_WARPS);
         const bool go = *ep_go != 0;
-        named_barrier_sync(1, 128);
+        named_barrier_sync(1, 32 * EPI_WARPS);
         if (!go) break;
         tc_fence_after();
       }
@@ -694,54 +670,85 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             mbar_arrive(acc_empty(buf));
         }
       };
-      const int f32 = x.f0 + static_cast<int>(rank) * FT + q * 32;  // this warp's features
-      const int f = f32 + lane;
+      const int f = x.f0 + static_cast<int>(rank) * FT + q * 32 + lane;
       const long long row0 = p.grad ? static_cast<long long>(x.e) * p.K + x.q0 : x.q0;
       const uint32_t taddr = tmem_base + lane_base + buf * QT;
-      if (sum && x.pieces == 1 && p.d_vec && !p.C) {
-        // 16-bit D, 16-byte rows: the fragments of 32 rows x 32 features are
-        // transposed into rows by stmatrix (16-byte units, unit u of row r at
-        // u ^ (r / 2) % 4 against bank conflicts) and leave as 16-byte stores
+      // This warp's last chunk of the tile; a tile of one chunk leaves the
+      // second group without any.
+      const int c_first = 32 * group;
+      auto c_last = [&](int c) { return c + 64 >= x.nq; };
+      if (sum && c_first >= x.nq) release();
+      // 16-bit D with 16-byte rows and no C leaves through shared memory, 32
+      // rows x 128 features at a time: a group's four warps put their features
+      // side by side (two boxes of 64 features, unit u of row r at u ^ r % 8,
+      // which is the TMA's swizzle and spares bank conflicts) and one thread
+      // stores the boxes by TMA.  The box that a group of rows ends in (rows
+      // form), or an N off the 16-byte grid, is stored by the threads.
+      const bool staged_store = DT != T_F32 && p.d_vec && !p.C;
+      uint8_t* const stage = sE + group * EPI_BYTES;
+      const uint32_t gbar = 2 + group;
+      auto stage_at = [&](int row, int u) {
+        return stage + (u >> 3) * 4096 + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+      };
+      auto stage_free = [&] {  // the chunk before has left the buffer
+        if (group_leader) bulk_wait_read_all();
+        named_barrier_sync(gbar, 128);
+      };
+      auto copy_out = [&](int c) {  // rows c .. c + 31 of the tile
+        const int fc = x.f0 + static_cast<int>(rank) * FT;
+        const bool box = p.d_tma && (p.grad || c + 32 <= x.nq);
+        if (box) fence_proxy_async_smem();
+        named_barrier_sync(gbar, 128);
+        if (box) {
+          if (group_leader) {
+            const uint32_t src = smem_u32(stage);
+            const int y = x.q0 + c, z = p.grad ? x.e : 0;
+            if (fc < p.N) store_3d(&tmD, src, fc, y, z);
+            if (fc + 64 < p.N) store_3d(&tmD, src + 4096u, fc + 64, y, z);
+            bulk_commit();
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 8 * q + 2 * i + (lane >> 4), u = lane & 15;
+            const int f8 = fc + 8 * u;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage_at(row, u));
+            if (c + row < x.nq && f8 < p.N) {
+              uint16_t* const d = static_cast<uint16_t*>(p.D) + (row0 + c + row) * p.ldd + f8;
+              if (f8 + 8 <= p.N) {
+                *reinterpret_cast<uint4*>(d) = v;
+              } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int j = 0; j < p.N - f8; ++j)
+                  d[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+              }
+            }
+          }
+        }
+      };
+      if (sum && x.pieces == 1 && staged_store) {
+        // fragments of 16 features x 8 rows, transposed into rows by stmatrix
         if constexpr (DT != T_F32) {
 #pragma unroll 1
-          for (int c = 0; c < x.nq; c += 32) {
+          for (int c = c_first; c < x.nq; c += 64) {
             uint32_t r[32];
             tmem_ld_16x256b_x4(taddr + c, r);
             tmem_ld_16x256b_x4(taddr + c + (16u << 16), r + 16);
             tmem_ld_wait();
-            if (c + 32 >= x.nq) release();
-            uint8_t* const out = stage + (staged++ & 1u) * EPI_BYTES;
+            if (c_last(c)) release();
             const int m = lane >> 3;
+            stage_free();
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int i = 0; i < 4; i += 2) {
                 const uint32_t* const v = r + 16 * h + 4 * i;
-                const int row = 8 * (i + (m >> 1)) + (lane & 7);
-                const int u = (2 * h + (m & 1)) ^ ((row >> 1) & 3);
-                stmatrix_x4_trans(smem_u32(out + row * 64 + u * 16), pack2<DT>(v[0], v[1]),
-                                  pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
-                                  pack2<DT>(v[6], v[7]));
+                stmatrix_x4_trans(
+                    smem_u32(stage_at(8 * (i + (m >> 1)) + (lane & 7), 4 * q + 2 * h + (m & 1))),
+                    pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
+                    pack2<DT>(v[6], v[7]));
               }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 8 * i + (lane >> 2), u = lane & 3;
-              const uint4 v =
-                  *reinterpret_cast<const uint4*>(out + row * 64 + ((u ^ ((row >> 1) & 3)) << 4));
-              const int f8 = f32 + 8 * u;
-              if (c + row < x.nq && f8 < p.N) {
-                uint16_t* const d =
-                    static_cast<uint16_t*>(p.D) + (row0 + c + row) * p.ldd + f8;
-                if (f8 + 8 <= p.N) {
-                  *reinterpret_cast<uint4*>(d) = v;
-                } else {
-                  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                  for (int j = 0; j < p.N - f8; ++j)
-                    d[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-                }
-              }
-            }
+            copy_out(c);
           }
         }
         ++acc_it;
@@ -758,7 +765,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         // leave the sums, see who is last
         float4* const mine = partial(unit, x.slot);
 #pragma unroll 1
-        for (int c = 0; c < x.nq; c += 32) {
+        for (int c = c_first; c < x.nq; c += 64) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(taddr + c, v);
           tmem_ld_wait();
@@ -769,7 +776,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
         }
         __threadfence();
-        named_barrier_sync(1, 128);
+        named_barrier_sync(1, 32 * EPI_WARPS);
         if (ep_leader) {
           unsigned* const count = p.counters + x.first * CG + rank;
           const bool last = atomicAdd(count, 1u) == static_cast<unsigned>(x.pieces) - 1u;
@@ -777,24 +784,24 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
           __threadfence();
           *ep_last = last ? 1 : 0;
         }
-        named_barrier_sync(1, 128);
+        named_barrier_sync(1, 32 * EPI_WARPS);
         const bool last = *ep_last != 0;
-        named_barrier_sync(1, 128);
+        named_barrier_sync(1, 32 * EPI_WARPS);
         if (!last) {
-          release();
+          if (c_first < x.nq) release();
           ++acc_it;
           continue;
         }
         __threadfence();
       }
 #pragma unroll 1
-      for (int c = 0; c < x.nq; c += 32) {
+      for (int c = c_first; c < x.nq; c += 64) {
         float v[32];
         if (sum) {
           uint32_t r[32];
           tmem_ld_32x32b_x32(taddr + c, r);
           tmem_ld_wait();
-          if (c + 32 >= x.nq) release();
+          if (c_last(c)) release();
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
         } else {
@@ -829,7 +836,16 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = t[j];
         }
-        if (f < p.N) {
+        if (staged_store) {
+          stage_free();
+          if constexpr (DT != T_F32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              *reinterpret_cast<uint16_t*>(stage_at(j, 4 * q + (lane >> 3)) + 2 * (lane & 7)) =
+                  static_cast<uint16_t>(pack2<DT>(__float_as_uint(v[j]), 0u));
+          }
+          copy_out(c);
+        } else if (f < p.N) {
           if (p.C) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -843,6 +859,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       }
       if (sum) ++acc_it;
     }
+    if (group_leader) bulk_wait_all();  // shared memory outlives the stores that read it
   }
   tc_fence_before();
   if constexpr (CG == 2)
@@ -856,6 +873,37 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     else
       tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
+}
+
+// ---------------------------------------------------------------- tensor maps of grad
+// One warp per expert: copies of the two maps whose second dimension (rows)
+// ends where the expert's group does.  (An empty group's are not used.)
+__global__ void __launch_bounds__(32)
+    group_maps_kernel(const __grid_constant__ CUtensorMap f, const __grid_constant__ CUtensorMap x,
+                      const int* offsets, int E, int R, CUtensorMap* maps, uint32_t* status) {
+  __shared__ __align__(128) CUtensorMap sm[2];
+  const int e = blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int2 r = expert_rows(offsets, e, R, status);
+  if (threadIdx.x < 16) {
+    const uint4* const src = reinterpret_cast<const uint4*>(threadIdx.x < 8 ? &f : &x);
+    reinterpret_cast<uint4*>(sm)[threadIdx.x] = src[threadIdx.x & 7];
+  }
+  __syncwarp();
+  if (threadIdx.x < 2)
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(
+                     smem_u32(sm + threadIdx.x)),
+                 "r"(max(r.y, 1))
+                 : "memory");
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm volatile(
+        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned "
+        "[%0], [%1], 128;" ::"l"(maps + i * E + e),
+        "r"(smem_u32(sm + i))
+        : "memory");
 }
 
 // ---------------------------------------------------------------- launches
@@ -896,10 +944,10 @@ int prepare(int num_sms) {
 
 template <int CG, int QT, int STAGES, int DT>
 cudaError_t launch(const CUtensorMap& f, const CUtensorMap& x128, const CUtensorMap& x32,
-                   const GroupedParams& p, int units, cudaStream_t st) {
+                   const CUtensorMap& d, const GroupedParams& p, int units, cudaStream_t st) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = config<CG, QT, STAGES, DT>(units, st, attr);
-  return cudaLaunchKernelEx(&cfg, grouped_kernel<CG, QT, STAGES, DT>, f, x128, x32, p);
+  return cudaLaunchKernelEx(&cfg, grouped_kernel<CG, QT, STAGES, DT>, f, x128, x32, d, p);
 }
 
 template <int DT>
@@ -909,10 +957,10 @@ int prepare_typed(bool wide, int num_sms) {
 }
 template <int DT>
 cudaError_t launch_typed(bool wide, const CUtensorMap& f, const CUtensorMap& x128,
-                         const CUtensorMap& x32, const GroupedParams& p, int units,
-                         cudaStream_t st) {
-  return wide ? launch<2, WIDE_QT, WIDE_STAGES, DT>(f, x128, x32, p, units, st)
-              : launch<1, NARROW_QT, NARROW_STAGES, DT>(f, x128, x32, p, units, st);
+                         const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
+                         int units, cudaStream_t st) {
+  return wide ? launch<2, WIDE_QT, WIDE_STAGES, DT>(f, x128, x32, d, p, units, st)
+              : launch<1, NARROW_QT, NARROW_STAGES, DT>(f, x128, x32, d, p, units, st);
 }
 
 }  // namespace
@@ -928,11 +976,16 @@ size_t grouped_partial_bytes(bool wide, int units) {
 }
 
 cudaError_t launch_grouped(bool wide, const CUtensorMap& f, const CUtensorMap& x128,
-                           const CUtensorMap& x32, const GroupedParams& p, int units,
-                           cudaStream_t st) {
-  return p.d_type == T_F32    ? launch_typed<T_F32>(wide, f, x128, x32, p, units, st)
-         : p.d_type == T_BF16 ? launch_typed<T_BF16>(wide, f, x128, x32, p, units, st)
-                              : launch_typed<T_F16>(wide, f, x128, x32, p, units, st);
+                           const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
+                           int units, cudaStream_t st) {
+  if (p.grad && p.R > 0) {
+    const cudaError_t e = launch_pdl(group_maps_kernel, dim3(p.E), dim3(32), 0, st, f, x128,
+                                     p.offsets, p.E, p.R, p.maps, p.status);
+    if (e != cudaSuccess) return e;
+  }
+  return p.d_type == T_F32    ? launch_typed<T_F32>(wide, f, x128, x32, d, p, units, st)
+         : p.d_type == T_BF16 ? launch_typed<T_BF16>(wide, f, x128, x32, d, p, units, st)
+                              : launch_typed<T_F16>(wide, f, x128, x32, d, p, units, st);
 }
 
 }  // namespace gb300

@@ -84,12 +84,12 @@ struct GroupedParams {
   const void* C;
   int d_type;          // also C's
   int d_vec;           // 16-bit D whose rows start on 16-byte boundaries
+  int d_tma;           // and N a multiple of 8: stored by TMA
   long long ldc, ldd;
   void* D;
-  // Fewer full waves than this: the partial last wave is dealt by K slices.
-  int split_waves;
   float* partial;      // grouped_partial_bytes()
   unsigned* counters;  // one per CTA, zero between calls
+  CUtensorMap* maps;   // grad: the experts' maps of the features, then of the rows operand
   uint32_t* status;
   unsigned long long timeout_ns;
   int debug_flags;
@@ -99,10 +99,12 @@ struct GroupedParams {
 int prepare_grouped(bool wide, int d_type, int num_sms);
 size_t grouped_partial_bytes(bool wide, int units);
 // Tensor maps: the features operand; the rows operand in boxes of 128 rows
-// and of 32 (rows form; in grad x128 has 64 x 64 boxes and x32 is not read).
+// and of 32 (rows form; in grad x128 has 64 x 64 boxes, x32 is not read, and
+// both are copied into p.maps per expert);
+// D in boxes of 64 columns x 32 rows (when d_tma).
 cudaError_t launch_grouped(bool wide, const CUtensorMap& f, const CUtensorMap& x128,
-                           const CUtensorMap& x32, const GroupedParams& p, int units,
-                           cudaStream_t st);
+                           const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
+                           int units, cudaStream_t st);
 
 // ---------------------------------------------------------------- 4-bit weights (w4.cu)
 struct W4Params {

@@ -49,7 +49,7 @@ struct gemm_op {
   bool copy_a = false, copy_b = false;
   int64_t a_rows = 0, a_cols = 0, b_rows = 0, b_cols = 0;
   int64_t ws_lda = 0, ws_ldb = 0;
-  size_t ws_b_off = 0, ws_partial_off = 0, ws_counters_off = 0;
+  size_t ws_b_off = 0, ws_partial_off = 0, ws_counters_off = 0, ws_maps_off = 0;
   bool wide = false;
   int units = 0;
   int grid = 0;  // route: blocks
@@ -393,7 +393,9 @@ int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc) {
   const size_t counters = 4 * static_cast<size_t>(most_units) * (wide ? 2 : 1);
   const size_t p_off = static_cast<size_t>(up(static_cast<int64_t>(a_bytes + b_bytes), 256));
   gemm_op* op = nullptr;
-  const int rc = make_op(Kind::kGrouped, p_off + partial + counters, &op);
+  const size_t maps_off = static_cast<size_t>(up(static_cast<int64_t>(p_off + partial + counters), 256));
+  const size_t maps = grad ? 2 * sizeof(CUtensorMap) * d.E : 0;
+  const int rc = make_op(Kind::kGrouped, maps_off + maps, &op);
   if (rc != GEMM_OK) return rc;
   op->units = std::min(most_units, prepare_grouped(wide, d.d_type, op->num_sms));
   if (op->units <= 0) {
@@ -404,6 +406,7 @@ int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc) {
   op->wide = wide;
   op->ws_partial_off = p_off;
   op->ws_counters_off = p_off + partial;
+  op->ws_maps_off = maps_off;
   op->grouped = d;
   op->copy_a = copy_a;
   op->copy_b = copy_b;
@@ -456,7 +459,7 @@ int gemm_grouped_run(gemm_op_t op, const void* A, const void* B, const int32_t* 
     if (rc != GEMM_OK) return rc;
   }
   GroupedParams p{};
-  CUtensorMap f{}, x128{}, x32{};
+  CUtensorMap f{}, x128{}, x32{}, dm{};
   if (reads) {
     bool ok;
     if (grad) {
@@ -482,18 +485,22 @@ int gemm_grouped_run(gemm_op_t op, const void* A, const void* B, const int32_t* 
   p.C = C;
   p.d_type = d.d_type;
   p.d_vec = is_16bit(d.d_type) && d.ldd % 8 == 0 && aligned(D, 16);
+  p.d_tma = p.d_vec && d.N % 8 == 0 && !C;
+  if (p.d_tma && !(grad ? encode_rows(&dm, D, d.ldd, d.N, d.K, d.E, 64, 32)
+                        : encode_rows(&dm, D, d.ldd, d.N, d.R, 1, 64, 32)))
+    return GEMM_ERR_CUDA;
   p.ldc = d.ldc;
   p.ldd = d.ldd;
   p.D = D;
-  p.split_waves = 8;
   uint8_t* const ws = static_cast<uint8_t*>(op->ws);
   p.partial = reinterpret_cast<float*>(ws + op->ws_partial_off);
   p.counters = reinterpret_cast<unsigned*>(ws + op->ws_counters_off);
+  p.maps = reinterpret_cast<CUtensorMap*>(ws + op->ws_maps_off);
   p.status = op->status;
   p.timeout_ns = op->timeout_ns;
   p.debug_flags = op->debug_flags;
   op->debug_flags = 0;
-  return launched(launch_grouped(op->wide, f, x128, x32, p, op->units, st));
+  return launched(launch_grouped(op->wide, f, x128, x32, dm, p, op->units, st));
 }
 
 // ---------------------------------------------------------------- 4-bit weights
