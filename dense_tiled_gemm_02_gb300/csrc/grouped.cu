@@ -12,8 +12,10 @@
 //
 // Two forms of one kernel:
 //   wide    CTA pairs (cta_group::2), 256 features x up to 256 rows; each CTA
-//           stages its 128 features and half of the rows, six 32 KB stages.
-//           Bound by the tensor pipe.
+//           stages its 128 features and half of the rows, five 32 KB stages
+//           (a sixth queued more loads in front of D's stores: 247 us against
+//           239 for 32 x 2048 x 4096 gradients of 512 rows).  Bound by the
+//           tensor pipe.
 //   narrow  single CTAs, 128 features x up to 64 rows, eight 24 KB stages: for
 //           groups of few rows, where reading the weights is the bound and
 //           bytes in flight count.
@@ -68,11 +70,13 @@ constexpr int QUEUE = 4;                      // pieces the schedule runs ahead
 
 template <int CG, int QT, int STAGES>
 struct Cfg {
+  // Buffers of an epilogue group: D's stores wait their turn behind the loads.
+  static constexpr int BUFS = CG == 2 ? 2 : 1;
   static constexpr uint32_t X_BYTES = (QT / CG) * BK * 2;
   static constexpr uint32_t STAGE_BYTES = F_BYTES + X_BYTES;
   static constexpr uint32_t TMEM_COLS = 2 * QT;
   static constexpr uint32_t BAR_BYTES = 768;  // barriers, flags, queue of pieces
-  static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + 2 * EPI_BYTES + BAR_BYTES +
+  static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + 2 * BUFS * EPI_BYTES + BAR_BYTES +
                                    4 * (2 * GEMM_MAX_EXPERTS + 2);
   static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
 };
@@ -136,6 +140,12 @@ __device__ __forceinline__ void store_3d(const void* tmap, uint32_t src, int32_t
                    reinterpret_cast<uint64_t>(tmap)),
                "r"(x), "r"(y), "r"(z), "r"(src)
                : "memory");
+}
+
+// Wait until at most N committed store groups still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // 16 lanes x 32 columns as 16 x 8 fragments: of columns 8 i .. 8 i + 7, thread
@@ -346,8 +356,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sF = smem;
   uint8_t* const sX = smem + STAGES * F_BYTES;
-  uint8_t* const sE = sX + STAGES * C::X_BYTES;  // epilogue: two buffers
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(sE + 2 * EPI_BYTES);
+  uint8_t* const sE = sX + STAGES * C::X_BYTES;  // epilogue: BUFS buffers a group
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(sE + 2 * C::BUFS * EPI_BYTES);
   constexpr int NBARS = 2 * STAGES + 5 + 2 * QUEUE;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -646,6 +656,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const bool ep_leader = threadIdx.x == 64, group_leader = threadIdx.x == 64 + 128 * group;
     uint32_t acc_it = 0;
+    int buffer = 0;  // of the next chunk
     const int unit = blockIdx.x / CG;
     while (next_piece(x)) {
       const uint32_t buf = acc_it & 1u;
@@ -685,13 +696,12 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       // stores the boxes by TMA.  The box that a group of rows ends in (rows
       // form), or an N off the 16-byte grid, is stored by the threads.
       const bool staged_store = DT != T_F32 && p.d_vec && !p.C;
-      uint8_t* const stage = sE + group * EPI_BYTES;
       const uint32_t gbar = 2 + group;
       auto stage_at = [&](int row, int u) {
-        return stage + (u >> 3) * 4096 + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+        return sE + (C::BUFS * group + buffer) * EPI_BYTES + (u >> 3) * 4096 + row * 128 + (((u & 7) ^ (row & 7)) << 4);
       };
-      auto stage_free = [&] {  // the chunk before has left the buffer
-        if (group_leader) bulk_wait_read_all();
+      auto stage_free = [&] {  // the buffer's last chunk has left it
+        if (group_leader) bulk_wait_read<C::BUFS - 1>();
         named_barrier_sync(gbar, 128);
       };
       auto copy_out = [&](int c) {  // rows c .. c + 31 of the tile
@@ -701,7 +711,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         named_barrier_sync(gbar, 128);
         if (box) {
           if (group_leader) {
-            const uint32_t src = smem_u32(stage);
+            const uint32_t src = smem_u32(sE + (C::BUFS * group + buffer) * EPI_BYTES);
             const int y = x.q0 + c, z = p.grad ? x.e : 0;
             if (fc < p.N) store_3d(&tmD, src, fc, y, z);
             if (fc + 64 < p.N) store_3d(&tmD, src + 4096u, fc + 64, y, z);
@@ -725,6 +735,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             }
           }
         }
+        buffer = buffer + 1 == C::BUFS ? 0 : buffer + 1;
       };
       if (sum && x.pieces == 1 && staged_store) {
         // fragments of 16 features x 8 rows, transposed into rows by stmatrix
@@ -907,7 +918,7 @@ __global__ void __launch_bounds__(32)
 }
 
 // ---------------------------------------------------------------- launches
-constexpr int WIDE_QT = 256, WIDE_STAGES = 6;
+constexpr int WIDE_QT = 256, WIDE_STAGES = 5;
 constexpr int NARROW_QT = 64, NARROW_STAGES = 8;
 
 template <int CG, int QT, int STAGES, int DT>
