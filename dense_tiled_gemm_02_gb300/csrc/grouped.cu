@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     const uint32_t sF0 = smem_u32(sF), sX0 = smem_u32(sX);
     const uint32_t full0 = CG == 2 ? map_shared_rank(full(0), 0) : full(0);
     while (next_piece(x)) {
-      if (lane == 0 && !stop) {
+      if (elect_one() && !stop) {
         const int half = ((x.nq + 31) & ~31) / CG;  // this CTA's rows of the tile
         const int q0 = x.q0 + static_cast<int>(rank) * half, f0 = x.f0 + static_cast<int>(rank) * FT;
         const bool big = half > 64;
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       }
       __syncwarp();
     }
-    if (lane == 0) {
+    if (elect_one()) {
       // Copies in flight land before the CTA leaves.  The even CTA's barriers
       // count both CTAs' (after giving up, the odd CTA gives its own time).
       if (leader) {
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     uint32_t s = 0, ph = 0, acc_it = 0;
     bool ok = true;
     while (next_piece(x)) {
-      if (leader && lane == 0 && ok && x.k < x.kend) {
+      if (elect_one() && leader && ok && x.k < x.kend) {
         const uint32_t buf = acc_it & 1u;
         const uint32_t d_tmem = tmem_base + buf * QT;
         const uint32_t idesc = p.idesc | (static_cast<uint32_t>(((x.nq + 31) & ~31) >> 3) << 17);
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       }
       __syncwarp();
     }
-    if (leader && lane == 0) {
+    if (elect_one() && leader) {
       commit<CG>(done_bar);
       drain_wait(done_bar, 0, 200000000ull);
     }

@@ -15,6 +15,22 @@ void* tensor_map_encoder();
 // Status bit beside STATUS_TIMEOUT: offsets or row indices out of range.
 constexpr uint32_t STATUS_BAD_INDEX = 2u;
 
+// True in one lane, always the same, of a converged warp.  The branch of a
+// thread that issues tcgen05 or TMA instructions is taken on this and not on
+// a lane number: the compiler then knows that one thread runs it and keeps
+// the operands in uniform registers, where the instructions read them.
+// (16 tcgen05.mma of 128 x 16 x 16 from tensor memory: 290 cycles to issue
+// against 1780 behind `lane == 0`.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(one));
+  return one != 0u;
+}
+
 // The rows [lo, hi) of expert e; empty, with the status set, when the offsets
 // decrease or leave [0, R].
 __device__ __forceinline__ int2 expert_rows(const int* offsets, int e, int R, uint32_t* status) {
@@ -117,8 +133,15 @@ struct W4Params {
   const uint8_t* zeros;  // null: 8
   const int* offsets;    // null: all rows to expert 0
   void* D;
+  float* partial;        // tensor-memory form: w4_partial_bytes()
+  unsigned* counters;    // one per block, zero between calls
   uint32_t* status;
+  unsigned long long timeout_ns;
+  int debug_flags;
 };
-cudaError_t launch_w4(const W4Params& p, int num_sms, cudaStream_t st);
+size_t w4_partial_bytes(int num_sms);
+// w: tensor map of the weights (E * N rows of K / 2 bytes, boxes of 128 rows x
+// 128 bytes, swizzled) for the tensor-memory form, null for the warp form.
+cudaError_t launch_w4(const W4Params& p, const CUtensorMap* w, int num_sms, cudaStream_t st);
 
 }  // namespace gb300

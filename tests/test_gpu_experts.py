@@ -16,6 +16,7 @@ import pytest
 import torch
 
 import dense_tiled_gemm_02_gb300 as pkg
+from gpu_helpers import forced_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -82,6 +83,7 @@ def grouped_ref(A, B, off, C, grad):
     return D, S
 
 
+@pytest.mark.parametrize("plan", ["wide=0", "wide=1"])
 @pytest.mark.parametrize("counts", COUNTS)
 @pytest.mark.parametrize("K,N,dtype,out,order,with_c", [
     (64, 128, BF16, BF16, "nk", False),
@@ -93,7 +95,7 @@ def grouped_ref(A, B, off, C, grad):
     (1, 1, BF16, F16, "nk", False),
     (8, 8, BF16, BF16, "kn", False),
 ])
-def test_grouped_rows(counts, K, N, dtype, out, order, with_c):
+def test_grouped_rows(plan, counts, K, N, dtype, out, order, with_c):
     counts = COUNTS[counts]
     E, R = len(counts), sum(counts)
     off = offsets_of(counts)
@@ -102,13 +104,15 @@ def test_grouped_rows(counts, K, N, dtype, out, order, with_c):
     B = B.transpose(1, 2) if order == "nk" else B
     C = rnd((R, N), out, 3) if with_c else None
     D = torch.full((R, N), 7.0, dtype=out, device="cuda")
-    op = pkg.GroupedGemm.like(A, B, off, C, D)
+    with forced_plan(plan):
+        op = pkg.GroupedGemm.like(A, B, off, C, D)
     op.run(A, B, off, C, D)
     done(op)
     ref, S = grouped_ref(A, B, off, C, False)
     near(D, ref, S, K + 1)
 
 
+@pytest.mark.parametrize("plan", ["wide=0", "wide=1"])
 @pytest.mark.parametrize("counts", COUNTS)
 @pytest.mark.parametrize("K,N,dtype,out,with_c", [
     (64, 128, BF16, BF16, False),
@@ -117,23 +121,25 @@ def test_grouped_rows(counts, K, N, dtype, out, order, with_c):
     (33, 61, BF16, BF16, False),
     (1, 300, F16, F32, False),
 ])
-def test_grouped_grad(counts, K, N, dtype, out, with_c):
+def test_grouped_grad(plan, counts, K, N, dtype, out, with_c):
     counts = COUNTS[counts]
     E, R = len(counts), sum(counts)
     off = offsets_of(counts)
     A, B = rnd((max(R, 1), K), dtype, 1)[:R], rnd((max(R, 1), N), dtype, 2)[:R]
     C = rnd((E, K, N), out, 3) if with_c else None
     D = torch.full((E, K, N), 7.0, dtype=out, device="cuda")
-    op = pkg.GroupedGemm.like(A, B, off, C, D)
+    with forced_plan(plan):
+        op = pkg.GroupedGemm.like(A, B, off, C, D)
     op.run(A, B, off, C, D)
     done(op)
     ref, S = grouped_ref(A, B, off, C, True)
     near(D, ref, S, max(counts) + 1)
 
 
+@pytest.mark.parametrize("plan", ["wide=0", "wide=1"])
 @pytest.mark.parametrize("grad", [False, True])
 @pytest.mark.parametrize("K,N", [(96, 136), (40, 300)])
-def test_grouped_rows_outside_and_nan_neighbours(grad, K, N):
+def test_grouped_rows_outside_and_nan_neighbours(plan, grad, K, N):
     """Rows before offsets[0] and past offsets[E] are NaN, as are the whole
     of expert 1 and the padding of every stride: no NaN reaches the others,
     and no row or column outside D is written."""
@@ -162,7 +168,8 @@ def test_grouped_rows_outside_and_nan_neighbours(grad, K, N):
         B[1] = nan
         whole = torch.full((R, N + pad), 7.0, dtype=BF16, device="cuda")
     D = whole[..., :N]
-    op = pkg.GroupedGemm.like(A, B, off, None, D)
+    with forced_plan(plan):
+        op = pkg.GroupedGemm.like(A, B, off, None, D)
     op.run(A, B, off, None, D)
     done(op)
     ref, S = grouped_ref(torch.nan_to_num(A), torch.nan_to_num(B), off, None, grad)
@@ -198,6 +205,29 @@ def test_grouped_k_zero_and_c_in_place():
     done(op)
     ref, S = grouped_ref(A, B, off, None, True)
     near(D, 2 * ref, 2 * S, 8)
+
+
+@pytest.mark.parametrize("plan", ["wide=0", "wide=1"])
+@pytest.mark.parametrize("grad", [False, True])
+def test_grouped_long_sums_are_shared_between_units(plan, grad):
+    """Fewer tiles than units and a long sum: its pieces are added in one
+    order, whoever is last, so every call gives the same bits."""
+    counts = [3000, 0, 1111] if grad else [70, 0, 300]
+    R, K, N = sum(counts), (96 if grad else 5000), 200
+    off = offsets_of(counts)
+    A = rnd((R, K), BF16, 1)
+    B = rnd((R, N) if grad else (3, K, N), BF16, 2)
+    D = torch.zeros((3, K, N) if grad else (R, N), device="cuda")
+    with forced_plan(plan):
+        op = pkg.GroupedGemm.like(A, B, off, None, D)
+    op.run(A, B, off, None, D)
+    ref, S = grouped_ref(A, B, off, None, grad)
+    near(D, ref, S, max(counts) if grad else K)
+    first = D.clone()
+    for _ in range(5):
+        op.run(A, B, off, None, D)
+        assert torch.equal(D, first)
+    done(op)
 
 
 def test_grouped_long_groups_and_many_experts():
@@ -325,6 +355,7 @@ def w4_ref(X, q, scales, zeros, off, group):
     return D, S
 
 
+@pytest.mark.parametrize("plan", ["tc=0", "tc=1"])
 @pytest.mark.parametrize("R", [1, 3, 8, 9, 16, 17, 32, 45])
 @pytest.mark.parametrize("K,N,group,dtype,scale,out,zeros", [
     (128, 64, 128, BF16, BF16, BF16, False),
@@ -335,7 +366,7 @@ def w4_ref(X, q, scales, zeros, off, group):
     (32, 130, 32, F16, F32, BF16, False),
     (96, 40, 128, BF16, BF16, BF16, True),   # less than one group
 ])
-def test_w4_dense(R, K, N, group, dtype, scale, out, zeros):
+def test_w4_dense(plan, R, K, N, group, dtype, scale, out, zeros):
     G = -(-K // group)
     g = torch.Generator().manual_seed(R + K)
     q = torch.randint(0, 16, (1, N, K), generator=g).cuda()
@@ -343,17 +374,59 @@ def test_w4_dense(R, K, N, group, dtype, scale, out, zeros):
     s = (rnd((1, N, G), F32, 2).abs() * 0.1 + 0.01).to(scale)
     z = torch.randint(0, 16, (1, N, G), generator=g).to(torch.uint8).cuda() if zeros else None
     D = torch.full((R, N), 7.0, dtype=out, device="cuda")
-    op = pkg.W4Gemm.like(X, W, s, z, None, D, group)
+    with forced_plan(plan):
+        op = pkg.W4Gemm.like(X, W, s, z, None, D, group)
+    assert plan in op.plan()
     op.run(X, W, s, z, None, D)
     done(op)
     ref, S = w4_ref(X, q, s, z, None, group)
     near(D, ref, S, K + 1)
 
 
+def test_w4_long_sums_are_shared_between_blocks():
+    """More blocks than tiles: each tile's sum over K is split, and the same
+    bits come back from every call."""
+    R, K, N, group = 5, 16384, 300, 64
+    q = torch.randint(0, 16, (1, N, K), generator=torch.Generator().manual_seed(2)).cuda()
+    W, X = pkg.pack_w4(q), rnd((R, K), BF16, 1)
+    s = (rnd((1, N, K // group), F32, 2).abs() * 0.1 + 0.01).to(BF16)
+    D = torch.zeros((R, N), device="cuda")
+    with forced_plan("tc=1"):
+        op = pkg.W4Gemm.like(X, W, s, None, None, D, group)
+    op.run(X, W, s, None, None, D)
+    ref, S = w4_ref(X, q, s, None, None, group)
+    near(D, ref, S, K + 1)
+    first = D.clone()
+    for _ in range(5):
+        op.run(X, W, s, None, None, D)
+        assert torch.equal(D, first)
+    done(op)
+
+
+def test_w4_bounded_wait_reports_timeout_and_stays_usable():
+    K, N, group = 1024, 256, 128
+    q = torch.randint(0, 16, (1, N, K), generator=torch.Generator().manual_seed(3)).cuda()
+    W, X = pkg.pack_w4(q), rnd((2, K), BF16, 1)
+    s = torch.ones((1, N, K // group), dtype=BF16, device="cuda")
+    D = torch.zeros((2, N), dtype=BF16, device="cuda")
+    with forced_plan("tc=1"):
+        op = pkg.W4Gemm.like(X, W, s, None, None, D, group)
+    op.debug_set(pkg.GEMM_DEBUG_SKIP_FIRST_FILL, 50_000_000)
+    op.run(X, W, s, None, None, D)
+    assert op.status() == pkg.GEMM_ERR_DEVICE_TIMEOUT
+    op.debug_set(0)
+    op.run(X, W, s, None, None, D)
+    done(op)
+    ref, S = w4_ref(X, q, s, None, None, group)
+    near(D, ref, S, K + 1)
+
+
+@pytest.mark.parametrize("plan", ["tc=0", "tc=1"])
 @pytest.mark.parametrize("counts", [[0, 1, 0, 2, 0, 0, 9], [1], [3, 0, 40, 17, 0, 1], [0, 0, 0]])
-@pytest.mark.parametrize("K,N,group,zeros", [(256, 72, 64, True), (512, 33, 128, False)])
-def test_w4_experts(counts, K, N, group, zeros):
-    E, first, tail, G = len(counts), 2, 3, K // group
+@pytest.mark.parametrize("K,N,group,zeros", [(256, 72, 64, True), (512, 33, 128, False),
+                                             (544, 130, 32, True)])
+def test_w4_experts(plan, counts, K, N, group, zeros):
+    E, first, tail, G = len(counts), 2, 3, -(-K // group)
     R, off = first + sum(counts) + tail, offsets_of(counts, first)
     g = torch.Generator().manual_seed(K)
     q = torch.randint(0, 16, (E, N, K), generator=g).cuda()
@@ -364,7 +437,8 @@ def test_w4_experts(counts, K, N, group, zeros):
     z = torch.randint(0, 16, (E, N, G), generator=g).to(torch.uint8).cuda() if zeros else None
     whole = torch.full((R, N + 3), 7.0, dtype=BF16, device="cuda")
     D = whole[:, :N]
-    op = pkg.W4Gemm.like(X, W, s, z, off, D, group)
+    with forced_plan(plan):
+        op = pkg.W4Gemm.like(X, W, s, z, off, D, group)
     op.run(X, W, s, z, off, D)
     done(op)
     live = slice(first, first + sum(counts))
@@ -382,11 +456,14 @@ def test_w4_specials_and_bad_offsets():
     W, s = pkg.pack_w4(q), torch.ones((1, N, 1), dtype=BF16, device="cuda")
     X = rnd((3, K), BF16, 1)
     X[0, 5], X[1, 7] = float("inf"), float("nan")
-    D = pkg.w4_matmul(X, W, s)
     inf = float("inf")
     want = torch.where(q[0, :, 5] == 8, float("nan"), torch.where(q[0, :, 5] > 8, inf, -inf))
-    assert torch.equal(torch.nan_to_num(D[0].double(), nan=3.0), torch.nan_to_num(want.double(), nan=3.0))
-    assert bool(torch.isnan(D[1]).all()) and bool(torch.isfinite(D[2]).all())
+    for plan in ("tc=0", "tc=1"):
+        with forced_plan(plan):
+            D = pkg.w4_matmul(X, W, s)
+        assert torch.equal(torch.nan_to_num(D[0].double(), nan=3.0),
+                           torch.nan_to_num(want.double(), nan=3.0))
+        assert bool(torch.isnan(D[1]).all()) and bool(torch.isfinite(D[2]).all())
     off = torch.tensor([0, 9], dtype=torch.int32, device="cuda")
     op = pkg.W4Gemm.like(X, W, s, None, off, D, 128)
     op.run(X, W, s, None, off, D)
