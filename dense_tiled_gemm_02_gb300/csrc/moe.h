@@ -133,15 +133,9 @@ struct W4Params {
   const uint8_t* zeros;  // null: 8
   const int* offsets;    // null: all rows to expert 0
   void* D;
-  float* partial;        // tensor-memory form: w4_partial_bytes()
-  unsigned* counters;    // one per block, zero between calls
   uint32_t* status;
-  unsigned long long timeout_ns;
-  int debug_flags;
+  uint32_t nibbles, nibble_base;  // set by launch_w4 (see expand in w4.cu)
 };
-size_t w4_partial_bytes(int num_sms);
-// w: tensor map of the weights (E * N rows of K / 2 bytes, boxes of 128 rows x
-// 128 bytes, swizzled) for the tensor-memory form, null for the warp form.
-cudaError_t launch_w4(const W4Params& p, const CUtensorMap* w, int num_sms, cudaStream_t st);
+cudaError_t launch_w4(const W4Params& p, cudaStream_t st);
 
 }  // namespace gb300

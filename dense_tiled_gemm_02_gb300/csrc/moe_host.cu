@@ -25,7 +25,6 @@ enum class Kind { kRoute, kPermute, kGrouped, kW4 };
 
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;  // 2 s per device-side wait
 constexpr size_t kStatusBytes = 256;
-constexpr int64_t kW4TensorBytes = 16 << 20;  // weights from which w4 takes its tensor-memory form
 
 bool is_16bit(int t) { return t == T_F16 || t == T_BF16; }
 bool is_float(int t) { return is_16bit(t) || t == T_F32; }
@@ -53,7 +52,7 @@ struct gemm_op {
   int64_t a_rows = 0, a_cols = 0, b_rows = 0, b_cols = 0;
   int64_t ws_lda = 0, ws_ldb = 0;
   size_t ws_b_off = 0, ws_partial_off = 0, ws_counters_off = 0, ws_maps_off = 0;
-  bool wide = false;  // grouped: CTA pairs; w4: the tensor-memory form
+  bool wide = false;
   int units = 0;
   int grid = 0;  // route: blocks
 };
@@ -118,19 +117,19 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Map of a row-major operand of es-byte elements (1 or 2), 128-byte swizzled
-// boxes of box_cols x box_rows, zeros outside.  depth > 0: that many matrices
-// of `rows` rows one after another, as a third dimension.
+// Map of a row-major 16-bit operand, 128-byte swizzled boxes of box_cols x
+// box_rows, zeros outside.  depth > 0: that many matrices of `rows` rows one
+// after another, as a third dimension.
 bool encode_rows(CUtensorMap* tm, const void* base, int64_t ld, int64_t cols, int64_t rows,
-                 int64_t depth, int box_cols, int box_rows, int es = 2) {
+                 int64_t depth, int box_cols, int box_rows) {
   EncodeFn enc = reinterpret_cast<EncodeFn>(tensor_map_encoder());
   if (!enc) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
-  const cuuint64_t strides[2] = {(cuuint64_t)(ld * es), (cuuint64_t)(ld * rows * es)};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(ld * rows) * 2};
   const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(tm, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
-             depth > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, depth > 0 ? 3 : 2, const_cast<void*>(base), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -532,26 +531,13 @@ int gemm_w4_create(gemm_op_t* out, const gemm_w4_desc_t* desc) {
     return GEMM_ERR_UNSUPPORTED;
   if (d.ldx % 8 != 0) return GEMM_ERR_MISALIGNED;
   gemm_op* op = nullptr;
-  // The tensor-memory form's start (tensor memory, rings, the exchange of
-  // partial sums) takes about 4 us longer than the warp form's, which streams
-  // the weights at about half the speed.
-  const int64_t active = std::min<int64_t>(d.E, d.R);
-  const bool tc = d.K > 0 && d.N > 0 && d.R > 0 && d.E * d.N < INT_MAX &&
-                  planned("tc", active * d.N * d.K / 2 >= kW4TensorBytes);
-  int sms = 0, dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    cudaGetLastError();
-  const size_t partial = tc ? w4_partial_bytes(sms) : 0;
-  const int rc = make_op(Kind::kW4, partial + (tc ? 4 * static_cast<size_t>(sms) : 0), &op);
+  const int rc = make_op(Kind::kW4, 0, &op);
   if (rc != GEMM_OK) return rc;
   op->w4 = d;
-  op->wide = tc;
-  op->ws_counters_off = partial;
   char buf[160];
-  std::snprintf(buf, sizeof buf, "w4 E=%d R=%lld K=%lld N=%lld group=%d zeros=%d tc=%d", d.E,
+  std::snprintf(buf, sizeof buf, "w4 E=%d R=%lld K=%lld N=%lld group=%d zeros=%d", d.E,
                 static_cast<long long>(d.R), static_cast<long long>(d.K),
-                static_cast<long long>(d.N), d.group, d.has_zeros != 0, tc);
+                static_cast<long long>(d.N), d.group, d.has_zeros != 0);
   op->plan = buf;
   *out = op;
   return GEMM_OK;
@@ -587,17 +573,7 @@ int gemm_w4_run(gemm_op_t op, const void* X, const uint8_t* W, const void* scale
   p.offsets = offsets;
   p.D = D;
   p.status = op->status;
-  p.timeout_ns = op->timeout_ns;
-  p.debug_flags = op->debug_flags;
-  op->debug_flags = 0;
-  CUtensorMap w{};
-  if (op->wide) {
-    p.partial = static_cast<float*>(op->ws);
-    p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(op->ws) + op->ws_counters_off);
-    if (!encode_rows(&w, W, d.K / 2, d.K / 2, d.E * d.N, 0, 128, 128, 1)) return GEMM_ERR_CUDA;
-  }
-  return launched(launch_w4(p, op->wide ? &w : nullptr, op->num_sms,
-                            static_cast<cudaStream_t>(stream)));
+  return launched(launch_w4(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -404,9 +404,8 @@ GEMM_API int gemm_trace_set(gemm_handle_t h, uint64_t* dev_buf);
  * operator or of another device than the current one),
  * GEMM_ERR_MISALIGNED or GEMM_ERR_CUDA.
  *
- * GEMM_FORCE_PLAN (read by the create calls, for tests and tuning) takes two
- * more keys: wide=0|1, the grouped product's single CTAs or CTA pairs, and
- * tc=0|1, the 4-bit product's warp-level or tensor-memory form.
+ * GEMM_FORCE_PLAN (read by the create calls, for tests and tuning) takes one
+ * more key: wide=0|1, the grouped product's single CTAs or CTA pairs.
  *
  * Experts are numbered 0 .. E-1, E <= GEMM_MAX_EXPERTS.  Rows sorted by
  * expert are described by `offsets`, E + 1 int32 values in device memory:
