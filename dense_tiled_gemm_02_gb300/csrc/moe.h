@@ -53,8 +53,8 @@ struct RouteParams {
   int* row_slot;
   int* slot_row;
   int blocks, tokens_per_block;  // several-block form
-  int* hist;                     // [blocks][E]: counts, then each block's first row per expert
-  unsigned* ticket;              // zero between calls
+  int* hist;                     // [blocks][ld_hist]: the blocks' slots of each expert
+  int ld_hist;                   // E up to a multiple of four
 };
 // Blocks of the forward kernel; 1: one block does the whole call.
 int route_blocks(long long T, int k, int num_sms);
@@ -68,6 +68,7 @@ struct RouteBackwardParams {
   const float* gates;
   const float* dgates;
   void* dlogits;
+  int num_sms;
 };
 cudaError_t launch_route_backward(const RouteBackwardParams& p, cudaStream_t st);
 

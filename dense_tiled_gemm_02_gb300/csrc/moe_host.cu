@@ -190,7 +190,7 @@ int gemm_route_create(gemm_op_t* out, const gemm_route_desc_t* desc) {
   cudaGetLastError();
   const int blocks = route_blocks(d.T, d.k, std::max(sms, 1));
   gemm_op* op = nullptr;
-  const size_t ws = blocks > 1 ? 256 + sizeof(int) * static_cast<size_t>(blocks) * d.E : 0;
+  const size_t ws = blocks > 1 ? sizeof(int) * static_cast<size_t>(blocks) * up(d.E, 4) : 0;
   const int rc = make_op(Kind::kRoute, ws, &op);
   if (rc != GEMM_OK) return rc;
   op->route = d;
@@ -227,8 +227,8 @@ int gemm_route_run(gemm_op_t op, const void* logits, int32_t* experts, float* ga
   p.slot_row = slot_row;
   p.blocks = op->grid;
   p.tokens_per_block = static_cast<int>((d.T + op->grid - 1) / op->grid);
-  p.ticket = static_cast<unsigned*>(op->ws);
-  p.hist = reinterpret_cast<int*>(static_cast<uint8_t*>(op->ws) + 256);
+  p.hist = static_cast<int*>(op->ws);
+  p.ld_hist = static_cast<int>(up(d.E, 4));
   return launched(launch_route(p, st));
 }
 
@@ -254,6 +254,7 @@ int gemm_route_backward(gemm_op_t op, const void* logits, const int32_t* experts
   p.gates = gates;
   p.dgates = dgates;
   p.dlogits = dlogits;
+  p.num_sms = op->num_sms;
   return launched(launch_route_backward(p, static_cast<cudaStream_t>(stream)));
 }
 
