@@ -135,6 +135,7 @@ struct W4Params {
   const int* offsets;    // null: all rows to expert 0
   void* D;
   uint32_t* status;
+  int num_sms;
   uint32_t nibbles, nibble_base;  // set by launch_w4 (see expand in w4.cu)
 };
 cudaError_t launch_w4(const W4Params& p, cudaStream_t st);

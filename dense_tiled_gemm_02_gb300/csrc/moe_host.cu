@@ -574,6 +574,7 @@ int gemm_w4_run(gemm_op_t op, const void* X, const uint8_t* W, const void* scale
   p.offsets = offsets;
   p.D = D;
   p.status = op->status;
+  p.num_sms = op->num_sms;
   return launched(launch_w4(p, static_cast<cudaStream_t>(stream)));
 }
 

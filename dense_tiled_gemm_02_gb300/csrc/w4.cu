@@ -23,18 +23,26 @@
 // 16-row tiles, and add their sums in shared memory in warp order:
 // deterministic.
 //
-// Measured (one GB300): 4 x 8192 x 32768, groups of 128: 44 us (3.2 TB/s; the
-// weights alone, without the arithmetic, take 34 this way), 16 x 8192 x 8192,
-// groups of 64: 21 us (45 with X loaded for every 16 rows), 64 rows over 40 experts of 4096 x 2048: 56 us.  What bounds it
-// is the time between a run's loads and its arithmetic, with 16 warps an SM
-// to cover it.  Measured against it on the same cases: the weights expanded
-// into tensor memory for tcgen05.mma (48, 29 and 64 us: four hand-overs a
-// stage of 16 KB cost more than the instructions saved), X in registers for
-// good with the weights through a bulk-copied ring (67, 31 and 101 us), and
-// a ring of asynchronous copies per warp (43, 33 and 66 us).
+// Measured (one GB300): 4 x 8192 x 32768, groups of 128: 39 us (3.5 TB/s),
+// 16 x 8192 x 8192, groups of 64: 21 us (45 with X loaded for every 16 rows),
+// 64 rows over 40 experts of 4096 x 2048: 49 us.  No unit is more than half
+// busy (logic 49%, L1 47%, issue 40% at the first case; the loads alone, with
+// as many in flight, run at 6.2 TB/s): what bounds it is the time between a
+// run's loads and its arithmetic, with 16 warps an SM to cover it.  Measured
+// against it on the same cases: a run's loads a run ahead in registers, by
+// blocks that stay (55, 26 and 67 us: the registers of the second run cost as
+// many instructions as the loads took), 24 and 32 warps an SM with half the
+// loads each (50 and 56 us for the first case), four weight tiles against one
+// X (48, 39 and 61), the weights expanded into tensor memory for tcgen05.mma
+// (48, 29 and 64: four hand-overs a stage of 16 KB cost more than the
+// instructions saved), X in registers for good with the weights through a
+// bulk-copied ring (67, 31 and 101), and a ring of asynchronous copies per
+// warp (43, 33 and 66).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "moe.h"
 #include "ptx.cuh"
@@ -44,8 +52,8 @@ namespace gb300 {
 
 namespace {
 
-constexpr int WARPS = 8;
-constexpr int THREADS = 32 * WARPS;
+constexpr int SM_WARPS = 16;  // resident, by the registers
+
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -93,9 +101,7 @@ __device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t base_plus
 
 template <int WPT>
 __device__ __forceinline__ void load_words(const uint8_t* p, bool ok, uint32_t (&w)[WPT]) {
-#pragma unroll
-  for (int i = 0; i < WPT; ++i) w[i] = 0u;
-  if (!ok) return;
+  if (!ok) return;  // what was there meets zeros of X
   if constexpr (WPT == 4) {
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
@@ -131,7 +137,7 @@ __device__ __forceinline__ void store_d(void* d, int type, long long i, float v)
 __device__ __forceinline__ int nth_expert(const W4Params& p, int y) {
   __shared__ uint32_t words[32];
   const int nw = (p.E + 31) / 32;
-  for (int e0 = threadIdx.x & ~31; e0 < 32 * nw; e0 += THREADS) {
+  for (int e0 = threadIdx.x & ~31; e0 < 32 * nw; e0 += blockDim.x) {
     const int e = e0 + (threadIdx.x & 31);
     bool any = false;
     if (e < p.E) {
@@ -156,12 +162,17 @@ constexpr int RT = 2;  // 16-row weight tiles a warp takes against one X
 template <int WPT, int NT>
 constexpr int kRun = WPT * NT >= 8 ? 1 : (8 / (WPT * NT) > 4 ? 4 : 8 / (WPT * NT));  // steps of a run
 
+// Most warps of a block (the sums of all of them in shared memory).
+template <int NT>
+constexpr int kMaxWarps = NT == 4 ? 8 : SM_WARPS;
+
 template <bool BF16, int WPT, int NT>
-__global__ void __launch_bounds__(THREADS, 2) w4_kernel(const W4Params p) {
+__global__ void __launch_bounds__(32 * kMaxWarps<NT>, SM_WARPS / kMaxWarps<NT>)
+    w4_kernel(const W4Params p) {
   constexpr int SPAN = 32 * WPT;  // K of one step
   constexpr int U = kRun<WPT, NT>;
-  __shared__ float red[WARPS][16 * RT][8 * NT + 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float red[kMaxWarps<NT>][16 * RT][8 * NT + 1];
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t mask = p.nibbles, base = p.nibble_base;
   pdl_wait();
@@ -175,13 +186,12 @@ __global__ void __launch_bounds__(THREADS, 2) w4_kernel(const W4Params p) {
     r1 = r.y;
   }
   const int n0 = blockIdx.x * 16 * RT;
-  // this thread's first weight row; rows past N read row 0 of the tile's
-  // place and are not stored
-  const long long row0 = static_cast<long long>(e) * p.N;
-  auto row_of = [&](int i, int h) {
-    const int n = n0 + 16 * i + 8 * h + g;
-    return row0 + (n < p.N ? n : 0);
-  };
+  // this thread's first weight row, and how far on the others are; rows past
+  // N read the first again and are not stored
+  const int left = p.N - n0 - g;
+  const long long row0 = static_cast<long long>(e) * p.N + n0 + (left > 0 ? g : 0);
+  const uint8_t* const w0 = p.W + row0 * (p.K / 2) + 4 * WPT * t;
+  auto rows_on = [&](int i, int h) { return 16 * i + 8 * h < left ? 16 * i + 8 * h : 0; };
   const int steps = (p.K + SPAN - 1) / SPAN;
   const int group_steps = p.group / SPAN;  // steps that share a scale
   for (int rb = r0; rb < r1; rb += 8 * NT) {
@@ -190,12 +200,13 @@ __global__ void __launch_bounds__(THREADS, 2) w4_kernel(const W4Params p) {
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
-    for (int s0 = warp * U; s0 < steps; s0 += WARPS * U) {
-      uint32_t w[2][U][2][WPT];
+    for (int s0 = warp * U; s0 < steps; s0 += warps * U) {
+      uint32_t w[2][U][2][WPT] = {};
       auto load_tile = [&](int i, uint32_t (&o)[U][2][WPT]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint8_t* const src = p.W + row_of(i, h) * (p.K / 2) + s0 * (SPAN / 2) + 4 * WPT * t;
+          const uint8_t* const src =
+              w0 + static_cast<long long>(rows_on(i, h)) * (p.K / 2) + s0 * (SPAN / 2);
 #pragma unroll
           for (int u = 0; u < U; ++u)
             load_words<WPT>(src + u * (SPAN / 2), (s0 + u) * SPAN + 8 * WPT * t < p.K, o[u][h]);
@@ -210,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, 2) w4_kernel(const W4Params p) {
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const long long at = row_of(i, h) * p.groups + G;
+          const long long at = row0 * p.groups + (rows_on(i, h) * p.groups + G);
           sc[i][h] = scale_bits(p.scales, p.scale_type, at);
           z[i][h] = p.zeros ? p.zeros[at] : 8u;
         }
@@ -278,12 +289,11 @@ __global__ void __launch_bounds__(THREADS, 2) w4_kernel(const W4Params p) {
         for (int q = 0; q < 4; ++q)
           red[warp][16 * i + g + 8 * (q >> 1)][8 * j + 2 * t + (q & 1)] = acc[i][j][q];
     __syncthreads();
-    for (int o = threadIdx.x; o < 16 * RT * 8 * NT; o += THREADS) {
+    for (int o = threadIdx.x; o < 16 * RT * 8 * NT; o += blockDim.x) {
       const int n = o % (16 * RT), m = o / (16 * RT);
       if (rb + m < r1 && n0 + n < p.N) {
         float v = 0.f;
-#pragma unroll
-        for (int x = 0; x < WARPS; ++x) v += red[x][n][m];
+        for (int x = 0; x < warps; ++x) v += red[x][n][m];
         store_d(p.D, p.d_type, (rb + m) * p.ldd + n0 + n, v);
       }
     }
@@ -292,8 +302,19 @@ __global__ void __launch_bounds__(THREADS, 2) w4_kernel(const W4Params p) {
 
 template <bool BF16, int WPT, int NT>
 cudaError_t launch_as(const W4Params& p, cudaStream_t st) {
-  const dim3 grid((p.N + 16 * RT - 1) / (16 * RT), p.E > 1 ? min(p.E, p.R) : 1);
-  return launch_pdl(w4_kernel<BF16, WPT, NT>, grid, dim3(THREADS), 0, st, p);
+  const int tiles = (p.N + 16 * RT - 1) / (16 * RT), experts = p.E > 1 ? std::min(p.E, p.R) : 1;
+  const int run = 32 * WPT * kRun<WPT, NT>, runs = (p.K + run - 1) / run;
+  // Warps that share a tile's K.  Few make better use of an SM, since its
+  // blocks then wait for one another's loads and sums less (4 against 8 warps:
+  // 4 x 8192 x 32768 39.4 against 42.4 us, 64 x 2048 x 1024 over 40 experts
+  // 16.6 against 18.9; 2 against 4 at K = 1024: 16.9 against 17.9), but where
+  // the tiles are few the SMs would be half empty (8 against 4: 16 x 8192 x
+  // 8192 20.9 against 27.5; 16 against 8: 1 x 4096 x 4096 5.2 against 5.7).
+  int warps = runs <= 4 ? 2 : 4;
+  while (warps < kMaxWarps<NT> && warps < runs &&
+         2ll * tiles * experts * warps < SM_WARPS * p.num_sms)
+    warps *= 2;
+  return launch_pdl(w4_kernel<BF16, WPT, NT>, dim3(tiles, experts), dim3(32 * warps), 0, st, p);
 }
 
 template <bool BF16, int WPT>
