@@ -9,8 +9,9 @@
 // The forward pass must read T x E logits once and write 20 bytes a slot: at
 // 32768 x 256, k = 8, fp32, 5.8 us of traffic.  The k rounds of a warp-wide
 // maximum bound it, not HBM: 23.7 us (1.6 TB/s), instructions issued in 64% of
-// the cycles; the sort takes 10-15 us more and the backward pass 11.7 us
-// (3.2 TB/s: latency of the choices, then a store of the row).  A warp
+// the cycles; the sort takes about 7 us more and the backward pass 8 us (a
+// token to a warp, with a trip of its own for its choices, took 11.7), 38.7
+// together.  A warp
 // owns a token: lane l holds the logits e = 32 i + l as order-preserving
 // 32-bit keys and its own largest; a round takes the warp's largest key (one
 // warp reduction) and, where several lanes hold it, the lowest expert, and
@@ -416,10 +417,15 @@ __global__ void __launch_bounds__(RANK_THREADS) route_rank_kernel(const RoutePar
     count_slots(now, p.k, p.E, cnt, expert);
     for (int e = threadIdx.x; e < p.E; e += RANK_THREADS) {
       int at = base[e];
-      for (int w = 0; w < WARPS; ++w) {
-        const int c = cnt[w * p.E + e];
-        cnt[w * p.E + e] = at;
-        at += c;
+      for (int w0 = 0; w0 < WARPS; w0 += 8) {
+        int c[8];  // read together, as none depends on a store before it
+#pragma unroll
+        for (int w = 0; w < 8; ++w) c[w] = cnt[(w0 + w) * p.E + e];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          cnt[(w0 + w) * p.E + e] = at;
+          at += c[w];
+        }
       }
       base[e] = at;
     }
@@ -430,70 +436,76 @@ __global__ void __launch_bounds__(RANK_THREADS) route_rank_kernel(const RoutePar
     if (t0 * p.k + i >= first[p.E]) p.row_slot[t0 * p.k + i] = -1;
 }
 
-// A warp takes a token at a time: its row is written whole, then its k chosen
-// entries (stores of one warp to one address stay in order across
-// __syncwarp).  The next token's choices are on their way meanwhile.
+// A warp takes 32 / K tokens together, K the power of two that holds k: lane
+// K i + j has choice j of the i-th, so all their choices come in one trip and
+// one butterfly sums each token's.  Then it writes their rows whole, one after
+// the other, and last all chosen entries (stores of one warp to one address
+// stay in order across __syncwarp).  VPL: 0 for normalized gates, where the
+// rest of a row is zeros.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(256) route_backward_kernel(const RouteBackwardParams p) {
-  const int lane = threadIdx.x & 31, stride = gridDim.x * 8;
-  long long t = blockIdx.x * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(256, VPL == 0 ? 6 : 1)
+    route_backward_kernel(const RouteBackwardParams p) {
+  const int lane = threadIdx.x & 31;
+  const int K = p.k <= 1 ? 1 : 1 << (32 - __clz(p.k - 1));
+  const int per = 32 / K, mine = lane / K, j = lane & (K - 1);
   pdl_wait();
   pdl_trigger();
   // 16-byte zeros where the rows allow it
   constexpr int V = 16 / sizeof(T);
-  const bool wide = p.normalize && p.E % V == 0 && p.ld % V == 0 &&
+  const bool wide = p.E % V == 0 && p.ld % V == 0 &&
                     (reinterpret_cast<uintptr_t>(p.dlogits) & 15u) == 0;
-  int e = -1;
-  float g = 0.f, dg = 0.f;
-  auto ask = [&](long long token) {
-    e = -1;
-    g = dg = 0.f;
-    if (token < p.T && lane < p.k) {
-      const long long at = token * p.k + lane;
-      e = p.experts[at];
-      g = p.gates[at];
-      dg = p.dgates[at];
+  T* const dlogits = static_cast<T*>(p.dlogits);
+  const long long stride = static_cast<long long>(gridDim.x) * 8 * per;
+  for (long long t0 = (blockIdx.x * 8ll + (threadIdx.x >> 5)) * per; t0 < p.T; t0 += stride) {
+    const long long t = t0 + mine;
+    int chosen = -1;
+    float gate = 0.f, dgate = 0.f;
+    if (t < p.T && j < p.k) {
+      const long long at = t * p.k + j;
+      chosen = p.experts[at];
+      gate = p.gates[at];
+      dgate = p.dgates[at];
     }
-  };
-  ask(t);
-  for (; t < p.T; t += stride) {
-    const int chosen = e >= p.E ? -1 : e;
-    const float gate = chosen >= 0 ? g : 0.f, dgate = chosen >= 0 ? dg : 0.f;
-    ask(t + stride);
-    const float s = warp_sum(gate * dgate);
-    T* const dx = static_cast<T*>(p.dlogits) + t * p.ld;
-    if (wide) {
-      for (int i = V * lane; i < p.E; i += 32 * V)
-        *reinterpret_cast<uint4*>(dx + i) = make_uint4(0u, 0u, 0u, 0u);
-    } else if (p.normalize) {
-      T zero;
-      narrow(0.f, zero);
+    if (chosen < 0 || chosen >= p.E) {
+      chosen = -1;
+      gate = dgate = 0.f;
+    }
+    float s = gate * dgate;
+    for (int d = K / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    for (int q = 0; q < per && t0 + q < p.T; ++q) {
+      T* const dx = dlogits + (t0 + q) * p.ld;
+      if constexpr (VPL == 0) {
+        if (wide) {
+          for (int i = V * lane; i < p.E; i += 32 * V)
+            *reinterpret_cast<uint4*>(dx + i) = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+          for (int i = lane; i < p.E; i += 32) narrow(0.f, dx[i]);
+        }
+      } else {
+        const float sum = __shfl_sync(0xFFFFFFFFu, s, q * K);
+        uint32_t key[VPL];
+        T row[VPL];
+        load_row<T, VPL>(static_cast<const T*>(p.logits) + (t0 + q) * p.ld, p.E, lane, row);
+        to_keys<T, VPL>(row, key);
+        uint32_t m = key[0];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (32 * i + lane < p.E) dx[32 * i + lane] = zero;
-    } else {
-      uint32_t key[VPL];
-      T row[VPL];
-      load_row<T, VPL>(static_cast<const T*>(p.logits) + t * p.ld, p.E, lane, row);
-      to_keys<T, VPL>(row, key);
-      uint32_t m = key[0];
+        for (int i = 1; i < VPL; ++i) m = max(m, key[i]);
+        const float top = key_value(__reduce_max_sync(0xFFFFFFFFu, m));
+        float ex[VPL], z = 0.f;
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) m = max(m, key[i]);
-      const float top = key_value(__reduce_max_sync(0xFFFFFFFFu, m));
-      float ex[VPL], z = 0.f;
+        for (int i = 0; i < VPL; ++i) {
+          ex[i] = key[i] > KEY_NEG_INF ? expf(key_value(key[i]) - top) : 0.f;
+          z += ex[i];
+        }
+        z = warp_sum(z);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        ex[i] = key[i] > KEY_NEG_INF ? expf(key_value(key[i]) - top) : 0.f;
-        z += ex[i];
+        for (int i = 0; i < VPL; ++i)
+          if (32 * i + lane < p.E)
+            narrow(key[i] > KEY_NEG_INF ? -(ex[i] / z) * sum : 0.f, dx[32 * i + lane]);
       }
-      z = warp_sum(z);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (32 * i + lane < p.E)
-          narrow(key[i] > KEY_NEG_INF ? -(ex[i] / z) * s : 0.f, dx[32 * i + lane]);
     }
     __syncwarp();
-    if (chosen >= 0) narrow(gate * (dgate - s), dx[chosen]);
+    if (chosen >= 0) narrow(gate * (dgate - s), dlogits[t * p.ld + chosen]);
     __syncwarp();
   }
 }
@@ -513,9 +525,12 @@ cudaError_t launch_fwd(const RouteParams& p, cudaStream_t st) {
 
 template <typename T, int VPL>
 cudaError_t launch_bwd(const RouteBackwardParams& p, cudaStream_t st) {
-  // at most as many blocks as are resident together
-  const int blocks = std::min((p.T + 7) / 8, 6 * p.num_sms);
-  return launch_pdl(route_backward_kernel<T, VPL>, dim3(blocks), dim3(256), 0, st, p);
+  int per = 32;  // tokens of a warp
+  while (per > 1 && per * p.k > 32) per /= 2;
+  const long long blocks = (p.T + 8ll * per - 1) / (8 * per);
+  return launch_pdl(route_backward_kernel<T, VPL>,
+                    dim3(static_cast<unsigned>(std::min<long long>(blocks, 6ll * p.num_sms))),
+                    dim3(256), 0, st, p);
 }
 
 template <typename T>
@@ -530,6 +545,7 @@ cudaError_t fwd_by_width(const RouteParams& p, cudaStream_t st) {
 
 template <typename T>
 cudaError_t bwd_by_width(const RouteBackwardParams& p, cudaStream_t st) {
+  if (p.normalize) return launch_bwd<T, 0>(p, st);
 #define GB_ROUTE(V) \
   if (p.E <= 32 * V) return launch_bwd<T, V>(p, st);
   GB_ROUTE(1) GB_ROUTE(2) GB_ROUTE(4) GB_ROUTE(8) GB_ROUTE(16) GB_ROUTE(32)

@@ -677,3 +677,18 @@ def test_expert_layer_matches_the_dense_formula():
                  + 2.0 ** -14 * mag).all())
     for op in (route, perm, out):
         done(op)
+
+
+def test_route_nan_of_either_sign_comes_first():
+    x = torch.zeros((3, 40))
+    x[0, 7], x[0, 31] = float("nan"), float("inf")
+    x[1, 39] = torch.tensor(-0x400000, dtype=torch.int32).view(F32)  # NaN with its sign bit set
+    x[1, 2] = 3.0
+    x[2] = float("nan")
+    for dtype in (F32, F16, BF16):
+        op = pkg.Route.like(x.to(dtype).cuda(), 2)
+        outs = op.outputs()
+        op.run(x.to(dtype).cuda(), *outs)
+        done(op)
+        assert outs[0].tolist() == [[7, 31], [39, 2], [0, 1]]
+        assert bool(torch.isnan(outs[1][2]).all())
