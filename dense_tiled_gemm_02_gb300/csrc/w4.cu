@@ -29,7 +29,8 @@
 // busy (logic 49%, L1 47%, issue 40% at the first case; the loads alone, with
 // as many in flight, run at 6.2 TB/s): what bounds it is the time between a
 // run's loads and its arithmetic, with 16 warps an SM to cover it (the
-// next run's first tile on its way during this run's second: no gain, 39.8).  Measured
+// next run's first tile on its way during this run's second: no gain, 39.8;
+// the scales of eight steps by one load a row: 39.1, 19.9 and 50.4).  Measured
 // against it on the same cases: a run's loads a run ahead in registers, by
 // blocks that stay (55, 26 and 67 us: the registers of the second run cost as
 // many instructions as the loads took), 24 and 32 warps an SM with half the

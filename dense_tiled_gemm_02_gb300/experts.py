@@ -58,16 +58,18 @@ def _stack_stride(t: torch.Tensor, what: str) -> int:
 class _Planned:
     """What a tensor argument must look like: shape, dtype and (for
     dimensions longer than one) strides."""
-    __slots__ = ("name", "shape", "dtype", "stride", "device")
+    __slots__ = ("name", "shape", "dtype", "stride", "device", "index", "packed")
 
     def __init__(self, name: str, t: torch.Tensor, device=None):
         self.name, self.shape, self.dtype, self.stride = name, t.shape, t.dtype, t.stride()
         self.device = device or t.device
+        self.index, self.packed = self.device.index, t.is_contiguous()
 
     def pointer(self, t: torch.Tensor) -> int:
-        # the usual case first: this runs for every operand of every call
-        if (t.shape == self.shape and t.dtype is self.dtype and t.stride() == self.stride and
-                t.device == self.device):
+        # The usual case first, by the cheapest calls: this runs for every
+        # operand of every call, and half of a decode step's calls is this.
+        if (t.shape == self.shape and t.dtype is self.dtype and t.get_device() == self.index and
+                (t.is_contiguous() if self.packed else t.stride() == self.stride)):
             return t.data_ptr()
         if (t.shape != self.shape or t.dtype is not self.dtype or t.device != self.device or
                 any(n > 1 and a != b for n, a, b in zip(t.shape, t.stride(), self.stride))):
