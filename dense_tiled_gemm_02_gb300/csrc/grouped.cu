@@ -67,7 +67,10 @@ constexpr int RASTER = 8;                     // row tiles that share a features
 constexpr int MIN_RUN = 8;                    // K slices: a shorter run costs more than it saves
 constexpr uint32_t EPI_BYTES = 32 * 256;      // staged 32 rows x 128 features of 16 bits
 // K slices by which a split must shorten the busiest unit's work: what the
-// exchange of partial sums costs (about 4 us at a quarter us a slice).
+// exchange of partial sums costs (about 4 us at a quarter us a slice).  Three
+// times as many for CTA pairs that share all of their tiles, whose 128 KB of
+// partial sums a CTA nothing else hides (36 tiles of 47 slices on 76 pairs:
+// 29.3 us split, 21.7 whole).
 constexpr int SPLIT_GAIN = 16;
 // warp 0: TMA loads, 1: MMA issue, 2-9: epilogue (two groups of four, taking
 // 32-row chunks of a tile in turn), 10: schedule
@@ -235,7 +238,9 @@ struct Schedule {
     // whole tiles take waves + 1 tiles of the busiest unit's time, equal runs
     // all / units slices
     const int64_t tile_kb = tiles > 0 ? all / tiles : 0;
-    const bool split = tiles % units != 0 && (waves + 1) * tile_kb - all / units >= SPLIT_GAIN;
+    const int64_t gain = (waves + 1) * tile_kb - all / units;
+    const bool split =
+        tiles % units != 0 && gain >= (CG == 2 && waves == 0 ? 3 * SPLIT_GAIN : SPLIT_GAIN);
     whole = !split ? tiles : (waves > 1 ? waves - 1 : 0) * units;
     s0 = p.grad ? slices_before(whole) : static_cast<int64_t>(whole) * kb;
     len = all - s0;
@@ -744,6 +749,20 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         }
         buffer = buffer + 1 == C::BUFS ? 0 : buffer + 1;
       };
+      // An empty sum: zeros, 16 bytes a lane, need no staging (gradients of 25
+      // experts of 4272 x 2816, 7 of them with a row: 110 us, 206 through it).
+      if (!sum && staged_store) {
+        const int f8 = x.f0 + static_cast<int>(rank) * FT + 8 * (lane & 15);
+        for (int r = 2 * (warp - 2) + (lane >> 4); r < x.nq && f8 < p.N; r += 2 * EPI_WARPS) {
+          uint16_t* const d = static_cast<uint16_t*>(p.D) + (row0 + r) * p.ldd + f8;
+          if (f8 + 8 <= p.N) {
+            *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
+          } else {
+            for (int j = 0; j < p.N - f8; ++j) d[j] = 0;
+          }
+        }
+        continue;
+      }
       if (sum && x.pieces == 1 && staged_store) {
         // fragments of 16 features x 8 rows, transposed into rows by stmatrix
         if constexpr (DT != T_F32) {

@@ -399,10 +399,18 @@ int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     cudaGetLastError();
   // The wide form needs D rows to fill a tile's columns (more than 64 an
-  // expert, on average) and a wave of tiles.
+  // expert, on average) and a wave of tiles; or, with sums long enough to make
+  // up for its slower ends, so many tiles that the narrow form would take a
+  // second wave (narrow against wide, us: 2000 rows over 2 of 4096 x 2048 50.1,
+  // 28.0; 1024 over 8 of 4096 x 2048 42.6, 32.5; 1024 over 4 of 2048 x 2048
+  // 18.7, 16.7; but 8 slices, 4096 over 2 of 512 x 512, 10.3, 11.5; and in one
+  // wave, 400 over 4 of 4096 x 2048, 18.6, 27.2).
   const int64_t m = grad ? d.K : d.R / d.E;
-  const bool wide =
-      planned("wide", m > 64 && d.E * ((m + 255) / 256) * ((d.N + 255) / 256) >= sms / 2);
+  const int64_t wide_tiles = d.E * ((m + 255) / 256) * ((d.N + 255) / 256);
+  const int64_t narrow_tiles = d.E * ((m + 63) / 64) * ft;
+  const int64_t slices = ((grad ? d.R / d.E : d.K) + BK - 1) / BK;
+  const bool wide = planned(
+      "wide", m > 64 && (wide_tiles >= sms / 2 || (2 * narrow_tiles > 3 * sms && slices >= 16)));
   const int most_units = std::max(1, wide ? sms / 2 : sms);
   const size_t partial = grouped_partial_bytes(wide, most_units);
   const size_t counters = 4 * static_cast<size_t>(most_units) * (wide ? 2 : 1);
