@@ -41,8 +41,8 @@
 // 338 us against 254 for 32 experts of 513 and of 528 rows, 2048 x 4096.)
 //
 // Measured (one GB300, bf16): 32768 rows x 4096 over 32 experts of 4096 x 4096
-// 637 us (1727 TFLOP/s, tensor-bound); weight gradients of 16384 rows, 32 of
-// 2048 x 4096, 225 us (1220 TFLOP/s; 174 without D's stores, which take the
+// 640 us (1718 TFLOP/s, tensor-bound); weight gradients of 16384 rows, 32 of
+// 2048 x 4096, 231 us (1190 TFLOP/s; 174 without D's stores, which take the
 // same road as the next tile's operands: 537 MB of D); 64 rows over 48 of 64
 // experts of 4096 x 2048 126 us (6.4 TB/s of weights); 1000 rows, 1000 x 1000
 // over 7 of 8 experts 12 us (launch, first loads and epilogue, one wave).

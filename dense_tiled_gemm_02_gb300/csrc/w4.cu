@@ -310,11 +310,12 @@ cudaError_t launch_as(const W4Params& p, cudaStream_t st) {
   // blocks then wait for one another's loads and sums less (4 against 8 warps:
   // 4 x 8192 x 32768 39.4 against 42.4 us, 64 x 2048 x 1024 over 40 experts
   // 16.6 against 18.9; 2 against 4 at K = 1024: 16.9 against 17.9), but where
-  // the tiles are few the SMs would be half empty (8 against 4: 16 x 8192 x
-  // 8192 20.9 against 27.5; 16 against 8: 1 x 4096 x 4096 5.2 against 5.7).
+  // the tiles are few the SMs would be partly empty (8 against 4: 16 x 8192 x
+  // 8192 20.9 against 27.5, 4 x 8192 x 10240 20.5 against 23.1, but 16 x 4096
+  // x 16384 21.4 against 20.0; 16 against 8: 1 x 4096 x 4096 5.2 against 5.7).
   int warps = runs <= 4 ? 2 : 4;
   while (warps < kMaxWarps<NT> && warps < runs &&
-         2ll * tiles * experts * warps < SM_WARPS * p.num_sms)
+         3ll * tiles * experts * warps < 2 * SM_WARPS * p.num_sms)
     warps *= 2;
   return launch_pdl(w4_kernel<BF16, WPT, NT>, dim3(tiles, experts), dim3(32 * warps), 0, st, p);
 }
