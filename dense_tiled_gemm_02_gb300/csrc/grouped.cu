@@ -727,7 +727,6 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             const int y = x.q0 + c, z = p.grad ? x.e : 0;
             if (fc < p.N) store_3d(&tmD, src, fc, y, z);
             if (fc + 64 < p.N) store_3d(&tmD, src + 4096u, fc + 64, y, z);
-            bulk_commit();
           }
         } else {
 #pragma unroll
@@ -747,6 +746,10 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             }
           }
         }
+        // One bulk group a chunk, empty where the threads stored it: stage_free
+        // counts groups, and a chunk without one would let it pass a buffer
+        // whose store is still reading.
+        if (group_leader) bulk_commit();
         buffer = buffer + 1 == C::BUFS ? 0 : buffer + 1;
       };
       // An empty sum: zeros, 16 bytes a lane, need no staging (gradients of 25

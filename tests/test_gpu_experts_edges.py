@@ -1,0 +1,49 @@
+"""Calls of the expert and 4-bit-weight operators at the edges of their
+protocols: staging buffers under many ragged tiles, streams, timeouts, and
+values that must not be looked at.  Bounds as in test_gpu_experts."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import dense_tiled_gemm_02_gb300 as pkg
+from gpu_helpers import forced_plan
+from test_gpu_experts import BF16, F16, done, grouped_ref, near, offsets_of, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+def ragged_counts(E, low, high, seed):
+    """Group sizes of which few are a multiple of 32."""
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(low, high, (E,), generator=g).tolist()
+
+
+# ---------------------------------------------------------------- grouped products
+@pytest.mark.parametrize("K,N,dtype,order", [(8, 520, BF16, "nk"), (64, 1032, F16, "kn"),
+                                             (200, 768, BF16, "nk")])
+def test_grouped_ragged_tiles_share_staging_buffers(K, N, dtype, order):
+    """Short sums, many tiles a CTA pair, and groups that end inside a box of
+    32 rows: boxes stored by TMA and boxes stored by the threads take turns in
+    the staging buffers, and a buffer is not written before its store has read
+    it."""
+    counts = ragged_counts(120, 200, 300, K) + [1, 31, 33, 0, 257, 289, 513]
+    E, R = len(counts), sum(counts)
+    off = offsets_of(counts)
+    A = rnd((R, K), dtype, 1)
+    B = rnd((E, N, K) if order == "nk" else (E, K, N), dtype, 2)
+    B = B.transpose(1, 2) if order == "nk" else B
+    D = torch.full((R, N), 7.0, dtype=dtype, device="cuda")
+    with forced_plan("wide=1"):
+        op = pkg.GroupedGemm.like(A, B, off, None, D)
+    assert "wide=1" in op.plan()
+    ref, S = grouped_ref(A, B, off, None, False)
+    first = None
+    for _ in range(20):
+        D.fill_(7.0)
+        op.run(A, B, off, None, D)
+        if first is None:
+            first = D.clone()
+            near(D, ref, S, K)
+        assert torch.equal(D, first)
+    done(op)
