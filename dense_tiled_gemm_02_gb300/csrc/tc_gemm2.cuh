@@ -824,6 +824,8 @@ __global__ void __launch_bounds__(PairCfg<BN, KSUB, I8X>::THREADS, 1)
             st_d_chunk_rows(stage + q * 32 * 128, static_cast<uint16_t*>(p.D), p.d_rs, y0w, x0,
                             p.M, half ? min(p.N, x0 + 32) : p.N, lane);
             __syncwarp();  // read out before the buffer takes a later chunk
+            // an empty group: the wait above counts groups, one to a chunk
+            if (lane == 0) bulk_commit();
           }
           const int j = c >> 1;  // this chunk
           if (use_ctma && j + 2 < NCHUNK) {
