@@ -12,6 +12,7 @@
 #include <new>
 #include <string>
 
+#include "clear.h"
 #include "common.h"
 #include "gemm.h"
 #include "moe.h"
@@ -70,8 +71,9 @@ bool planned(const char* key, bool choice) {
   return choice;
 }
 
-// Handle of a kind on the current device with `ws_bytes` of zeroed workspace.
-int make_op(Kind kind, size_t ws_bytes, gemm_op** out) {
+// Handle of a kind on the current device with `ws_bytes` of workspace, of which
+// [zero_off, zero_off + zero_bytes) starts as zeros.
+int make_op(Kind kind, size_t ws_bytes, size_t zero_off, size_t zero_bytes, gemm_op** out) {
   int dev = 0, major = 0, minor = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
@@ -88,9 +90,9 @@ int make_op(Kind kind, size_t ws_bytes, gemm_op** out) {
   op->num_sms = sms;
   op->ws_bytes = ws_bytes;
   if (cudaMalloc(&op->status, kStatusBytes) != cudaSuccess ||
-      cudaMemset(op->status, 0, kStatusBytes) != cudaSuccess ||
-      (ws_bytes && (cudaMalloc(&op->ws, ws_bytes) != cudaSuccess ||
-                    cudaMemset(op->ws, 0, ws_bytes) != cudaSuccess))) {
+      (ws_bytes && cudaMalloc(&op->ws, ws_bytes) != cudaSuccess) ||
+      clear_now({{op->status, kStatusBytes},
+                 {static_cast<uint8_t*>(op->ws) + zero_off, zero_bytes}}) != cudaSuccess) {
     cudaGetLastError();
     if (op->ws) cudaFree(op->ws);
     if (op->status) cudaFree(op->status);
@@ -140,11 +142,16 @@ extern "C" {
 
 int gemm_op_status(gemm_op_t op, gemm_stream_t stream) {
   if (!op) return GEMM_ERR_INVALID_ARG;
+  // all on the caller's stream: what was cleared on another one could be
+  // cleared after the next run had set it
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint32_t word = 0;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;
-  if (cudaMemcpy(&word, op->status, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess)
+  if (cudaMemcpyAsync(&word, op->status, sizeof word, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
     return GEMM_ERR_CUDA;
-  if (word != 0 && cudaMemset(op->status, 0, sizeof word) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (word != 0 && (cudaMemsetAsync(op->status, 0, sizeof word, st) != cudaSuccess ||
+                    cudaStreamSynchronize(st) != cudaSuccess))
+    return GEMM_ERR_CUDA;
   if (word & STATUS_TIMEOUT) return GEMM_ERR_DEVICE_TIMEOUT;
   return (word & STATUS_BAD_INDEX) ? GEMM_ERR_INVALID_ARG : GEMM_OK;
 }
@@ -191,7 +198,7 @@ int gemm_route_create(gemm_op_t* out, const gemm_route_desc_t* desc) {
   const int blocks = route_blocks(d.T, d.k, std::max(sms, 1));
   gemm_op* op = nullptr;
   const size_t ws = blocks > 1 ? sizeof(int) * static_cast<size_t>(blocks) * up(d.E, 4) : 0;
-  const int rc = make_op(Kind::kRoute, ws, &op);
+  const int rc = make_op(Kind::kRoute, ws, 0, ws, &op);
   if (rc != GEMM_OK) return rc;
   op->route = d;
   op->grid = blocks;
@@ -269,7 +276,7 @@ int gemm_permute_create(gemm_op_t* out, const gemm_permute_desc_t* desc) {
     return GEMM_ERR_INVALID_ARG;
   if (!is_float(d.type)) return GEMM_ERR_UNSUPPORTED;
   gemm_op* op = nullptr;
-  const int rc = make_op(Kind::kPermute, 0, &op);
+  const int rc = make_op(Kind::kPermute, 0, 0, 0, &op);
   if (rc != GEMM_OK) return rc;
   op->permute = d;
   op->plan = "permute T=" + std::to_string(d.T) + " k=" + std::to_string(d.k) +
@@ -418,7 +425,7 @@ int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc) {
   gemm_op* op = nullptr;
   const size_t maps_off = static_cast<size_t>(up(static_cast<int64_t>(p_off + partial + counters), 256));
   const size_t maps = grad ? 2 * sizeof(CUtensorMap) * d.E : 0;
-  const int rc = make_op(Kind::kGrouped, maps_off + maps, &op);
+  const int rc = make_op(Kind::kGrouped, maps_off + maps, p_off + partial, counters, &op);
   if (rc != GEMM_OK) return rc;
   op->units = std::min(most_units, prepare_grouped(wide, d.d_type, op->num_sms));
   if (op->units <= 0) {
@@ -540,7 +547,7 @@ int gemm_w4_create(gemm_op_t* out, const gemm_w4_desc_t* desc) {
     return GEMM_ERR_UNSUPPORTED;
   if (d.ldx % 8 != 0) return GEMM_ERR_MISALIGNED;
   gemm_op* op = nullptr;
-  const int rc = make_op(Kind::kW4, 0, &op);
+  const int rc = make_op(Kind::kW4, 0, 0, 0, &op);
   if (rc != GEMM_OK) return rc;
   op->w4 = d;
   char buf[160];

@@ -47,3 +47,56 @@ def test_grouped_ragged_tiles_share_staging_buffers(K, N, dtype, order):
             near(D, ref, S, K)
         assert torch.equal(D, first)
     done(op)
+
+
+# ---------------------------------------------------------------- streams
+def busy(milliseconds=30):
+    """Work on the current stream that takes about that long."""
+    torch.cuda._sleep(int(milliseconds * 2e6))
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("K,N", [(61, 1000), (5000, 264)])  # copied rows; sums shared by units
+def test_grouped_first_run_on_a_side_stream(K, N, grad):
+    """A handle made while the default stream is busy is ready for a stream
+    that does not wait for it."""
+    counts = [70, 0, 300]
+    off, R = offsets_of(counts), sum(counts)
+    A = rnd((R, K), BF16, 1)
+    B = rnd((R, N) if grad else (3, K, N), BF16, 2)
+    D = torch.zeros((3, K, N) if grad else (R, N), device="cuda")
+    ref, S = grouped_ref(A, B, off, None, grad)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy()
+    op = pkg.GroupedGemm.like(A, B, off, None, D)
+    op.run(A, B, off, None, D, stream=side)
+    assert op.status(side) == pkg.GEMM_OK
+    side.synchronize()
+    with torch.cuda.stream(side):
+        got = D.clone()
+    torch.cuda.synchronize()
+    near(got, ref, S, max(counts) if grad else K)
+    op.run(A, B, off, None, D, stream=side)  # nothing was cleared late
+    torch.cuda.synchronize()
+    assert torch.equal(D, got)
+    done(op)
+
+
+def test_route_first_run_on_a_side_stream():
+    x = rnd((5000, 90), torch.float32, 1)
+    op = pkg.Route.like(x, 3)
+    want = op.outputs()
+    op.run(x, *want)
+    done(op)
+    outs = tuple(torch.empty_like(o) for o in want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy()
+    op = pkg.Route.like(x, 3)
+    op.run(x, *outs, stream=side)
+    assert op.status(side) == pkg.GEMM_OK
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert torch.equal(a, b)
+    op.close()
