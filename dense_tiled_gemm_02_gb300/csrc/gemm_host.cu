@@ -12,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "clear.h"
 #include "common.h"
 #include "gemm.h"
 #include "moe.h"
@@ -368,13 +369,10 @@ int plan_decode(gemm_plan* h, int sms, bool mma) {
     h->ws = nullptr;
     return GEMM_ERR_ALLOC_FAILED;
   }
-  if (cudaMemset(static_cast<char*>(h->ws) + h->ws_flags_off, 0, col_blocks * 4) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    cudaFree(h->ws);
-    return GEMM_ERR_CUDA;
-  }
-  if (cudaMalloc(&h->status, 256) != cudaSuccess || cudaMemset(h->status, 0, 256) != cudaSuccess) {
+  if (cudaMalloc(&h->status, 256) != cudaSuccess ||
+      clear_now({{h->status, 256},
+                 {static_cast<char*>(h->ws) + h->ws_flags_off, (size_t)col_blocks * 4}}) !=
+          cudaSuccess) {
     cudaGetLastError();
     if (h->status) cudaFree(h->status);
     cudaFree(h->ws);
@@ -451,7 +449,8 @@ int plan_native_i8(gemm_plan* h) {
     h->ws = nullptr;
     return GEMM_ERR_ALLOC_FAILED;
   }
-  if (cudaMalloc(&h->status, 256) != cudaSuccess || cudaMemset(h->status, 0, 256) != cudaSuccess) {
+  if (cudaMalloc(&h->status, 256) != cudaSuccess ||
+      clear_now({{h->status, 256}}) != cudaSuccess) {
     cudaGetLastError();
     if (h->status) cudaFree(h->status);
     if (h->ws) cudaFree(h->ws);
@@ -673,7 +672,7 @@ int gemm_create(gemm_handle_t* out, const gemm_desc_t* desc) {
     h->N = d.N;
     h->K = d.K;
     if (cudaMalloc(&h->status, 256) != cudaSuccess ||
-        cudaMemset(h->status, 0, 256) != cudaSuccess) {
+        clear_now({{h->status, 256}}) != cudaSuccess) {
       cudaGetLastError();
       if (h->status) cudaFree(h->status);
       delete h;
@@ -974,17 +973,12 @@ int gemm_create(gemm_handle_t* out, const gemm_desc_t* desc) {
     delete h;
     return GEMM_ERR_ALLOC_FAILED;
   }
-  if ((sk_slots > 0 &&
-       cudaMemset(static_cast<char*>(h->ws) + h->ws_flags_off, 0, sk_slots * 2 * 4) !=
-           cudaSuccess) ||
-      (kp.sk1 && cudaMemset(static_cast<char*>(h->ws) + h->ws_fixflag_off, 0,
-                            (size_t)h->grid * 4) != cudaSuccess)) {
-    cudaGetLastError();
-    cudaFree(h->ws);
-    delete h;
-    return GEMM_ERR_CUDA;
-  }
-  if (cudaMalloc(&h->status, 256) != cudaSuccess || cudaMemset(h->status, 0, 256) != cudaSuccess) {
+  if (cudaMalloc(&h->status, 256) != cudaSuccess ||
+      clear_now({{h->status, 256},
+                 {static_cast<char*>(h->ws) + h->ws_flags_off,
+                  sk_slots > 0 ? (size_t)sk_slots * 2 * 4 : 0},
+                 {static_cast<char*>(h->ws) + h->ws_fixflag_off,
+                  kp.sk1 ? (size_t)h->grid * 4 : 0}}) != cudaSuccess) {
     cudaGetLastError();
     if (h->status) cudaFree(h->status);
     if (h->ws) cudaFree(h->ws);
@@ -1336,12 +1330,16 @@ extern "C" {
 
 int gemm_get_status(gemm_handle_t h, gemm_stream_t stream) {
   if (!h) return GEMM_ERR_INVALID_ARG;
+  // all on the caller's stream: what was cleared on another one could be
+  // cleared after the next run had set it
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint32_t word = 0;
-  if (cudaStreamSynchronize(st) != cudaSuccess) return GEMM_ERR_CUDA;
-  if (cudaMemcpy(&word, h->status, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess)
+  if (cudaMemcpyAsync(&word, h->status, sizeof word, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
     return GEMM_ERR_CUDA;
-  if (word != 0 && cudaMemset(h->status, 0, sizeof word) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (word != 0 && (cudaMemsetAsync(h->status, 0, sizeof word, st) != cudaSuccess ||
+                    cudaStreamSynchronize(st) != cudaSuccess))
+    return GEMM_ERR_CUDA;
   return (word & STATUS_TIMEOUT) ? GEMM_ERR_DEVICE_TIMEOUT : GEMM_OK;
 }
 
