@@ -448,6 +448,18 @@ class Gemm:
             pass
 
 
+def _after_current(stream, new) -> None:
+    """Let `stream` (a torch stream, a raw handle, or None: the current one)
+    wait for what the current stream has enqueued before it writes the tensor
+    `new`, just made there: its filling, and the last use of its memory."""
+    import torch
+    if stream is None or not new.is_cuda:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), new.device)
+    stream.wait_stream(torch.cuda.current_stream(new.device))
+
+
 def matmul_add(A, B, C=None, out_dtype=None, D=None, stream=None):
     """D = A @ B + C through the library (plans a fresh handle each call)."""
     import torch

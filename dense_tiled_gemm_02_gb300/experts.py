@@ -327,11 +327,19 @@ def pack_w4(q: torch.Tensor) -> torch.Tensor:
     return (q[..., 0::2] | (q[..., 1::2] << 4)).contiguous()
 
 
+def _new_zeros(shape, dtype, device, stream) -> torch.Tensor:
+    """Zeros that a call on `stream` may write."""
+    D = torch.zeros(shape, dtype=dtype, device=device)
+    _gemm._after_current(stream, D)
+    return D
+
+
 def grouped_matmul(A, B, offsets, C=None, out_dtype=None, D=None, stream=None):
     """D[r] = A[r] @ B[e] (+ C[r]) for the rows r of each expert e (plans a
-    fresh handle each call).  A new D's rows of no expert are zero."""
+    fresh handle each call).  A new D's rows of no expert are zero, and a
+    `stream` waits for the current one before it writes them."""
     if D is None:
-        D = torch.zeros((A.shape[0], B.shape[2]), dtype=out_dtype or A.dtype, device=A.device)
+        D = _new_zeros((A.shape[0], B.shape[2]), out_dtype or A.dtype, A.device, stream)
     g = GroupedGemm.like(A, B, offsets, C, D)
     try:
         g.run(A, B, offsets, C, D, stream)
@@ -342,9 +350,10 @@ def grouped_matmul(A, B, offsets, C=None, out_dtype=None, D=None, stream=None):
 
 def w4_matmul(X, W, scales, zeros=None, offsets=None, group: int = 128, out_dtype=None, D=None,
               stream=None):
-    """D = X @ ((q - zeros) * scales)^T (plans a fresh handle each call)."""
+    """D = X @ ((q - zeros) * scales)^T (plans a fresh handle each call; a new
+    D and `stream` as in grouped_matmul)."""
     if D is None:
-        D = torch.zeros((X.shape[0], W.shape[1]), dtype=out_dtype or X.dtype, device=X.device)
+        D = _new_zeros((X.shape[0], W.shape[1]), out_dtype or X.dtype, X.device, stream)
     g = W4Gemm.like(X, W, scales, zeros, offsets, D, group)
     try:
         g.run(X, W, scales, zeros, offsets, D, stream)

@@ -8,7 +8,7 @@ import torch
 
 import dense_tiled_gemm_02_gb300 as pkg
 from gpu_helpers import forced_plan
-from test_gpu_experts import BF16, F16, done, grouped_ref, near, offsets_of, rnd
+from test_gpu_experts import BF16, F16, done, grouped_ref, near, offsets_of, rnd, w4_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,27 @@ def test_route_first_run_on_a_side_stream():
     for a, b in zip(outs, want):
         assert torch.equal(a, b)
     op.close()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_new_results_on_a_given_stream(raw):
+    """grouped_matmul and w4_matmul with `stream`: the zeros of a new result
+    do not arrive after the product."""
+    off = offsets_of([30, 0, 50], first=2)
+    A, B = rnd((90, 128), BF16, 1), rnd((3, 128, 72), BF16, 2)
+    ref, S = grouped_ref(A, B, off, None, False)
+    q = torch.randint(0, 16, (3, 72, 128), generator=torch.Generator().manual_seed(3)).cuda()
+    W, s = pkg.pack_w4(q), rnd((3, 72, 1), BF16, 4)
+    wref, wS = w4_ref(A, q, s, None, off, 128)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+    busy()
+    D = pkg.grouped_matmul(A, B, off, stream=stream)
+    torch.cuda.synchronize()
+    near(D, ref, S, 128)
+    busy()
+    D = pkg.w4_matmul(A, W, s, None, off, 128, stream=stream)
+    torch.cuda.synchronize()
+    near(D, wref, wS, 129)
+    assert bool((D[:2] == 0).all()) and bool((D[82:] == 0).all())
