@@ -461,11 +461,14 @@ def _after_current(stream, new) -> None:
 
 
 def matmul_add(A, B, C=None, out_dtype=None, D=None, stream=None):
-    """D = A @ B + C through the library (plans a fresh handle each call)."""
+    """D = A @ B + C through the library (plans a fresh handle each call).
+    Without a D, a given `stream` waits for the current one: the new D's memory
+    may still be in use there."""
     import torch
     if D is None:
         dt = out_dtype or (torch.int32 if A.dtype == torch.int8 else A.dtype)
         D = torch.empty((A.shape[0], B.shape[1]), dtype=dt, device=A.device)
+        _after_current(stream, D)
     g = Gemm.like(A, B, C, D)
     try:
         g.run(A, B, C, D, stream)

@@ -38,3 +38,19 @@ def test_first_run_on_a_side_stream(M, N, K, plan):
     assert torch.equal(D, got)
     assert g.status(side) == pkg.GEMM_OK
     g.close()
+
+
+def test_matmul_add_on_a_given_stream():
+    """A new D may get memory whose last use the current stream has yet to
+    run: it is not written after the product."""
+    A, B = rnd((200, 256), BF16, 1), rnd((256, 136), BF16, 2)
+    ref, S = A.double() @ B.double(), A.double().abs() @ B.double().abs()
+    side = torch.cuda.Stream()
+    old = torch.empty((200, 136), dtype=BF16, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(60_000_000)
+    old.fill_(9.0)
+    del old
+    D = pkg.matmul_add(A, B, stream=side)
+    torch.cuda.synchronize()
+    near(D, ref, S, 256)
