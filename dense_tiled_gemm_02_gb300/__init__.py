@@ -37,6 +37,7 @@ GEMM_ERR_DEVICE_TIMEOUT = -5
 GEMM_ERR_ALLOC_FAILED = -6
 GEMM_ERR_NO_DEVICE = -7
 GEMM_DEBUG_SKIP_FIRST_FILL = 1
+GEMM_DEBUG_SKIP_ONE_FILL = 2
 
 EXPORTED = ["gemm_create", "gemm_run", "gemm_get_status", "gemm_destroy", "gemm_strerror",
             "gemm_plan_string", "gemm_workspace_bytes", "gemm_raster_tile", "gemm_debug_set",

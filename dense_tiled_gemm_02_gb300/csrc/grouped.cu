@@ -508,6 +508,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     uint32_t it = 0, s = 0, ph = 0;
     int mapped = -1;  // grad: the expert whose tensor maps have been acquired
     bool stop = false, skipped = false;
+    const bool skip = leader && ((p.debug_flags & DBG_SKIP_FIRST_FILL) ||
+                                 ((p.debug_flags & DBG_SKIP_ONE_FILL) && blockIdx.x < CG));
     const uint32_t sF0 = smem_u32(sF), sX0 = smem_u32(sX);
     const uint32_t full0 = CG == 2 ? map_shared_rank(full(0), 0) : full(0);
     while (next_piece(x)) {
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
               stop = true;
               return;
             }
-            if (it == 0 && leader && (p.debug_flags & DBG_SKIP_FIRST_FILL)) {
+            if (it == 0 && skip) {
               skipped = true;  // test hook: the MMA's wait on the first stage expires
             } else {
               if (leader) mbar_arrive_expect_tx(full(s), both);

@@ -14,6 +14,8 @@ void* tensor_map_encoder();
 
 // Status bit beside STATUS_TIMEOUT: offsets or row indices out of range.
 constexpr uint32_t STATUS_BAD_INDEX = 2u;
+// Debug flag beside DBG_SKIP_FIRST_FILL: the same in the first unit alone.
+constexpr int DBG_SKIP_ONE_FILL = 2;
 
 // True in one lane, always the same, of a converged warp.  The branch of a
 // thread that issues tcgen05 or TMA instructions is taken on this and not on
@@ -105,7 +107,7 @@ struct GroupedParams {
   long long ldc, ldd;
   void* D;
   float* partial;      // grouped_partial_bytes()
-  unsigned* counters;  // one per CTA, zero between calls
+  unsigned* counters;  // one per CTA, zero between calls (cleared by the host after a timeout)
   CUtensorMap* maps;   // grad: the experts' maps of the features, then of the rows operand
   uint32_t* status;
   unsigned long long timeout_ns;

@@ -53,6 +53,7 @@ struct gemm_op {
   int64_t a_rows = 0, a_cols = 0, b_rows = 0, b_cols = 0;
   int64_t ws_lda = 0, ws_ldb = 0;
   size_t ws_b_off = 0, ws_partial_off = 0, ws_counters_off = 0, ws_maps_off = 0;
+  size_t counters_bytes = 0;
   bool wide = false;
   int units = 0;
   int grid = 0;  // route: blocks
@@ -148,6 +149,12 @@ int gemm_op_status(gemm_op_t op, gemm_stream_t stream) {
   uint32_t word = 0;
   if (cudaMemcpyAsync(&word, op->status, sizeof word, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess)
+    return GEMM_ERR_CUDA;
+  // Units that gave up left the counters of the tiles they shared part-way:
+  // the next call would take such a tile for finished too early.
+  if ((word & STATUS_TIMEOUT) && op->counters_bytes &&
+      cudaMemsetAsync(static_cast<uint8_t*>(op->ws) + op->ws_counters_off, 0, op->counters_bytes,
+                      st) != cudaSuccess)
     return GEMM_ERR_CUDA;
   if (word != 0 && (cudaMemsetAsync(op->status, 0, sizeof word, st) != cudaSuccess ||
                     cudaStreamSynchronize(st) != cudaSuccess))
@@ -436,6 +443,7 @@ int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc) {
   op->wide = wide;
   op->ws_partial_off = p_off;
   op->ws_counters_off = p_off + partial;
+  op->counters_bytes = counters;
   op->ws_maps_off = maps_off;
   op->grouped = d;
   op->copy_a = copy_a;

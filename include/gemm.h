@@ -425,7 +425,9 @@ typedef struct gemm_op* gemm_op_t;
 /* gemm_op_status: synchronise stream, then return and clear the handle's
  * device status word: GEMM_OK, GEMM_ERR_DEVICE_TIMEOUT (a bounded device-side
  * wait of a grouped product expired) or GEMM_ERR_INVALID_ARG (offsets or row
- * indices out of range); GEMM_ERR_CUDA if the synchronisation fails. */
+ * indices out of range); GEMM_ERR_CUDA if the synchronisation fails.  After a
+ * timeout the outputs of the handle's calls are undefined until this has
+ * reported it. */
 GEMM_API int gemm_op_status(gemm_op_t op, gemm_stream_t stream);
 
 /* gemm_op_destroy: synchronise the device and free the handle; NULL is a no-op. */
@@ -440,7 +442,10 @@ GEMM_API int64_t gemm_op_workspace_bytes(gemm_op_t op);
 GEMM_API int gemm_op_plan_string(gemm_op_t op, char* buf, size_t n);
 
 /* gemm_op_debug_set: the test hook of gemm_debug_set, for the grouped
- * product's ring (the other operators wait for nothing and ignore it). */
+ * product's ring (the other operators wait for nothing and ignore it).
+ * GEMM_DEBUG_SKIP_ONE_FILL: only the first CTA or CTA pair of the next run
+ * leaves its first stage unfilled. */
+#define GEMM_DEBUG_SKIP_ONE_FILL 2
 GEMM_API int gemm_op_debug_set(gemm_op_t op, int flags, uint64_t timeout_ns);
 
 /*

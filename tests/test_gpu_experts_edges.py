@@ -124,3 +124,31 @@ def test_new_results_on_a_given_stream(raw):
     torch.cuda.synchronize()
     near(D, wref, wS, 129)
     assert bool((D[:2] == 0).all()) and bool((D[82:] == 0).all())
+
+
+# ---------------------------------------------------------------- timeouts
+@pytest.mark.parametrize("plan", ["wide=0", "wide=1"])
+@pytest.mark.parametrize("grad", [False, True])
+def test_grouped_shared_sums_after_a_timeout(plan, grad):
+    """One unit gives up a wait while the others finish their pieces of the
+    tiles they share with it: once that is reported, the next calls are right."""
+    counts = [3000, 0, 1111] if grad else [70, 0, 300]
+    R, K, N = sum(counts), (96 if grad else 5000), 200
+    off = offsets_of(counts)
+    A = rnd((R, K), BF16, 1)
+    B = rnd((R, N) if grad else (3, K, N), BF16, 2)
+    D = torch.zeros((3, K, N) if grad else (R, N), device="cuda")
+    ref, S = grouped_ref(A, B, off, None, grad)
+    with forced_plan(plan):
+        op = pkg.GroupedGemm.like(A, B, off, None, D)
+    for _ in range(3):
+        op.debug_set(pkg.GEMM_DEBUG_SKIP_ONE_FILL, 20_000_000)
+        op.run(A, B, off, None, D)
+        assert op.status() == pkg.GEMM_ERR_DEVICE_TIMEOUT
+        op.debug_set(0)
+        for _ in range(3):
+            D.fill_(7.0)
+            op.run(A, B, off, None, D)
+            assert op.status() == pkg.GEMM_OK
+            near(D, ref, S, max(counts) if grad else K)
+    op.close()
