@@ -373,10 +373,10 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
   constexpr int NBARS = 2 * STAGES + 5 + 2 * QUEUE;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  volatile int* const ep_go = abort_flag + 1;
-  volatile int* const ep_last = abort_flag + 2;
+  volatile int* const ep_go = abort_flag + 1;  // two, taken in turn
+  volatile int* const ep_last = abort_flag + 3;
   Piece* const queue = reinterpret_cast<Piece*>(reinterpret_cast<uint8_t*>(bars) + 512);
-  static_assert(8 * NBARS + 16 <= 512 && 512 + QUEUE * sizeof(Piece) <= C::BAR_BYTES, "layout");
+  static_assert(8 * NBARS + 20 <= 512 && 512 + QUEUE * sizeof(Piece) <= C::BAR_BYTES, "layout");
   int* const lo = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + C::BAR_BYTES);
   int* const prefix = lo + p.E + 1;
 
@@ -461,7 +461,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const uint64_t tmo = p.timeout_ns;
-  // The next piece of this CTA's work; false at its end or after a timeout.
+  // The next piece of this CTA's work, taken by one warp for itself; false at
+  // its end or after a timeout.
   uint32_t q_at = 0, q_ph = 0;
   auto next_piece = [&](Piece& x) {
     bool ok = true;
@@ -672,19 +673,31 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     uint32_t acc_it = 0;
     int buffer = 0;  // of the next chunk
     const int unit = blockIdx.x / CG;
-    while (next_piece(x)) {
+    for (uint32_t turn = 0;; turn ^= 1u) {
       const uint32_t buf = acc_it & 1u;
-      const bool sum = x.k < x.kend;
-      if (sum) {
-        if (ep_leader)
-          *ep_go = bounded_wait(acc_full(buf), (acc_it >> 1) & 1u, abort_flag, p.status,
-                                STATUS_TIMEOUT, tmo) ? 1 : 0;
-        named_barrier_sync(1, 32 * EPI_WARPS);
-        const bool go = *ep_go != 0;
-        named_barrier_sync(1, 32 * EPI_WARPS);
-        if (!go) break;
-        tc_fence_after();
+      // One thread decides for all eight warps whether there is a piece and
+      // its sums: after a timeout a warp that found the last piece would wait
+      // for ever in the barriers below for one that had given up.  (Of the two
+      // flags the other is written before the next barrier, this one after it.)
+      if (ep_leader) {
+        bool go = bounded_wait(q_full(q_at), q_ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
+        if (go && queue[q_at].more && queue[q_at].k < queue[q_at].kend)
+          go = bounded_wait(acc_full(buf), (acc_it >> 1) & 1u, abort_flag, p.status,
+                            STATUS_TIMEOUT, tmo);
+        ep_go[turn] = go ? 1 : 0;
       }
+      named_barrier_sync(1, 32 * EPI_WARPS);
+      if (!ep_go[turn]) break;
+      x = queue[q_at];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty(q_at));
+      if (++q_at == QUEUE) {
+        q_at = 0;
+        q_ph ^= 1u;
+      }
+      if (!x.more) break;
+      const bool sum = x.k < x.kend;
+      if (sum) tc_fence_after();
       auto release = [&] {  // the accumulator has been read
         tc_fence_before();
         __syncwarp();

@@ -152,3 +152,29 @@ def test_grouped_shared_sums_after_a_timeout(plan, grad):
             assert op.status() == pkg.GEMM_OK
             near(D, ref, S, max(counts) if grad else K)
     op.close()
+
+
+@pytest.mark.parametrize("plan", ["wide=0", "wide=1"])
+@pytest.mark.parametrize("flag", [pkg.GEMM_DEBUG_SKIP_FIRST_FILL, pkg.GEMM_DEBUG_SKIP_ONE_FILL])
+@pytest.mark.parametrize("out", [BF16, torch.float32])
+def test_grouped_timeout_among_empty_groups(plan, flag, out):
+    """Empty groups need no wait, so pieces of them are still handed out when a
+    wait has run out: every warp of the kernel ends all the same."""
+    counts = ([40] + [0] * 9 + [70] + [0] * 3) * 6
+    E, R, K, N = len(counts), sum(counts), 136, 264
+    off = offsets_of(counts)
+    A, B = rnd((R, K), BF16, 1), rnd((R, N), BF16, 2)
+    D = torch.zeros((E, K, N), dtype=out, device="cuda")
+    ref, S = grouped_ref(A, B, off, None, True)
+    with forced_plan(plan):
+        op = pkg.GroupedGemm.like(A, B, off, None, D)
+    for timeout_ns in (1_000_000, 3_000_000, 10_000_000):
+        op.debug_set(flag, timeout_ns)
+        op.run(A, B, off, None, D)
+        assert op.status() == pkg.GEMM_ERR_DEVICE_TIMEOUT
+        op.debug_set(0)
+        D.fill_(7.0)
+        op.run(A, B, off, None, D)
+        assert op.status() == pkg.GEMM_OK
+        near(D, ref, S, max(counts))
+    op.close()
