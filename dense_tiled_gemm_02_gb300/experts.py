@@ -55,6 +55,13 @@ def _stack_stride(t: torch.Tensor, what: str) -> int:
     return max(ld, 1)
 
 
+def _on_one_device(device: torch.device, **operands) -> None:
+    """Refuse operands elsewhere: their pointers would go to the kernels."""
+    for name, t in operands.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
 class _Planned:
     """What a tensor argument must look like: shape, dtype and (for
     dimensions longer than one) strides."""
@@ -255,6 +262,7 @@ class GroupedGemm(_Op):
             raise ValueError("C must have D's shape and type")
         if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
             raise ValueError("offsets must be E + 1 contiguous int32 values")
+        _on_one_device(A.device, B=B, offsets=offsets, C=C, D=D)
         desc = _gemm.GroupedDesc(
             1 if grad else 0, E, R, K, N, _type(A), 0 if C is None else _type(C), _type(D), layout,
             _row_stride(A, "A"), ldb, 0 if C is None else ld_of(C, "C"), ld_of(D, "D"))
@@ -299,6 +307,7 @@ class W4Gemm(_Op):
         elif (tuple(offsets.shape) != (E + 1,) or offsets.dtype != torch.int32 or
               not offsets.is_contiguous()):
             raise ValueError("offsets must be E + 1 contiguous int32 values")
+        _on_one_device(X.device, W=W, scales=scales, zeros=zeros, offsets=offsets, D=D)
         desc = _gemm.W4Desc(E, group, int(zeros is not None), R, K, N, _type(X), _type(scales),
                             _type(D), _row_stride(X, "X"), _row_stride(D, "D"))
         op = cls("gemm_w4_create", desc, X.device)

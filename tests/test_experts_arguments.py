@@ -1,0 +1,62 @@
+"""What the Python classes of the expert and 4-bit-weight operators refuse
+before anything is planned or launched, and what they accept: on the CPU, where
+the next error of an accepted call is the missing CUDA device."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import dense_tiled_gemm_02_gb300 as pkg
+
+BF16 = torch.bfloat16
+
+
+def grouped_operands(E=2, R=4, K=8, N=16, with_c=False):
+    return dict(A=torch.zeros(R, K, dtype=BF16), B=torch.zeros(E, K, N, dtype=BF16),
+                offsets=torch.zeros(E + 1, dtype=torch.int32),
+                C=torch.zeros(R, N, dtype=BF16) if with_c else None,
+                D=torch.zeros(R, N, dtype=BF16))
+
+
+def w4_operands(E=2, R=4, K=64, N=16, group=32):
+    G = -(-K // group)
+    return dict(X=torch.zeros(R, K, dtype=BF16), W=torch.zeros(E, N, K // 2, dtype=torch.uint8),
+                scales=torch.zeros(E, N, G, dtype=BF16),
+                zeros=torch.zeros(E, N, G, dtype=torch.uint8),
+                offsets=torch.zeros(E + 1, dtype=torch.int32), D=torch.zeros(R, N, dtype=BF16),
+                group=group)
+
+
+@pytest.mark.parametrize("name", ["B", "offsets", "C", "D"])
+def test_grouped_operands_are_on_one_device(name):
+    t = grouped_operands(with_c=True)
+    t[name] = t[name].to("meta")
+    with pytest.raises(ValueError, match=f"{name} is on meta, not on cpu"):
+        pkg.GroupedGemm.like(**t)
+
+
+@pytest.mark.parametrize("name", ["W", "scales", "zeros", "offsets", "D"])
+def test_w4_operands_are_on_one_device(name):
+    t = w4_operands()
+    t[name] = t[name].to("meta")
+    with pytest.raises(ValueError, match=f"{name} is on meta, not on cpu"):
+        pkg.W4Gemm.like(**t)
+
+
+def test_operands_on_the_host_need_a_device():
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.GroupedGemm.like(**grouped_operands(with_c=True))
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.W4Gemm.like(**w4_operands())
+
+
+@pytest.mark.gpu
+def test_operands_on_the_host_are_refused_beside_others_on_the_gpu():
+    t = grouped_operands()
+    t.update(A=t["A"].cuda(), D=t["D"].cuda(), offsets=t["offsets"].cuda())
+    with pytest.raises(ValueError, match="B is on cpu, not on cuda:0"):
+        pkg.GroupedGemm.like(**t)
+    t = w4_operands()
+    t.update(X=t["X"].cuda(), W=t["W"].cuda(), D=t["D"].cuda(), offsets=t["offsets"].cuda())
+    with pytest.raises(ValueError, match="scales is on cpu, not on cuda:0"):
+        pkg.W4Gemm.like(**t)
