@@ -66,6 +66,23 @@ __device__ __forceinline__ void rows_of(const PermuteParams& p, long long t, int
   if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
 }
 
+// Whether sorted rows t * k + j0 .. + KU - 1 have no slot and become zeros; the
+// same for their entries of row_slot.
+template <int KU>
+__device__ __forceinline__ void without_slot(const PermuteParams& p, long long t, int j0,
+                                             bool (&clear)[KU]) {
+  int slot[KU];
+#pragma unroll
+  for (int u = 0; u < KU; ++u) slot[u] = j0 + u < p.k ? p.row_slot[t * p.k + j0 + u] : 0;
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < KU; ++u) {
+    clear[u] = slot[u] < 0 || slot[u] >= p.T * p.k;
+    bad |= clear[u] && slot[u] != -1;
+  }
+  if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
+}
+
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> zeros() {
   Pack<T, V> z;
@@ -90,8 +107,7 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const PermuteParams p, 
     int row[KU];
     bool clear[KU];
     rows_of(p, t, j0, row);
-#pragma unroll
-    for (int u = 0; u < KU; ++u) clear[u] = j0 + u < p.k && p.row_slot[t * p.k + j0 + u] < 0;
+    without_slot(p, t, j0, clear);
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
       if (row[u] >= 0) *reinterpret_cast<P*>(out + row[u] * p.ld_rows) = x;
@@ -176,11 +192,11 @@ __global__ void __launch_bounds__(THREADS, V > 1 && KU <= 4 ? 3 : 2)
     float g[KU], dot[KU];
     bool clear[KU];
     rows_of(p, t, j0, row);
+    without_slot(p, t, j0, clear);
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
       dot[u] = 0.f;
       g[u] = row[u] >= 0 ? p.gates[t * p.k + j0 + u] : 0.f;
-      clear[u] = j0 + u < p.k && p.row_slot[t * p.k + j0 + u] < 0;
     }
     for (long long h = static_cast<long long>(threadIdx.x) * V; h < p.H; h += THREADS * V) {
       const P d = *reinterpret_cast<const P*>(dY + h);

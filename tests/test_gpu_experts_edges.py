@@ -178,3 +178,33 @@ def test_grouped_timeout_among_empty_groups(plan, flag, out):
         assert op.status() == pkg.GEMM_OK
         near(D, ref, S, max(counts))
     op.close()
+
+
+# ---------------------------------------------------------------- row movement
+@pytest.mark.parametrize("H", [64, 77])
+@pytest.mark.parametrize("bad", [12, 1000, -2, -2 ** 31])
+def test_permute_rows_with_a_bad_slot_are_zeros(H, bad):
+    """row_slot outside [-1, T * k) counts as -1 and sets the status, in the
+    gather and in the gated sum's gradient."""
+    T, k = 4, 3
+    row_slot = torch.arange(T * k, dtype=torch.int32, device="cuda").flip(0)
+    slot_row = row_slot.clone().view(T, k)  # its own inverse
+    row = 7
+    slot_row.view(-1)[int(row_slot[row])] = -1
+    row_slot[row] = bad
+    X, Ys, gates = rnd((T, H), BF16, 1), rnd((T * k, H), BF16, 2), rnd((T, k), torch.float32, 3)
+    out, dgates = torch.full_like(Ys, 7.0), torch.empty_like(gates)
+    op = pkg.Permute.like(X, slot_row)
+    op.gather(X, row_slot, slot_row, out)
+    assert op.status() == pkg.GEMM_ERR_INVALID_ARG
+    live = torch.arange(T * k, device="cuda") != row
+    token = row_slot.long().clamp(0, T * k - 1) // k
+    assert bool((out[row] == 0).all()) and torch.equal(out[live], X[token[live]])
+    out.fill_(7.0)
+    op.combine_backward(X, Ys, row_slot, slot_row, gates, out, dgates)
+    assert op.status() == pkg.GEMM_ERR_INVALID_ARG
+    assert bool((out[row] == 0).all()) and not bool((out[live] == 7).all())
+    row_slot[row] = -1
+    op.gather(X, row_slot, slot_row, out)
+    op.combine_backward(X, Ys, row_slot, slot_row, gates, out, dgates)
+    done(op)
