@@ -330,8 +330,15 @@ class W4Gemm(_Op):
 
 
 def pack_w4(q: torch.Tensor) -> torch.Tensor:
-    """4-bit values (..., K), 0..15, as W4Gemm reads them: (..., K / 2) uint8,
-    the even k in the low half."""
+    """4-bit values (..., K), K even, as W4Gemm reads them: (..., K / 2) uint8,
+    the even k in the low half.  Other values than 0..15 are refused (which
+    waits for the device)."""
+    if q.shape[-1] % 2:
+        raise ValueError(f"K = {q.shape[-1]} is odd")
+    if q.numel():
+        low, high = torch.aminmax(q)
+        if not (low >= 0 and high <= 15):  # NaN is not either
+            raise ValueError(f"4-bit values are 0..15, not {low.item()}..{high.item()}")
     q = q.to(torch.uint8)
     return (q[..., 0::2] | (q[..., 1::2] << 4)).contiguous()
 

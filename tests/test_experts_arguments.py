@@ -60,3 +60,24 @@ def test_operands_on_the_host_are_refused_beside_others_on_the_gpu():
     t.update(X=t["X"].cuda(), W=t["W"].cuda(), D=t["D"].cuda(), offsets=t["offsets"].cuda())
     with pytest.raises(ValueError, match="scales is on cpu, not on cuda:0"):
         pkg.W4Gemm.like(**t)
+
+
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.int8, torch.int32, torch.int64,
+                                   torch.float32, torch.bfloat16])
+def test_pack_w4_takes_four_bits(dtype):
+    q = torch.arange(16).reshape(2, 8).to(dtype)
+    assert pkg.pack_w4(q).tolist() == [[0x10, 0x32, 0x54, 0x76], [0x98, 0xBA, 0xDC, 0xFE]]
+    assert pkg.pack_w4(torch.zeros(3, 0, 4, dtype=dtype)).shape == (3, 0, 2)
+
+
+@pytest.mark.parametrize("q,match", [
+    (torch.tensor([[1, 16]]), "0..15, not 1..16"),       # would spill into its neighbour
+    (torch.tensor([[-1, 3]]), "0..15, not -1..3"),
+    (torch.tensor([[16.0, 3.0]]), "0..15"),
+    (torch.tensor([[float("nan"), 3.0]]), "0..15"),
+    (torch.tensor([[1, 2, 3]]), "K = 3 is odd"),         # would pair 1 and 3 with the one 2
+    (torch.tensor([[1]]), "K = 1 is odd"),
+])
+def test_pack_w4_refuses_other_values(q, match):
+    with pytest.raises(ValueError, match=match):
+        pkg.pack_w4(q)
