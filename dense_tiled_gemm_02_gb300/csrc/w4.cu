@@ -215,16 +215,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps<NT>, SM_WARPS / kMaxWarps<NT>)
         }
       };
       load_tile(0, w[0]);
-      // scales and zero points: thread t of a row's four holds step t's
+      // scales and zero points: thread t of a row's four holds step t's.  Steps
+      // past K take the scale 0: their sums are zeros, and the last group's
+      // scale may be infinite.
       uint32_t sc[RT][2], z[RT][2];
-      const int st = min(s0 + (t < U ? t : U - 1), steps - 1);
+      const int step = s0 + (t < U ? t : U - 1), st = min(step, steps - 1);
       const int G = group_steps == 1 ? st : st / group_steps;
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const long long at = row0 * p.groups + (rows_on(i, h) * p.groups + G);
-          sc[i][h] = scale_bits(p.scales, p.scale_type, at);
+          sc[i][h] = step < steps ? scale_bits(p.scales, p.scale_type, at) : 0u;
           z[i][h] = p.zeros ? p.zeros[at] : 8u;
         }
       uint32_t xf[U][WPT][NT][4];

@@ -208,3 +208,23 @@ def test_permute_rows_with_a_bad_slot_are_zeros(H, bad):
     op.gather(X, row_slot, slot_row, out)
     op.combine_backward(X, Ys, row_slot, slot_row, gates, out, dgates)
     done(op)
+
+
+# ---------------------------------------------------------------- 4-bit weights
+@pytest.mark.parametrize("R", [1, 12, 32])
+@pytest.mark.parametrize("K,group", [(32, 32), (64, 64), (96, 32), (128, 128), (320, 64),
+                                     (384, 128), (160, 128)])
+def test_w4_infinite_scale_of_the_last_group(K, group, R):
+    """The last group's scale is applied to its sum alone: an infinite one
+    gives infinities (its sum is not zero), and nothing past K turns them into
+    NaN."""
+    N, G = 40, -(-K // group)
+    q = torch.full((1, N, K), 12).cuda()
+    W, s = pkg.pack_w4(q), torch.ones((1, N, G), dtype=F16, device="cuda")
+    s[0, ::2, -1] = float("inf")
+    X = rnd((R, K), F16, 1).abs() + 0.5
+    D = pkg.w4_matmul(X, W, s, group=group, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert bool((D[:, ::2] == float("inf")).all())
+    near(D[:, 1::2], 4 * X.double().sum(1, keepdim=True).expand(R, N // 2),
+         4 * X.double().sum(1, keepdim=True).expand(R, N // 2), K + 1)
