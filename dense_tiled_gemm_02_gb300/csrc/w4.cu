@@ -215,18 +215,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps<NT>, SM_WARPS / kMaxWarps<NT>)
         }
       };
       load_tile(0, w[0]);
-      // scales and zero points: thread t of a row's four holds step t's.  Steps
-      // past K take the scale 0: their sums are zeros, and the last group's
-      // scale may be infinite.
+      // scales and zero points: thread t of a row's four holds step t's
       uint32_t sc[RT][2], z[RT][2];
-      const int step = s0 + (t < U ? t : U - 1), st = min(step, steps - 1);
+      const int st = min(s0 + (t < U ? t : U - 1), steps - 1);
       const int G = group_steps == 1 ? st : st / group_steps;
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const long long at = row0 * p.groups + (rows_on(i, h) * p.groups + G);
-          sc[i][h] = step < steps ? scale_bits(p.scales, p.scale_type, at) : 0u;
+          sc[i][h] = scale_bits(p.scales, p.scale_type, at);
           z[i][h] = p.zeros ? p.zeros[at] : 8u;
         }
       uint32_t xf[U][WPT][NT][4];
@@ -256,8 +254,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps<NT>, SM_WARPS / kMaxWarps<NT>)
           const int from = (lane & ~3) | u;
           const uint32_t zl = base + __shfl_sync(0xFFFFFFFFu, z[i][0], from) * 0x00010001u;
           const uint32_t zh = base + __shfl_sync(0xFFFFFFFFu, z[i][1], from) * 0x00010001u;
-          const float sl = scale_value(__shfl_sync(0xFFFFFFFFu, sc[i][0], from), p.scale_type);
-          const float sh = scale_value(__shfl_sync(0xFFFFFFFFu, sc[i][1], from), p.scale_type);
+          float sl = scale_value(__shfl_sync(0xFFFFFFFFu, sc[i][0], from), p.scale_type);
+          float sh = scale_value(__shfl_sync(0xFFFFFFFFu, sc[i][1], from), p.scale_type);
+          // past K: the sums are zeros, but the last group's scale may be infinite
+          if (u > 0 && s0 + u >= steps) sl = sh = 0.f;
           float part[NT][4];
 #pragma unroll
           for (int j = 0; j < NT; ++j) part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.f;
