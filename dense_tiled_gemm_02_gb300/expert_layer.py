@@ -23,7 +23,8 @@ import argparse
 import torch
 
 import dense_tiled_gemm_02_gb300 as gemm
-from dense_tiled_gemm_02_gb300.experts import GroupedGemm, Permute, Route, W4Gemm, pack_w4
+from dense_tiled_gemm_02_gb300.experts import (GroupedGemm, Permute, Route, W4Gemm, _on_one_device,
+                                               _Planned, pack_w4)
 
 
 def quantize_w4(w: torch.Tensor, group: int):
@@ -41,13 +42,26 @@ def quantize_w4(w: torch.Tensor, group: int):
     return pack_w4(q.flatten(-2)[..., :K]), scales, zeros.to(torch.uint8)
 
 
+def _sizes(router, W1, W2):
+    """(E, F, H) of a layer's weights, which must agree."""
+    E, F, H = W1.shape
+    if tuple(router.shape) != (E, H) or tuple(W2.shape) != (E, H, F):
+        raise ValueError(f"router {tuple(router.shape)} and W2 {tuple(W2.shape)} do not go with W1 "
+                         f"{tuple(W1.shape)}: {(E, H)} and {(E, H, F)} do")
+    for name, t in (("router", router), ("W1", W1), ("W2", W2)):
+        if t.dtype != W1.dtype or t.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"{name} is {t.dtype}: the weights are of one 16-bit type")
+    _on_one_device(W1.device, router=router, W2=W2)
+    return E, F, H
+
+
 class ExpertLayer:
     """The layer for T tokens in training.  router is E x H, W1 E x F x H and
     W2 E x H x F, of one 16-bit type; `grads` holds the gradients of all three
     after `backward`."""
 
     def __init__(self, tokens: int, router, W1, W2, k: int):
-        E, F, H = W1.shape
+        E, F, H = _sizes(router, W1, W2)
         T, R, dtype, dev = tokens, tokens * k, W1.dtype, W1.device
         self.router, self.W1, self.W2 = router, W1, W2
 
@@ -55,6 +69,8 @@ class ExpertLayer:
             return torch.empty(shape, dtype=dtype, device=dev)
 
         X, Y = new(T, H), new(T, H)
+        # the dense products do not look at what they are given: checked here
+        self._tokens = {name: _Planned(name, X) for name in ("X", "Y", "dY", "dX")}
         self.logits = new(T, E, dtype=torch.float32)
         self.route = Route.like(self.logits, k)
         self.experts, self.gates, self.offsets, self.row_slot, self.slot_row = self.route.outputs()
@@ -78,8 +94,13 @@ class ExpertLayer:
         self.router_dx = gemm.Gemm.like(self.dlog, router, Y, Y)
         self.router_dw = gemm.Gemm.like(self.dlog.T, X, None, g["router"])
 
+    def _check_tokens(self, **tensors) -> None:
+        for name, t in tensors.items():
+            self._tokens[name].pointer(t)
+
     def forward(self, X: torch.Tensor, Y: torch.Tensor) -> None:
         """Enqueue Y = layer(X), both T x H."""
+        self._check_tokens(X=X, Y=Y)
         self.logit_gemm.run(X, self.router.T, None, self.logits)
         self.route.run(self.logits, self.experts, self.gates, self.offsets, self.row_slot,
                        self.slot_row)
@@ -92,6 +113,7 @@ class ExpertLayer:
     def backward(self, X: torch.Tensor, dY: torch.Tensor, dX: torch.Tensor) -> None:
         """Enqueue the gradients for dY, after `forward` with this X: dX and
         `grads`."""
+        self._check_tokens(X=X, dY=dY, dX=dX)
         off, g = self.offsets, self.grads
         self.permute.combine_backward(dY, self.Ys, self.row_slot, self.slot_row, self.gates,
                                       self.dYs, self.dgates)
@@ -121,7 +143,7 @@ class ExpertDecoder:
     `step` works on the buffers X and Y; the graph is recorded by the first."""
 
     def __init__(self, tokens: int, router, W1, W2, k: int, group: int = 128):
-        E, F, H = W1.shape
+        E, F, H = _sizes(router, W1, W2)
         dtype, dev = W1.dtype, W1.device
         self.router = router
         self.w1, self.w2 = quantize_w4(W1, group), quantize_w4(W2, group)
@@ -152,6 +174,8 @@ class ExpertDecoder:
     def step(self, X: torch.Tensor) -> torch.Tensor:
         """Enqueue Y = layer(X) for T x H tokens; returns the buffer Y, which
         the next step overwrites."""
+        if X.shape != self.X.shape:
+            raise ValueError(f"X: planned for {tuple(self.X.shape)}, got {tuple(X.shape)}")
         self.X.copy_(X)
         if self._graph is None:
             side = torch.cuda.Stream(self.X.device)  # loads the kernels
