@@ -55,6 +55,14 @@ def _sizes(router, W1, W2):
     return E, F, H
 
 
+def _check(ops, what: str) -> None:
+    """Synchronise; raise if a kernel of these handles reported an error."""
+    stream = torch.cuda.current_stream()
+    for rc in [op.status(stream) for op in ops]:
+        if rc != gemm.GEMM_OK:
+            raise gemm.GemmError(rc, what)
+
+
 class ExpertLayer:
     """The layer for T tokens in training.  router is E x H, W1 E x F x H and
     W2 E x H x F, of one 16-bit type; `grads` holds the gradients of all three
@@ -131,11 +139,9 @@ class ExpertLayer:
 
     def check(self) -> None:
         """Synchronise; raise if a kernel reported an error."""
-        ops = (self.route, self.permute, self.up, self.down, self.down_dx, self.up_dx,
-               self.down_dw, self.up_dw)
-        for rc in [op.status() for op in ops]:
-            if rc != gemm.GEMM_OK:
-                raise gemm.GemmError(rc, "expert layer")
+        _check((self.logit_gemm, self.route, self.permute, self.up, self.down, self.down_dx,
+                self.up_dx, self.down_dw, self.up_dw, self.router_dx, self.router_dw),
+               "expert layer")
 
 
 class ExpertDecoder:
@@ -192,9 +198,7 @@ class ExpertDecoder:
 
     def check(self) -> None:
         """Synchronise; raise if a kernel reported an error."""
-        for rc in [op.status() for op in (self.route, self.permute, self.up, self.down)]:
-            if rc != gemm.GEMM_OK:
-                raise gemm.GemmError(rc, "expert decoder")
+        _check((self.logit_gemm, self.route, self.permute, self.up, self.down), "expert decoder")
 
 
 def random_weights(E: int, H: int, F: int, dtype=torch.bfloat16, device="cuda", seed: int = 0):

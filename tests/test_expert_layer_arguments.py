@@ -48,3 +48,26 @@ def test_tokens_of_another_shape_are_refused():
     decoder = el.ExpertDecoder(8, k=2, group=32, **w)
     with pytest.raises(ValueError, match="X: planned"):
         decoder.step(X[:1])  # copy_ would have repeated it
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["logit_gemm", "router_dx", "router_dw", "up", "down_dw"])
+def test_check_reports_every_product(name):
+    """A wait that runs out in any product of the layer reaches check()."""
+    w = el.random_weights(16, 128, 64)
+    layer = el.ExpertLayer(256, *w, 2)
+    X = torch.randn(256, 128, device="cuda").bfloat16()
+    Y, dX = torch.empty_like(X), torch.empty_like(X)
+    op = getattr(layer, name)
+    hook = op.debug_set if hasattr(op, "debug_set") else (
+        lambda flags, ns: el.gemm.gemm_debug_set(op.handle, flags, ns))
+    hook(el.gemm.GEMM_DEBUG_SKIP_FIRST_FILL, 20_000_000)
+    layer.forward(X, Y)
+    layer.backward(X, Y, dX)
+    with pytest.raises(el.gemm.GemmError) as e:
+        layer.check()
+    assert e.value.code == el.gemm.GEMM_ERR_DEVICE_TIMEOUT
+    hook(0, 0)
+    layer.forward(X, Y)
+    layer.backward(X, Y, dX)
+    layer.check()
