@@ -251,7 +251,9 @@ class GroupedGemm(_Op):
                 raise ValueError(f"A {tuple(A.shape)}, B {tuple(B.shape)} and {E} experts do not "
                                  f"give D {tuple(D.shape)}")
             N = B.shape[2]
-            if B.stride(2) == 1 or N <= 1:
+            # a single column lies along K where it can: its rows of one
+            # element would have to follow each other over all experts
+            if B.stride(2) == 1 and N > 1 or N <= 1 and B.stride(1) != 1:
                 layout, ldb = _gemm.GEMM_ROW_MAJOR, _stack_stride(B, "B")
             else:
                 layout, ldb = _gemm.GEMM_COL_MAJOR, _stack_stride(B.transpose(1, 2), "B")

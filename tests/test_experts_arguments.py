@@ -81,3 +81,15 @@ def test_pack_w4_takes_four_bits(dtype):
 def test_pack_w4_refuses_other_values(q, match):
     with pytest.raises(ValueError, match=match):
         pkg.pack_w4(q)
+
+
+@pytest.mark.parametrize("E,K,ld", [(3, 24, 32), (3, 24, 24), (1, 24, 32), (3, 1, 8), (1, 1, 1)])
+def test_grouped_takes_a_single_column_with_padding(E, K, ld):
+    """B of one column, stored along K with a gap after each expert's."""
+    t = grouped_operands(E=E, K=K, N=1)
+    t["B"] = torch.zeros(E, 1, ld, dtype=BF16)[:, :, :K].transpose(1, 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.GroupedGemm.like(**t)
+    t["B"] = torch.zeros(E, K, ld, dtype=BF16)[:, :, :1]  # or across it
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.GroupedGemm.like(**t)

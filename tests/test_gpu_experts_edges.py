@@ -228,3 +228,20 @@ def test_w4_infinite_scale_of_the_last_group(K, group, R):
     assert bool((D[:, ::2] == float("inf")).all())
     near(D[:, 1::2], 4 * X.double().sum(1, keepdim=True).expand(R, N // 2),
          4 * X.double().sum(1, keepdim=True).expand(R, N // 2), K + 1)
+
+
+@pytest.mark.parametrize("plan", ["wide=0", "wide=1"])
+@pytest.mark.parametrize("K,ld,order", [(24, 32, "nk"), (25, 25, "nk"), (24, 1, "kn"), (24, 8, "kn")])
+def test_grouped_single_column(plan, K, ld, order):
+    counts = [5, 0, 70]
+    off, E, R = offsets_of(counts), 3, 75
+    A = rnd((R, K), BF16, 1)
+    B = (rnd((E, 1, ld), BF16, 2)[:, :, :K].transpose(1, 2) if order == "nk" else
+         rnd((E, K, ld), BF16, 2)[:, :, :1])
+    D = torch.full((R, 1), 7.0, device="cuda")
+    with forced_plan(plan):
+        op = pkg.GroupedGemm.like(A, B, off, None, D)
+    op.run(A, B, off, None, D)
+    done(op)
+    ref, S = grouped_ref(A, B, off, None, False)
+    near(D, ref, S, K)
