@@ -292,6 +292,8 @@ class W4Gemm(_Op):
         pack_w4), scales and zeros (E, N, ceil(K / group)), zeros None for 8;
         offsets (E + 1) group the rows, None for E = 1."""
         R, K = X.shape
+        if group < 1:
+            raise ValueError(f"group must be a multiple of 32, got {group}")
         E, N = W.shape[:2]
         G = -(-K // group)
         if tuple(W.shape) != (E, N, K // 2) or W.dtype != torch.uint8 or not W.is_contiguous():

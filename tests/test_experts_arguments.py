@@ -93,3 +93,11 @@ def test_grouped_takes_a_single_column_with_padding(E, K, ld):
     t["B"] = torch.zeros(E, K, ld, dtype=BF16)[:, :, :1]  # or across it
     with pytest.raises(ValueError, match="CUDA"):
         pkg.GroupedGemm.like(**t)
+
+
+@pytest.mark.parametrize("group", [0, -32])
+def test_w4_group_is_positive(group):
+    t = w4_operands()
+    t["group"] = group
+    with pytest.raises(ValueError, match="group"):
+        pkg.W4Gemm.like(**t)
