@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     fence_proxy_async_smem();
   }
   if (warp == 0 && lane == 0) {
-    if (!p.grad) {
+    if (!p.grad && p.K > 0) {  // the maps of operands that are not read are not made
       tma_prefetch_desc(&tmF);
       tma_prefetch_desc(&tmX128);
       tma_prefetch_desc(&tmX32);
