@@ -3,11 +3,13 @@
 //
 //   D[r,n] = sum_groups s[n,G] * ( sum_{k in G} X[r,k] (q[n,k] - z[n,G]) )
 //
+// (a group's sum in steps of 128, 64 or 32 values, each scaled for itself)
+//
 // Bound by reading the weights once: N K / 2 bytes.  The integers q - z are
 // exact in fp16 and bf16, so the inner sum goes to the tensor core
 // (mma.sync.m16n8k16, fp32 accumulators) with the weights as its 16-row
 // operand and 8 tokens as its columns, and the scale is applied to the fp32
-// group sum: nothing is rounded before D.  (A tcgen05 tile would have to
+// sums: nothing is rounded before D.  (A tcgen05 tile would have to
 // stage the expanded weights in shared memory, four times their bytes, for
 // at most a handful of useful columns.)
 //
@@ -324,7 +326,9 @@ cudaError_t launch_as(const W4Params& p, cudaStream_t st) {
 
 template <bool BF16, int WPT>
 cudaError_t launch_wpt(const W4Params& p, cudaStream_t st) {
-  // Tokens a pass covers: as many as an expert has on average.
+  // Tokens a pass covers: as many as an expert has on average (the host does
+  // not know the groups).  Under skew the long groups take more passes, each
+  // reading the expert's weights.
   const int rows = p.E > 1 ? (p.R + p.E - 1) / p.E : p.R;
   if (rows <= 8) return launch_as<BF16, WPT, 1>(p, st);
   if (rows <= 16) return launch_as<BF16, WPT, 2>(p, st);

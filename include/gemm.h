@@ -560,9 +560,13 @@ GEMM_API int gemm_grouped_run(gemm_op_t op, const void* A, const void* B, const 
  * or BF16; D R x N (ldd), F16, BF16 or F32.  With E = 1 offsets may be NULL
  * (all R rows); otherwise they group the rows as above, and rows of no expert
  * are not written.  K and group are multiples of 32, W is 16-byte aligned and
- * so are X's rows.  Products of X with the integers q - z are summed in fp32 per
- * group, scaled in fp32, and rounded once.  Made for the few rows of a
- * decode step: the weights are read once for every 32 rows of an expert.
+ * so are X's rows.  Products of X with the integers q - z are summed in fp32
+ * within a group (128 values at a time where 128 divides the group, else 64 or
+ * 32), those sums scaled and added up in fp32, and rounded once.  Made for the
+ * few rows of a decode step: an expert's weights are read once for every 8 of
+ * its rows when R is at most 8 E, once for every 16 up to 16 E, else once for
+ * every 32.  That goes by the average over all E: an expert with most of the
+ * rows has its weights read that much more often.
  */
 typedef struct {
   int32_t E, group, has_zeros;
