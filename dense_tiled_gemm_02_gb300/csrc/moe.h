@@ -3,6 +3,8 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "common.h"
@@ -32,6 +34,14 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(one));
   return one != 0u;
 }
+
+// Element types to fp32 and back.
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void narrow(float v, float& x) { x = v; }
+__device__ __forceinline__ void narrow(float v, __half& x) { x = __float2half_rn(v); }
+__device__ __forceinline__ void narrow(float v, __nv_bfloat16& x) { x = __float2bfloat16_rn(v); }
 
 // The rows [lo, hi) of expert e; empty, with the status set, when the offsets
 // decrease or leave [0, R].

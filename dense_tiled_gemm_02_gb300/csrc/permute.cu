@@ -40,13 +40,6 @@ struct alignas(sizeof(T) * V) Pack {
   T v[V];
 };
 
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void narrow(float v, float& x) { x = v; }
-__device__ __forceinline__ void narrow(float v, __half& x) { x = __float2half_rn(v); }
-__device__ __forceinline__ void narrow(float v, __nv_bfloat16& x) { x = __float2bfloat16_rn(v); }
-
 // The sorted rows of slots j0 .. j0 + KU - 1 of token t, -1 for none (or no
 // such slot).  All indices are loaded before any is looked at: a check
 // between them (its atomic orders memory) left one index and one row load in
