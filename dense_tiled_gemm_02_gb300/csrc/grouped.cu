@@ -41,11 +41,17 @@
 // 338 us against 254 for 32 experts of 513 and of 528 rows, 2048 x 4096.)
 //
 // Measured (one GB300, bf16): 32768 rows x 4096 over 32 experts of 4096 x 4096
-// 640 us (1718 TFLOP/s, tensor-bound); weight gradients of 16384 rows, 32 of
-// 2048 x 4096, 231 us (1190 TFLOP/s; 174 without D's stores, which take the
-// same road as the next tile's operands: 537 MB of D); 64 rows over 48 of 64
-// experts of 4096 x 2048 126 us (6.4 TB/s of weights); 1000 rows, 1000 x 1000
-// over 7 of 8 experts 12 us (launch, first loads and epilogue, one wave).
+// 625 us in the first 60 calls (1759 TFLOP/s, tensor-bound), 725 us after
+// seconds of them (1517 TFLOP/s, SM clock 1.41 GHz under the 1400 W cap; a
+// cuBLAS product loses as much); with an N-contiguous B 681, with fp32 D 707
+// against 640 in the same run; weight gradients of 16384 rows, 32 of 2048 x
+// 4096, 229 and 241 us (1200, 1140 TFLOP/s; 174 without D's stores, which take
+// the same road as the next tile's operands: 537 MB of D); 64 rows over 48 of
+// 64 experts of 4096 x 2048 126 us (6.4 TB/s of weights); 1000 rows, 1000 x
+// 1000 over 7 of 8 experts 11.5-13.5 us (launch, first loads and epilogue, 168
+// tiles on 152 SMs).  C and fp32 D are read and stored by the threads, a row of
+// D at a time: the first case with C takes 1916 us, the gradients into fp32 D
+// 418, and added up there (C = D) 3217.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -11,7 +11,7 @@
 // k rows that use them, and the k sums need no atomics: a fixed order, the
 // same bits every time.  Rows move in 16-byte units where their addresses
 // allow it, else element by element.  16384 tokens x 4 rows of 4096 bf16, both
-// ways with gradients: 515 us for 2.7 GB (5.2 TB/s).  A decode step (16 tokens
+// ways with gradients: 511 us for 2.7 GB (5.3 TB/s).  A decode step (16 tokens
 // x 8 rows) is bound by its two calls.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -77,7 +77,7 @@ __device__ __forceinline__ Pack<T, V> zeros() {
 }
 
 // blockIdx.x: token and chunk of THREADS * V columns.  16384 tokens x 4 rows
-// of 4096 bf16: 97 us (6.9 TB/s).
+// of 4096 bf16: 99 us (6.8 TB/s).
 template <typename T, int V, int KU>
 __global__ void __launch_bounds__(THREADS) gather_kernel(const PermuteParams p, int chunks) {
   using P = Pack<T, V>;

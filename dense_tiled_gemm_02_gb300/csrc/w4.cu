@@ -25,9 +25,11 @@
 // 16-row tiles, and add their sums in shared memory in warp order:
 // deterministic.
 //
-// Measured (one GB300): 4 x 8192 x 32768, groups of 128: 39 us (3.5 TB/s),
+// Measured (one GB300): 4 x 8192 x 32768, groups of 128: 40 us (3.5 TB/s),
 // 16 x 8192 x 8192, groups of 64: 21 us (45 with X loaded for every 16 rows),
-// 64 rows over 40 experts of 4096 x 2048: 49 us.  No unit is more than half
+// 64 rows over 40 experts of 4096 x 2048: 49 us (over 2 of 64 experts 34, on
+// one 53: eight passes over its weights).  A prompt is not what this is for:
+// 2048 x 4096 x 4096 takes 720 us, 64 passes.  No unit is more than half
 // busy (logic 49%, L1 47%, issue 40% at the first case; the loads alone, with
 // as many in flight, run at 6.2 TB/s): what bounds it is the time between a
 // run's loads and its arithmetic, with 16 warps an SM to cover it (the
