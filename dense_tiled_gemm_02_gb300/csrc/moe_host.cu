@@ -10,7 +10,6 @@
 #include <cstdlib>
 #include <cstring>
 #include <new>
-#include <string>
 
 #include "clear.h"
 #include "common.h"
@@ -47,7 +46,7 @@ struct gemm_op {
   uint32_t* status = nullptr;
   uint64_t timeout_ns = kDefaultTimeoutNs;
   int debug_flags = 0;
-  std::string plan;
+  char plan[192] = "";  // not a string: its allocation could throw out of a C entry
   // grouped: operands copied to workspace rows the TMA unit can read
   bool copy_a = false, copy_b = false;
   int64_t a_rows = 0, a_cols = 0, b_rows = 0, b_cols = 0;
@@ -178,8 +177,8 @@ int64_t gemm_op_workspace_bytes(gemm_op_t op) {
 
 int gemm_op_plan_string(gemm_op_t op, char* buf, size_t n) {
   if (!op) return GEMM_ERR_INVALID_ARG;
-  if (buf && n) std::snprintf(buf, n, "%s", op->plan.c_str());
-  return static_cast<int>(op->plan.size());
+  if (buf && n) std::snprintf(buf, n, "%s", op->plan);
+  return static_cast<int>(std::strlen(op->plan));
 }
 
 int gemm_op_debug_set(gemm_op_t op, int flags, uint64_t timeout_ns) {
@@ -209,8 +208,8 @@ int gemm_route_create(gemm_op_t* out, const gemm_route_desc_t* desc) {
   if (rc != GEMM_OK) return rc;
   op->route = d;
   op->grid = blocks;
-  op->plan = "route T=" + std::to_string(d.T) + " E=" + std::to_string(d.E) +
-             " k=" + std::to_string(d.k) + " blocks=" + std::to_string(blocks);
+  std::snprintf(op->plan, sizeof op->plan, "route T=%lld E=%d k=%d blocks=%d",
+                static_cast<long long>(d.T), d.E, d.k, blocks);
   *out = op;
   return GEMM_OK;
 }
@@ -286,8 +285,8 @@ int gemm_permute_create(gemm_op_t* out, const gemm_permute_desc_t* desc) {
   const int rc = make_op(Kind::kPermute, 0, 0, 0, &op);
   if (rc != GEMM_OK) return rc;
   op->permute = d;
-  op->plan = "permute T=" + std::to_string(d.T) + " k=" + std::to_string(d.k) +
-             " H=" + std::to_string(d.H);
+  std::snprintf(op->plan, sizeof op->plan, "permute T=%lld k=%d H=%lld",
+                static_cast<long long>(d.T), d.k, static_cast<long long>(d.H));
   *out = op;
   return GEMM_OK;
 }
@@ -455,12 +454,10 @@ int gemm_grouped_create(gemm_op_t* out, const gemm_grouped_desc_t* desc) {
   op->ws_lda = copy_a ? ws_lda : d.lda;
   op->ws_ldb = copy_b ? ws_ldb : d.ldb;
   op->ws_b_off = a_bytes;
-  char buf[160];
-  std::snprintf(buf, sizeof buf, "grouped form=%s E=%d R=%lld K=%lld N=%lld wide=%d copy=%d%d units=%d",
+  std::snprintf(op->plan, sizeof op->plan, "grouped form=%s E=%d R=%lld K=%lld N=%lld wide=%d copy=%d%d units=%d",
                 grad ? "grad" : "rows", d.E, static_cast<long long>(d.R),
                 static_cast<long long>(d.K), static_cast<long long>(d.N), wide, copy_a, copy_b,
                 op->units);
-  op->plan = buf;
   *out = op;
   return GEMM_OK;
 }
@@ -558,11 +555,9 @@ int gemm_w4_create(gemm_op_t* out, const gemm_w4_desc_t* desc) {
   const int rc = make_op(Kind::kW4, 0, 0, 0, &op);
   if (rc != GEMM_OK) return rc;
   op->w4 = d;
-  char buf[160];
-  std::snprintf(buf, sizeof buf, "w4 E=%d R=%lld K=%lld N=%lld group=%d zeros=%d", d.E,
+  std::snprintf(op->plan, sizeof op->plan, "w4 E=%d R=%lld K=%lld N=%lld group=%d zeros=%d", d.E,
                 static_cast<long long>(d.R), static_cast<long long>(d.K),
                 static_cast<long long>(d.N), d.group, d.has_zeros != 0);
-  op->plan = buf;
   *out = op;
   return GEMM_OK;
 }

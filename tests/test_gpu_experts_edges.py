@@ -245,3 +245,24 @@ def test_grouped_single_column(plan, K, ld, order):
     done(op)
     ref, S = grouped_ref(A, B, off, None, False)
     near(D, ref, S, K)
+
+
+# ---------------------------------------------------------------- handles
+def test_plan_strings_are_whole():
+    logits = torch.zeros((100_000, 1024), dtype=BF16, device="cuda")
+    slot_row = torch.zeros((100_000, 32), dtype=torch.int32, device="cuda")
+    X = torch.zeros((100_000, 8), dtype=BF16, device="cuda")
+    off = offsets_of([0] * 1024)
+    A, B = X[:, :8], torch.zeros((1024, 8, 16), dtype=BF16, device="cuda")
+    D = torch.zeros((100_000, 16), dtype=BF16, device="cuda")
+    W = torch.zeros((1024, 16, 16), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((1024, 16, 1), dtype=BF16, device="cuda")
+    for op, want in (
+            (pkg.Route.like(logits, 32), "route T=100000 E=1024 k=32 blocks="),
+            (pkg.Permute.like(X, slot_row), "permute T=100000 k=32 H=8"),
+            (pkg.GroupedGemm.like(A, B, off, None, D), "grouped form=rows E=1024 R=100000 K=8 N=16 "),
+            (pkg.W4Gemm.like(torch.zeros((100_000, 32), dtype=BF16, device="cuda"), W, s, None, off,
+                             D, 32), "w4 E=1024 R=100000 K=32 N=16 group=32 zeros=0")):
+        assert op.plan().startswith(want), op.plan()
+        assert pkg.load().gemm_op_plan_string(op.handle, None, 0) == len(op.plan())
+        done(op)
