@@ -15,7 +15,8 @@ Low-level names mirror ``include/gemm.h``: ``gemm_create``, ``gemm_run``,
 ``gemm_noalloc_status``, ``gemm_run_mx``, ``gemm_trace_set``.
 ``Gemm`` wraps a handle for torch tensors.  The operators of
 mixture-of-experts layers and of 4-bit weights (``Route``, ``Permute``,
-``GroupedGemm``, ``W4Gemm``) are in ``experts.py``.
+``GroupedGemm``, ``W4Gemm``) are in ``experts.py``, those on rows held in 8
+bits (``RmsNorm``, ``Rows8``, ``Rows8Grad``, ``I8Gemm``) in ``rows.py``.
 """
 from __future__ import annotations
 
@@ -48,7 +49,9 @@ EXPORTED = ["gemm_create", "gemm_run", "gemm_get_status", "gemm_destroy", "gemm_
             "gemm_op_debug_set", "gemm_route_create", "gemm_route_run", "gemm_route_backward",
             "gemm_permute_create", "gemm_permute_gather", "gemm_permute_combine",
             "gemm_permute_combine_backward", "gemm_grouped_create", "gemm_grouped_run",
-            "gemm_w4_create", "gemm_w4_run"]
+            "gemm_w4_create", "gemm_w4_run", "gemm_norm_create", "gemm_norm_run",
+            "gemm_norm_backward", "gemm_rows8_create", "gemm_rows8_pack", "gemm_rows8_unpack",
+            "gemm_rows8_grad_create", "gemm_rows8_grad_run", "gemm_i8_create", "gemm_i8_run"]
 GEMM_TRACE_EVENTS = 32
 GEMM_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -86,6 +89,31 @@ class W4Desc(ctypes.Structure):
                 ("R", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("x_type", ctypes.c_int), ("scale_type", ctypes.c_int), ("d_type", ctypes.c_int),
                 ("ldx", ctypes.c_int64), ("ldd", ctypes.c_int64)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("type", ctypes.c_int),
+                ("weight_type", ctypes.c_int), ("y_type", ctypes.c_int),
+                ("residual", ctypes.c_int32), ("eps", ctypes.c_float), ("ldx", ctypes.c_int64),
+                ("ldr", ctypes.c_int64), ("ldh", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class Rows8Desc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("type", ctypes.c_int),
+                ("block", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldq", ctypes.c_int64)]
+
+
+class Rows8GradDesc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("R", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("b_type", ctypes.c_int), ("c_type", ctypes.c_int),
+                ("d_type", ctypes.c_int), ("ldq", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldc", ctypes.c_int64), ("ldd", ctypes.c_int64)]
+
+
+class I8Desc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("R", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("d_type", ctypes.c_int), ("ldx", ctypes.c_int64),
+                ("ldw", ctypes.c_int64), ("ldd", ctypes.c_int64)]
 
 
 class GemmError(RuntimeError):
@@ -154,12 +182,16 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
                                         ctypes.POINTER(vp), ctypes.POINTER(vp), vp]
     lib.gemm_run_host_batch.restype = ci
     for name, desc in (("gemm_route_create", RouteDesc), ("gemm_permute_create", PermuteDesc),
-                       ("gemm_grouped_create", GroupedDesc), ("gemm_w4_create", W4Desc)):
+                       ("gemm_grouped_create", GroupedDesc), ("gemm_w4_create", W4Desc),
+                       ("gemm_norm_create", NormDesc), ("gemm_rows8_create", Rows8Desc),
+                       ("gemm_rows8_grad_create", Rows8GradDesc), ("gemm_i8_create", I8Desc)):
         getattr(lib, name).argtypes = [ctypes.POINTER(vp), ctypes.POINTER(desc)]
     for name, pointers in (("gemm_route_run", 6), ("gemm_route_backward", 5),
                            ("gemm_permute_gather", 4), ("gemm_permute_combine", 4),
                            ("gemm_permute_combine_backward", 7), ("gemm_grouped_run", 5),
-                           ("gemm_w4_run", 6)):
+                           ("gemm_w4_run", 6), ("gemm_norm_run", 7), ("gemm_norm_backward", 8),
+                           ("gemm_rows8_pack", 3), ("gemm_rows8_unpack", 3),
+                           ("gemm_rows8_grad_run", 6), ("gemm_i8_run", 6)):
         # handle, operands, stream
         getattr(lib, name).argtypes = [vp] * (pointers + 2)
         getattr(lib, name).restype = ci
@@ -481,9 +513,15 @@ def matmul_add(A, B, C=None, out_dtype=None, D=None, stream=None):
 _EXPERTS = ("GroupedGemm", "Permute", "Route", "W4Gemm", "grouped_matmul", "pack_w4", "w4_matmul")
 
 
+_ROWS = ("I8Gemm", "RmsNorm", "Rows8", "Rows8Grad", "i8_matmul")
+
+
 def __getattr__(name):
-    # experts.py needs torch at import; this module does not
+    # these modules need torch at import; this one does not
     if name in _EXPERTS:
         from . import experts
         return getattr(experts, name)
+    if name in _ROWS:
+        from . import rows
+        return getattr(rows, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -42,6 +42,10 @@ UNITS = [
     ("permute.cu", [], "permute.o"),
     ("grouped.cu", [], "grouped.o"),
     ("w4.cu", [], "w4.o"),
+    ("rows_host.cu", [], "rows_host.o"),
+    ("norm.cu", [], "norm.o"),
+    ("rows8.cu", [], "rows8.o"),
+    ("i8_rows.cu", [], "i8_rows.o"),
 ]
 
 

@@ -1,4 +1,4 @@
-// clear.h -- zeroing of a handle's device memory at its creation.
+// clear.h -- zeroing and first values of a handle's device memory at its creation.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -23,6 +23,18 @@ inline cudaError_t clear_now(std::initializer_list<Clear> ranges) {
   if (e != cudaSuccess) return e;
   for (const Clear& r : ranges)
     if (e == cudaSuccess && r.bytes) e = cudaMemsetAsync(r.at, 0, r.bytes, st);
+  const cudaError_t done = cudaStreamSynchronize(st);
+  cudaStreamDestroy(st);
+  return e != cudaSuccess ? e : done;
+}
+
+// Copies host bytes to the device before it returns (cudaMemcpy may return with
+// the last of the copy still under way on the null stream).
+inline cudaError_t write_now(void* at, const void* from, size_t bytes) {
+  cudaStream_t st;
+  cudaError_t e = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyAsync(at, from, bytes, cudaMemcpyHostToDevice, st);
   const cudaError_t done = cudaStreamSynchronize(st);
   cudaStreamDestroy(st);
   return e != cudaSuccess ? e : done;

@@ -1,0 +1,205 @@
+// i8_rows.cu -- few rows times weights of 8-bit integers, with a scale for each
+// row and each output; dense or grouped by expert.
+//
+//   D[r,n] = x_scales[r] w_scales[e,n] sum_k X[r,k] W_e[n,k]
+//
+// Bound by reading the weights once: N K bytes.  The integer matrix instruction
+// (mma.sync.m16n8k32.s32.s8.s8.s32) takes the bytes as they are loaded, the
+// weights as its 16-row operand and 8 rows of X as its columns, and its sums
+// are exact.  Because a sum over K may take K in any order, the fragment's K
+// positions are given to whatever the loads bring: thread (g, t) of a warp (g =
+// lane / 4, t = lane % 4) loads the 16 bytes at 64 s + 16 t of weight rows g
+// and g + 8 and of X's row g, which are two instructions' fragments.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "moe.h"
+#include "ptx.cuh"
+#include "rows.h"
+#include "tc_launch.h"
+
+namespace gb300 {
+
+namespace {
+
+constexpr int STEP = 64;  // K of a step
+constexpr int SM_WARPS = 16;
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 load16(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// 16 bytes from any address, of which the first n (1 to 16) are the operand's:
+// the aligned 16-byte units that hold these, shifted together.  (A unit that
+// holds a byte of an allocation is within it.)
+__device__ __forceinline__ uint4 load16_at(const int8_t* p, int n) {
+  const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint4* const unit = reinterpret_cast<const uint4*>(p - s);
+  const uint4 a = __ldg(unit);
+  uint4 b = make_uint4(0u, 0u, 0u, 0u);
+  if (static_cast<int>(s) + n > 16) b = __ldg(unit + 1);
+  const bool by8 = s & 8u, by4 = s & 4u;
+  const uint32_t w[6] = {by8 ? a.z : a.x, by8 ? a.w : a.y, by8 ? b.x : a.z,
+                         by8 ? b.y : a.w, by8 ? b.z : b.x, by8 ? b.w : b.y};
+  const uint32_t v[5] = {by4 ? w[1] : w[0], by4 ? w[2] : w[1], by4 ? w[3] : w[2],
+                         by4 ? w[4] : w[3], by4 ? w[5] : w[4]};
+  const uint32_t sh = 8u * (s & 3u);
+  return make_uint4(__funnelshift_r(v[0], v[1], sh), __funnelshift_r(v[1], v[2], sh),
+                    __funnelshift_r(v[2], v[3], sh), __funnelshift_r(v[3], v[4], sh));
+}
+
+// The first n of a word's bytes, zeros after them.
+__device__ __forceinline__ uint32_t first_bytes(uint32_t w, int n) {
+  return n >= 4 ? w : n <= 0 ? 0u : w & (0xFFFFFFFFu >> (32 - 8 * n));
+}
+
+__device__ __forceinline__ void store_d(void* d, int type, long long i, float v) {
+  if (type == T_F32)
+    static_cast<float*>(d)[i] = v;
+  else if (type == T_BF16)
+    static_cast<__nv_bfloat16*>(d)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(d)[i] = __float2half_rn(v);
+}
+
+// RT 16-row weight tiles a warp takes against NT tiles of 8 rows; U steps in
+// flight.  ALIGNED: rows of X and W are 16-byte multiples apart and start so.
+template <int RT, int NT, bool ALIGNED>
+__global__ void __launch_bounds__(32 * SM_WARPS, 1) i8_rows_kernel(const I8RowsParams p) {
+  constexpr int U = RT == 1 ? 4 : 2;
+  __shared__ int red[SM_WARPS][16 * RT][8 * NT + 1];
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+  int e = 0, r0 = 0, r1 = p.R;
+  if (p.offsets) {
+    e = p.E > 1 ? nth_expert(p.offsets, p.E, p.R, p.status, blockIdx.y) : 0;
+    if (e < 0) return;
+    const int2 r = expert_rows(p.offsets, e, p.R, p.status);
+    r0 = r.x;
+    r1 = r.y;
+  }
+  const int n0 = blockIdx.x * 16 * RT;
+  // this thread's first weight row, and how far on the others are; rows past
+  // N read the first again and are not stored
+  const int left = p.N - n0 - g;
+  const int8_t* const w0 =
+      p.W + (static_cast<long long>(e) * p.N + n0 + (left > 0 ? g : 0)) * p.ldw + 16 * t;
+  auto rows_on = [&](int i, int h) { return 16 * i + 8 * h < left ? 16 * i + 8 * h : 0; };
+  const int steps = (p.K + STEP - 1) / STEP;
+  for (int rb = r0; rb < r1; rb += 8 * NT) {
+    int acc[RT][NT][4] = {};
+    for (int s0 = warp * U; s0 < steps; s0 += warps * U) {
+      uint4 w[RT][2][U], x[NT][U];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int8_t* const src = w0 + rows_on(i, h) * p.ldw + s0 * STEP;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int k = (s0 + u) * STEP + 16 * t;
+            w[i][h][u] = make_uint4(0u, 0u, 0u, 0u);
+            if (k < p.K)
+              w[i][h][u] = ALIGNED ? load16(src + u * STEP) : load16_at(src + u * STEP, min(16, p.K - k));
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int r = rb + 8 * j + g;
+        const int8_t* const src = p.X + (r < r1 ? r : rb) * p.ldx + s0 * STEP + 16 * t;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int k = (s0 + u) * STEP + 16 * t;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (r < r1 && k < p.K) {
+            if constexpr (ALIGNED) {
+              v = __ldg(reinterpret_cast<const uint4*>(src + u * STEP));
+            } else {
+              const int n = min(16, p.K - k);  // what follows in W meets zeros here
+              v = load16_at(src + u * STEP, n);
+              v = make_uint4(first_bytes(v.x, n), first_bytes(v.y, n - 4), first_bytes(v.z, n - 8),
+                             first_bytes(v.w, n - 12));
+            }
+          }
+          x[j][u] = v;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma_s8(acc[i][j], w[i][0][u].x, w[i][1][u].x, w[i][0][u].y, w[i][1][u].y, x[j][u].x,
+                   x[j][u].y);
+            mma_s8(acc[i][j], w[i][0][u].z, w[i][1][u].z, w[i][0][u].w, w[i][1][u].w, x[j][u].z,
+                   x[j][u].w);
+          }
+    }
+    __syncthreads();  // the previous rows' sums have been read
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          red[warp][16 * i + g + 8 * (q >> 1)][8 * j + 2 * t + (q & 1)] = acc[i][j][q];
+    __syncthreads();
+    for (int o = threadIdx.x; o < 16 * RT * 8 * NT; o += blockDim.x) {
+      const int n = o % (16 * RT), m = o / (16 * RT);
+      if (rb + m < r1 && n0 + n < p.N) {
+        int v = 0;
+        for (int y = 0; y < warps; ++y) v += red[y][n][m];
+        store_d(p.D, p.d_type, (rb + m) * p.ldd + n0 + n,
+                static_cast<float>(v) * p.x_scales[rb + m] *
+                    p.w_scales[static_cast<long long>(e) * p.N + n0 + n]);
+      }
+    }
+  }
+}
+
+template <int RT, int NT, bool ALIGNED>
+cudaError_t launch_as(const I8RowsParams& p, cudaStream_t st) {
+  const int tiles = (p.N + 16 * RT - 1) / (16 * RT), experts = p.E > 1 ? std::min(p.E, p.R) : 1;
+  const int steps = (p.K + STEP - 1) / STEP;
+  int warps = 4;
+  while (warps < SM_WARPS && 2 * warps <= steps / 2 &&
+         static_cast<long long>(tiles) * experts * warps < SM_WARPS * p.num_sms)
+    warps *= 2;
+  return launch_pdl(i8_rows_kernel<RT, NT, ALIGNED>, dim3(tiles, experts), dim3(32 * warps), 0, st, p);
+}
+
+template <bool ALIGNED>
+cudaError_t launch_rows(const I8RowsParams& p, cudaStream_t st) {
+  const int rows = p.E > 1 ? (p.R + p.E - 1) / p.E : p.R;
+  return rows <= 8 ? launch_as<1, 1, ALIGNED>(p, st) : launch_as<1, 2, ALIGNED>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_i8_rows(const I8RowsParams& p, cudaStream_t st) {
+  const bool aligned = p.K % 16 == 0 && p.ldx % 16 == 0 && p.ldw % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(p.X) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(p.W) % 16 == 0;
+  return aligned ? launch_rows<true>(p, st) : launch_rows<false>(p, st);
+}
+
+}  // namespace gb300

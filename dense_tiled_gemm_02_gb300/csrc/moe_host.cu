@@ -7,141 +7,21 @@
 #include <algorithm>
 #include <climits>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
-#include <new>
 
-#include "clear.h"
 #include "common.h"
 #include "gemm.h"
 #include "moe.h"
+#include "op.h"
 #include "tc_launch.h"
 
 using namespace gb300;
-
-namespace {
-
-enum class Kind { kRoute, kPermute, kGrouped, kW4 };
-
-constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;  // 2 s per device-side wait
-constexpr size_t kStatusBytes = 256;
-
-bool is_16bit(int t) { return t == T_F16 || t == T_BF16; }
-bool is_float(int t) { return is_16bit(t) || t == T_F32; }
-int64_t elem_size(int t) { return t == T_F32 ? 4 : 2; }
-int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-bool aligned(const void* p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-}  // namespace
-
-struct gemm_op {
-  Kind kind;
-  int device = 0, num_sms = 0;
-  gemm_route_desc_t route{};
-  gemm_permute_desc_t permute{};
-  gemm_grouped_desc_t grouped{};
-  gemm_w4_desc_t w4{};
-  void* ws = nullptr;
-  size_t ws_bytes = 0;
-  uint32_t* status = nullptr;
-  uint64_t timeout_ns = kDefaultTimeoutNs;
-  int debug_flags = 0;
-  char plan[192] = "";  // not a string: its allocation could throw out of a C entry
-  // grouped: operands copied to workspace rows the TMA unit can read
-  bool copy_a = false, copy_b = false;
-  int64_t a_rows = 0, a_cols = 0, b_rows = 0, b_cols = 0;
-  int64_t ws_lda = 0, ws_ldb = 0;
-  size_t ws_b_off = 0, ws_partial_off = 0, ws_counters_off = 0, ws_maps_off = 0;
-  size_t counters_bytes = 0;
-  bool wide = false;
-  int units = 0;
-  int grid = 0;  // route: blocks
-};
-
-namespace {
-
-// The plan's choice for `key`, unless GEMM_FORCE_PLAN="key=0|1,..." names it.
-bool planned(const char* key, bool choice) {
-  const char* env = std::getenv("GEMM_FORCE_PLAN");
-  const size_t n = std::strlen(key);
-  for (const char* s = env; s && *s; s = std::strchr(s, ',')) {
-    if (*s == ',') ++s;
-    if (std::strncmp(s, key, n) == 0 && s[n] == '=') return s[n + 1] != '0';
-  }
-  return choice;
-}
-
-// Handle of a kind on the current device with `ws_bytes` of workspace, of which
-// [zero_off, zero_off + zero_bytes) starts as zeros.
-int make_op(Kind kind, size_t ws_bytes, size_t zero_off, size_t zero_bytes, gemm_op** out) {
-  int dev = 0, major = 0, minor = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_NO_DEVICE;
-  }
-  if (major != 10 || minor != 3) return GEMM_ERR_NO_DEVICE;
-  gemm_op* op = new (std::nothrow) gemm_op();
-  if (!op) return GEMM_ERR_ALLOC_FAILED;
-  op->kind = kind;
-  op->device = dev;
-  op->num_sms = sms;
-  op->ws_bytes = ws_bytes;
-  if (cudaMalloc(&op->status, kStatusBytes) != cudaSuccess ||
-      (ws_bytes && cudaMalloc(&op->ws, ws_bytes) != cudaSuccess) ||
-      clear_now({{op->status, kStatusBytes},
-                 {static_cast<uint8_t*>(op->ws) + zero_off, zero_bytes}}) != cudaSuccess) {
-    cudaGetLastError();
-    if (op->ws) cudaFree(op->ws);
-    if (op->status) cudaFree(op->status);
-    delete op;
-    return GEMM_ERR_ALLOC_FAILED;
-  }
-  *out = op;
-  return GEMM_OK;
-}
-
-bool usable(const gemm_op* op, Kind kind) {
-  int dev = -1;
-  return op && op->kind == kind && cudaGetDevice(&dev) == cudaSuccess && dev == op->device;
-}
-
-int launched(cudaError_t e) {
-  if (e == cudaSuccess) return GEMM_OK;
-  cudaGetLastError();
-  return GEMM_ERR_CUDA;
-}
-
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Map of a row-major 16-bit operand, 128-byte swizzled boxes of box_cols x
-// box_rows, zeros outside.  depth > 0: that many matrices of `rows` rows one
-// after another, as a third dimension.
-bool encode_rows(CUtensorMap* tm, const void* base, int64_t ld, int64_t cols, int64_t rows,
-                 int64_t depth, int box_cols, int box_rows) {
-  EncodeFn enc = reinterpret_cast<EncodeFn>(tensor_map_encoder());
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(ld * rows) * 2};
-  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, depth > 0 ? 3 : 2, const_cast<void*>(base), dims,
-             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-}  // namespace
 
 extern "C" {
 
 int gemm_op_status(gemm_op_t op, gemm_stream_t stream) {
   if (!op) return GEMM_ERR_INVALID_ARG;
+  if (op->inner) return gemm_op_status(op->inner, stream);  // what it ends in has the kernels that report
   // all on the caller's stream: what was cleared on another one could be
   // cleared after the next run had set it
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -165,6 +45,7 @@ int gemm_op_status(gemm_op_t op, gemm_stream_t stream) {
 int gemm_op_destroy(gemm_op_t op) {
   if (!op) return GEMM_OK;
   const int rc = cudaDeviceSynchronize() == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  gemm_op_destroy(op->inner);
   if (op->ws) cudaFree(op->ws);
   if (op->status) cudaFree(op->status);
   delete op;
@@ -172,7 +53,8 @@ int gemm_op_destroy(gemm_op_t op) {
 }
 
 int64_t gemm_op_workspace_bytes(gemm_op_t op) {
-  return op ? static_cast<int64_t>(op->ws_bytes) : -1;
+  if (!op) return -1;
+  return static_cast<int64_t>(op->ws_bytes + (op->inner ? op->inner->ws_bytes : 0));
 }
 
 int gemm_op_plan_string(gemm_op_t op, char* buf, size_t n) {
@@ -183,6 +65,7 @@ int gemm_op_plan_string(gemm_op_t op, char* buf, size_t n) {
 
 int gemm_op_debug_set(gemm_op_t op, int flags, uint64_t timeout_ns) {
   if (!op) return GEMM_ERR_INVALID_ARG;
+  if (op->inner) return gemm_op_debug_set(op->inner, flags, timeout_ns);
   op->debug_flags = flags;
   op->timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
   return GEMM_OK;
@@ -306,15 +189,6 @@ PermuteParams permute_params(const gemm_op* op) {
   p.ld_rows = d.ld_rows;
   p.status = op->status;
   return p;
-}
-
-// GEMM_OK when every pointer is present and aligned to n bytes.
-int check_pointers(std::initializer_list<const void*> ptrs, int64_t n) {
-  for (const void* q : ptrs)
-    if (!q) return GEMM_ERR_INVALID_ARG;
-  for (const void* q : ptrs)
-    if (!aligned(q, n)) return GEMM_ERR_MISALIGNED;
-  return GEMM_OK;
 }
 
 }  // namespace

@@ -1,0 +1,79 @@
+// rows.h -- parameters and launches of the operators on rows held in 8 bits
+// (norm.cu, rows8.cu, i8_rows.cu), used by rows_host.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.h"
+
+namespace gb300 {
+
+constexpr int ROW_BLOCK = 32;  // values that share an exponent
+
+// ---------------------------------------------------------------- norm (norm.cu)
+struct NormParams {
+  long long T;
+  int H, type, weight_type, i8;
+  float eps;
+  long long ldx, ldr, ldh, ldy;
+  const void* x;
+  const void* residual;  // null: h is x
+  const void* weight;
+  void* h;
+  void* y;
+  float* scales;
+  float* rstd;  // may be null
+};
+cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t st);
+
+struct NormBackwardParams {
+  long long T;
+  int H, type, weight_type;
+  long long ldy, ldh, ldr, ldx;  // dy, h, dresidual, dx
+  const void* dy;
+  const void* h;      // of type, or int8 when E
+  const uint8_t* E;   // null: h is of type
+  const void* weight;
+  const float* rstd;
+  const void* dresidual;  // may be null
+  void* dx;
+  float* dweight;     // may be null
+  float* partial;     // norm_partial_rows() x H
+};
+// Blocks of the backward kernel, each of which leaves a row of partial sums of dweight.
+int norm_partial_rows(long long T, int num_sms);
+cudaError_t launch_norm_backward(const NormBackwardParams& p, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- rows to 8 bits (rows8.cu)
+struct Rows8Params {
+  long long T;
+  int H, type, block;
+  long long ldx, ldq;
+  const void* X;
+  void* X_out;
+  const int8_t* q;
+  int8_t* q_out;
+  const void* scales;
+  void* scales_out;
+};
+cudaError_t launch_rows8_pack(const Rows8Params& p, int num_sms, cudaStream_t st);
+cudaError_t launch_rows8_unpack(const Rows8Params& p, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- products (i8_rows.cu)
+struct I8RowsParams {
+  int E, R, K, N, d_type;
+  long long ldx, ldw, ldd;
+  const int8_t* X;
+  const float* x_scales;
+  const int8_t* W;
+  const float* w_scales;
+  const int* offsets;  // null: all rows to expert 0
+  void* D;
+  uint32_t* status;
+  int num_sms;
+};
+cudaError_t launch_i8_rows(const I8RowsParams& p, cudaStream_t st);
+
+}  // namespace gb300

@@ -1,0 +1,319 @@
+// rows_host.cu -- C ABI of the operators on rows held in 8 bits: validation,
+// handles and launches.  See include/gemm.h for the contract of each entry.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdio>
+
+#include "op.h"
+#include "rows.h"
+
+using namespace gb300;
+
+namespace {
+
+// Leading dimension 0 is packed; false for one below that.
+bool settle(int64_t& ld, int64_t cols) {
+  if (ld == 0) ld = std::max<int64_t>(cols, 1);
+  return ld >= cols;
+}
+
+int64_t blocks_of(int64_t n) { return (n + ROW_BLOCK - 1) / ROW_BLOCK; }
+
+}  // namespace
+
+extern "C" {
+
+// ---------------------------------------------------------------- norm
+int gemm_norm_create(gemm_op_t* out, const gemm_norm_desc_t* desc) {
+  if (!out || !desc) return GEMM_ERR_INVALID_ARG;
+  gemm_norm_desc_t d = *desc;
+  d.residual = d.residual != 0;
+  if (d.T < 0 || d.H < 0 || d.T > INT_MAX / 2 || d.H > INT_MAX / 2 || !settle(d.ldx, d.H) ||
+      !settle(d.ldr, d.H) || !settle(d.ldh, d.H) || !settle(d.ldy, d.H) || !std::isfinite(d.eps) ||
+      d.eps < 0)
+    return GEMM_ERR_INVALID_ARG;
+  if (!is_float(d.type) || (d.weight_type != d.type && d.weight_type != GEMM_F32) ||
+      (d.y_type != d.type && d.y_type != GEMM_I8))
+    return GEMM_ERR_UNSUPPORTED;
+  if (!d.residual) d.ldr = d.ldh = d.ldx;  // h is x
+  int sms = 1, dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaGetLastError();
+  // partial sums of dweight; a norm out in 8 bits has no backward pass
+  const size_t partial =
+      d.y_type == GEMM_I8 ? 0 : sizeof(float) * norm_partial_rows(d.T, std::max(sms, 1)) * static_cast<size_t>(d.H);
+  gemm_op* op = nullptr;
+  const int rc = make_op(Kind::kNorm, partial, 0, 0, &op);
+  if (rc != GEMM_OK) return rc;
+  op->norm = d;
+  std::snprintf(op->plan, sizeof op->plan, "norm T=%lld H=%lld residual=%d out=%s",
+                static_cast<long long>(d.T), static_cast<long long>(d.H), d.residual,
+                d.y_type == GEMM_I8 ? "i8" : "x");
+  *out = op;
+  return GEMM_OK;
+}
+
+int gemm_norm_run(gemm_op_t op, const void* x, const void* residual, const void* weight, void* h,
+                  void* y, float* scales, float* rstd, gemm_stream_t stream) {
+  if (!usable(op, Kind::kNorm)) return GEMM_ERR_INVALID_ARG;
+  const gemm_norm_desc_t& d = op->norm;
+  const bool i8 = d.y_type == GEMM_I8;
+  if (d.T == 0 || d.H == 0) return GEMM_OK;
+  const int64_t s = elem_size(d.type);
+  int rc = check_pointers({x}, s);
+  if (rc == GEMM_OK) rc = check_pointers({weight}, elem_size(d.weight_type));
+  if (rc == GEMM_OK) rc = check_pointers({y}, i8 ? 1 : s);
+  if (rc == GEMM_OK && d.residual) rc = check_pointers({residual, h}, s);
+  if (rc == GEMM_OK && i8) rc = check_pointers({scales}, 4);
+  if (rc != GEMM_OK) return rc;
+  if (!aligned(rstd, 4)) return GEMM_ERR_MISALIGNED;
+  NormParams p{};
+  p.T = d.T;
+  p.H = static_cast<int>(d.H);
+  p.type = d.type;
+  p.weight_type = d.weight_type;
+  p.i8 = i8;
+  p.eps = d.eps;
+  p.ldx = d.ldx;
+  p.ldr = d.ldr;
+  p.ldh = d.ldh;
+  p.ldy = d.ldy;
+  p.x = x;
+  p.residual = d.residual ? residual : nullptr;
+  p.weight = weight;
+  p.h = d.residual ? h : nullptr;
+  p.y = y;
+  p.scales = scales;
+  p.rstd = rstd;
+  return launched(launch_norm(p, op->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int gemm_norm_backward(gemm_op_t op, const void* dy, const void* h, const uint8_t* E,
+                       const void* weight, const float* rstd, const void* dresidual, void* dx,
+                       float* dweight, gemm_stream_t stream) {
+  if (!usable(op, Kind::kNorm) || op->norm.y_type == GEMM_I8) return GEMM_ERR_INVALID_ARG;
+  const gemm_norm_desc_t& d = op->norm;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d.H == 0) return GEMM_OK;
+  if (!aligned(dweight, 4)) return GEMM_ERR_MISALIGNED;
+  if (d.T == 0)
+    return dweight ? launched(cudaMemsetAsync(dweight, 0, sizeof(float) * d.H, st)) : GEMM_OK;
+  const int64_t s = elem_size(d.type);
+  int rc = check_pointers({dy, dx}, s);
+  if (rc == GEMM_OK) rc = check_pointers({h}, E ? 1 : s);
+  if (rc == GEMM_OK) rc = check_pointers({weight}, elem_size(d.weight_type));
+  if (rc == GEMM_OK) rc = check_pointers({rstd}, 4);
+  if (rc != GEMM_OK) return rc;
+  if (!aligned(dresidual, s)) return GEMM_ERR_MISALIGNED;
+  NormBackwardParams p{};
+  p.T = d.T;
+  p.H = static_cast<int>(d.H);
+  p.type = d.type;
+  p.weight_type = d.weight_type;
+  p.ldy = d.ldy;
+  p.ldh = E ? d.H : d.ldh;
+  p.ldr = d.ldh;
+  p.ldx = d.ldx;
+  p.dy = dy;
+  p.h = h;
+  p.E = E;
+  p.weight = weight;
+  p.rstd = rstd;
+  p.dresidual = dresidual;
+  p.dx = dx;
+  p.dweight = dweight;
+  p.partial = static_cast<float*>(op->ws);
+  return launched(launch_norm_backward(p, op->num_sms, st));
+}
+
+// ---------------------------------------------------------------- rows to 8 bits
+int gemm_rows8_create(gemm_op_t* out, const gemm_rows8_desc_t* desc) {
+  if (!out || !desc) return GEMM_ERR_INVALID_ARG;
+  gemm_rows8_desc_t d = *desc;
+  if (d.T < 0 || d.H < 0 || d.T > INT_MAX / 2 || d.H > INT_MAX / 2 || !settle(d.ldx, d.H) ||
+      !settle(d.ldq, d.H) || (d.block != 0 && d.block != ROW_BLOCK))
+    return GEMM_ERR_INVALID_ARG;
+  if (!is_float(d.type)) return GEMM_ERR_UNSUPPORTED;
+  gemm_op* op = nullptr;
+  const int rc = make_op(Kind::kRows8, 0, 0, 0, &op);
+  if (rc != GEMM_OK) return rc;
+  op->rows8 = d;
+  std::snprintf(op->plan, sizeof op->plan, "rows8 T=%lld H=%lld block=%d",
+                static_cast<long long>(d.T), static_cast<long long>(d.H), d.block);
+  *out = op;
+  return GEMM_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+int run_rows8(gemm_op_t op, const void* X_in, void* X_out, const int8_t* q_in, int8_t* q_out,
+              const void* scales_in, void* scales_out, gemm_stream_t stream) {
+  if (!usable(op, Kind::kRows8)) return GEMM_ERR_INVALID_ARG;
+  const gemm_rows8_desc_t& d = op->rows8;
+  const bool pack = q_out != nullptr;
+  if (d.T == 0 || d.H == 0) return GEMM_OK;
+  int rc = check_pointers({pack ? X_in : X_out}, elem_size(d.type));
+  if (rc == GEMM_OK) rc = check_pointers({pack ? q_out : q_in}, 1);
+  if (rc == GEMM_OK) rc = check_pointers({pack ? scales_out : scales_in}, d.block ? 1 : 4);
+  if (rc != GEMM_OK) return rc;
+  Rows8Params p{};
+  p.T = d.T;
+  p.H = static_cast<int>(d.H);
+  p.type = d.type;
+  p.block = d.block;
+  p.ldx = d.ldx;
+  p.ldq = d.ldq;
+  p.X = X_in;
+  p.X_out = X_out;
+  p.q = q_in;
+  p.q_out = q_out;
+  p.scales = scales_in;
+  p.scales_out = scales_out;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launched(pack ? launch_rows8_pack(p, op->num_sms, st)
+                       : launch_rows8_unpack(p, op->num_sms, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_rows8_pack(gemm_op_t op, const void* X, int8_t* q, void* scales, gemm_stream_t stream) {
+  if (!q && usable(op, Kind::kRows8) && op->rows8.T > 0 && op->rows8.H > 0)
+    return GEMM_ERR_INVALID_ARG;
+  return run_rows8(op, X, nullptr, nullptr, q, nullptr, scales, stream);
+}
+
+int gemm_rows8_unpack(gemm_op_t op, const int8_t* q, const void* scales, void* X,
+                      gemm_stream_t stream) {
+  return run_rows8(op, nullptr, X, q, nullptr, scales, nullptr, stream);
+}
+
+// ---------------------------------------------------------------- gradients from block rows
+int gemm_rows8_grad_create(gemm_op_t* out, const gemm_rows8_grad_desc_t* desc) {
+  if (!out || !desc) return GEMM_ERR_INVALID_ARG;
+  gemm_rows8_grad_desc_t d = *desc;
+  if (d.R < 0 || d.K < 0 || d.K > INT_MAX / 2 || !settle(d.ldq, d.K)) return GEMM_ERR_INVALID_ARG;
+  gemm_grouped_desc_t g{};
+  g.form = GEMM_GROUPED_GRAD;
+  g.E = d.E;
+  g.R = d.R;
+  g.K = d.K;
+  g.N = d.N;
+  g.ab_type = d.b_type;
+  g.c_type = d.c_type;
+  g.d_type = d.d_type;
+  g.layout_b = GEMM_ROW_MAJOR;
+  g.lda = up(std::max<int64_t>(d.K, 1), 64);
+  g.ldb = d.ldb;
+  g.ldc = d.ldc;
+  g.ldd = d.ldd;
+  gemm_op* inner = nullptr;
+  int rc = gemm_grouped_create(&inner, &g);
+  if (rc != GEMM_OK) return rc;
+  // the rows in B's type, and the offsets of a single group
+  const size_t rows = static_cast<size_t>(up(2 * d.R * g.lda, 256));
+  gemm_op* op = nullptr;
+  rc = make_op(Kind::kRows8Grad, rows + 256, rows, 256, &op);
+  if (rc != GEMM_OK) {
+    gemm_op_destroy(inner);
+    return rc;
+  }
+  op->inner = inner;
+  op->rows8_grad = d;
+  op->ws_lda = g.lda;
+  op->ws_b_off = rows;
+  const int32_t one[2] = {0, static_cast<int32_t>(d.R)};
+  if (write_now(static_cast<uint8_t*>(op->ws) + rows, one, sizeof one) != cudaSuccess) {
+    cudaGetLastError();
+    gemm_op_destroy(op);
+    return GEMM_ERR_CUDA;
+  }
+  std::snprintf(op->plan, sizeof op->plan, "rows8_grad: %s", inner->plan);
+  *out = op;
+  return GEMM_OK;
+}
+
+int gemm_rows8_grad_run(gemm_op_t op, const int8_t* q, const uint8_t* E, const void* B,
+                        const int32_t* offsets, const void* C, void* D, gemm_stream_t stream) {
+  if (!usable(op, Kind::kRows8Grad)) return GEMM_ERR_INVALID_ARG;
+  const gemm_rows8_grad_desc_t& d = op->rows8_grad;
+  if (d.N == 0 || d.K == 0) return GEMM_OK;
+  if (!D || (d.R > 0 && (!q || !E || !B)) || (d.E > 1 && !offsets)) return GEMM_ERR_INVALID_ARG;
+  const int32_t* const groups =
+      offsets ? offsets
+              : reinterpret_cast<const int32_t*>(static_cast<uint8_t*>(op->ws) + op->ws_b_off);
+  if (d.R > 0) {
+    Rows8Params p{};
+    p.T = d.R;
+    p.H = static_cast<int>(d.K);
+    p.type = d.b_type;
+    p.block = ROW_BLOCK;
+    p.ldx = op->ws_lda;
+    p.ldq = d.ldq;
+    p.X_out = op->ws;
+    p.q = q;
+    p.scales = E;
+    const int rc = launched(launch_rows8_unpack(p, op->num_sms, static_cast<cudaStream_t>(stream)));
+    if (rc != GEMM_OK) return rc;
+  }
+  return gemm_grouped_run(op->inner, op->ws, B, groups, C, D, stream);
+}
+
+// ---------------------------------------------------------------- scaled products
+int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
+  if (!out || !desc) return GEMM_ERR_INVALID_ARG;
+  gemm_i8_desc_t d = *desc;
+  if (d.E < 1 || d.E > GEMM_MAX_EXPERTS || d.R < 0 || d.K < 0 || d.N < 0 || d.R > INT_MAX / 2 ||
+      d.K >= 1 << 17 || d.N > INT_MAX / 2 / d.E || !settle(d.ldx, d.K) || !settle(d.ldw, d.K) ||
+      !settle(d.ldd, d.N))
+    return GEMM_ERR_INVALID_ARG;
+  if (!is_float(d.d_type)) return GEMM_ERR_UNSUPPORTED;
+  gemm_op* op = nullptr;
+  const int rc = make_op(Kind::kI8, 0, 0, 0, &op);
+  if (rc != GEMM_OK) return rc;
+  op->i8 = d;
+  std::snprintf(op->plan, sizeof op->plan, "i8 E=%d R=%lld K=%lld N=%lld", d.E,
+                static_cast<long long>(d.R), static_cast<long long>(d.K),
+                static_cast<long long>(d.N));
+  *out = op;
+  return GEMM_OK;
+}
+
+int gemm_i8_run(gemm_op_t op, const int8_t* X, const float* x_scales, const int8_t* W,
+                const float* w_scales, const int32_t* offsets, void* D, gemm_stream_t stream) {
+  if (!usable(op, Kind::kI8)) return GEMM_ERR_INVALID_ARG;
+  const gemm_i8_desc_t& d = op->i8;
+  if (d.R == 0 || d.N == 0) return GEMM_OK;
+  if (!D || !x_scales || !w_scales || (d.K > 0 && (!X || !W)) || (d.E > 1 && !offsets))
+    return GEMM_ERR_INVALID_ARG;
+  if (!aligned(D, elem_size(d.d_type)) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
+      !aligned(offsets, 4))
+    return GEMM_ERR_MISALIGNED;
+  I8RowsParams p{};
+  p.E = d.E;
+  p.R = static_cast<int>(d.R);
+  p.K = static_cast<int>(d.K);
+  p.N = static_cast<int>(d.N);
+  p.d_type = d.d_type;
+  p.ldx = d.ldx;
+  p.ldw = d.ldw;
+  p.ldd = d.ldd;
+  p.X = X;
+  p.x_scales = x_scales;
+  p.W = W;
+  p.w_scales = w_scales;
+  p.offsets = offsets;
+  p.D = D;
+  p.status = op->status;
+  p.num_sms = op->num_sms;
+  return launched(launch_i8_rows(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -579,6 +579,114 @@ GEMM_API int gemm_w4_run(gemm_op_t op, const void* X, const uint8_t* W, const vo
                          const uint8_t* zeros, const int32_t* offsets, void* D,
                          gemm_stream_t stream);
 
+/*
+ * Operators on rows held in 8 bits: the norm that makes them, the products
+ * that read them, and the rows that training keeps in them.  Handles and
+ * conventions are those of the operators above.  Two forms:
+ *   block rows   T x H int8 (ldq apart) and T x ceil(H / 32) bytes E, packed:
+ *                element i of row t is q[t, i] * 2^(E[t, i / 32] - 127), exact
+ *                in bf16 and, rows of fp16 packed, in fp16 (a byte 255 is NaN)
+ *   scaled rows  T x H int8 and T fp32 scales: q[t, i] * scales[t]
+ *
+ * Rows of T x H elements, type F16, BF16 or F32; ld 0 = H throughout.
+ */
+
+/*
+ * Root-mean-square norm.  x: T rows of H elements (ldx apart).
+ *   h = x + residual, rounded to type         (residual != 0; else h is x)
+ *   rstd[t] = 1 / sqrt(mean_i h[t, i]^2 + eps)
+ *   y[t, i] = h[t, i] * rstd[t] * weight[i]
+ * y_type type: y rounded once.  y_type I8: scaled rows, scales[t] = max_i
+ * |y[t, i]| / 127 and q the nearest integers (ties to even); a row of zeros
+ * has scale 0, a row in which y is not finite a scale that is not finite, and
+ * q 0.  weight: H values of type or F32.  rstd (T fp32) may be NULL.  Sums are
+ * fp32.  h may be x or residual itself (of the same leading dimension);
+ * nothing else may overlap.
+ * gemm_norm_backward (y_type = type): from dy (laid out like y) and what
+ * arrives at h by the residual, dresidual (like h, NULL for zero),
+ *   dx = rstd (weight dy - h rstd^2 / H sum_j dy_j weight_j h_j) + dresidual
+ *   dweight[i] = sum_t dy[t, i] h[t, i] rstd[t]      (H fp32; NULL: not wanted)
+ * dx (like x) is the gradient of x and of residual.  h: the forward pass's h
+ * (x where there is no residual); or, with E (else NULL), its block rows,
+ * packed.  dx may be dy or dresidual itself (of the same leading dimension).
+ * Sums are fp32 in a fixed order.
+ */
+typedef struct {
+  int64_t T, H;
+  gemm_dtype_t type, weight_type, y_type;
+  int32_t residual;
+  float eps;
+  int64_t ldx, ldr, ldh, ldy; /* x, residual, h, y */
+} gemm_norm_desc_t;
+GEMM_API int gemm_norm_create(gemm_op_t* out, const gemm_norm_desc_t* desc);
+GEMM_API int gemm_norm_run(gemm_op_t op, const void* x, const void* residual, const void* weight,
+                           void* h, void* y, float* scales, float* rstd, gemm_stream_t stream);
+GEMM_API int gemm_norm_backward(gemm_op_t op, const void* dy, const void* h, const uint8_t* E,
+                                const void* weight, const float* rstd, const void* dresidual,
+                                void* dx, float* dweight, gemm_stream_t stream);
+
+/*
+ * Rows to 8 bits and back.  block 32: block rows, scales the bytes E; the
+ * exponent of a block is the least for which its largest magnitude is at most
+ * 127 steps (at least 2^-127, of fp16 rows 2^-24), q the nearest integers, ties
+ * to even; a block with a value that is not finite gets the byte 255 and comes
+ * back as NaN.  block 0: scaled rows, scales T fp32, as gemm_norm_run makes
+ * them.  pack reads X and writes q and scales, unpack the reverse; what rounds
+ * past type's largest finite value comes back as that.
+ */
+typedef struct {
+  int64_t T, H;
+  gemm_dtype_t type;
+  int32_t block; /* 32 or 0 */
+  int64_t ldx, ldq;
+} gemm_rows8_desc_t;
+GEMM_API int gemm_rows8_create(gemm_op_t* out, const gemm_rows8_desc_t* desc);
+GEMM_API int gemm_rows8_pack(gemm_op_t op, const void* X, int8_t* q, void* scales,
+                             gemm_stream_t stream);
+GEMM_API int gemm_rows8_unpack(gemm_op_t op, const int8_t* q, const void* scales, void* X,
+                               gemm_stream_t stream);
+
+/*
+ * Weight gradients from block rows: the product GEMM_GROUPED_GRAD with A held
+ * in 8 bits,
+ *   D_e[k, n] = sum over the rows r of expert e of A[r, k] B[r, n] (+ C_e[k, n])
+ * A[r, k] = q[r, k] * 2^(E[r, k / 32] - 127) rounded to B's type (which is
+ * exact for BF16 and for packed rows of fp16).  With E = 1 offsets may be NULL
+ * (all R rows).  B, C, D and everything else as there; ldq: 0 = K.
+ */
+typedef struct {
+  int32_t E;
+  int64_t R, K, N;
+  gemm_dtype_t b_type, c_type, d_type;
+  int64_t ldq, ldb, ldc, ldd;
+} gemm_rows8_grad_desc_t;
+GEMM_API int gemm_rows8_grad_create(gemm_op_t* out, const gemm_rows8_grad_desc_t* desc);
+GEMM_API int gemm_rows8_grad_run(gemm_op_t op, const int8_t* q, const uint8_t* E, const void* B,
+                                 const int32_t* offsets, const void* C, void* D,
+                                 gemm_stream_t stream);
+
+/*
+ * Scaled rows times weights of 8-bit integers with a scale for each output:
+ *   D[r, n] = x_scales[r] * w_scales[e, n] * sum_k X[r, k] W_e[n, k]
+ * X: R x K int8 (ldx); W: E matrices N x K int8 one after another, E * N rows
+ * ldw apart; w_scales E x N fp32; D R x N (ldd), F16, BF16 or F32.  With E = 1
+ * offsets may be NULL (all R rows); otherwise they group the rows as above,
+ * and rows of no expert are not written.  The sums are exact as long as they
+ * stay below 2^24 (always up to K = 1024), and beyond that off by at most
+ * K * 2^-24 of the sum of magnitudes; scaled in fp32 and rounded once.
+ * K < 2^17.
+ */
+typedef struct {
+  int32_t E;
+  int64_t R, K, N;
+  gemm_dtype_t d_type;
+  int64_t ldx, ldw, ldd;
+} gemm_i8_desc_t;
+GEMM_API int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc);
+GEMM_API int gemm_i8_run(gemm_op_t op, const int8_t* X, const float* x_scales, const int8_t* W,
+                         const float* w_scales, const int32_t* offsets, void* D,
+                         gemm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
