@@ -46,6 +46,7 @@ UNITS = [
     ("norm.cu", [], "norm.o"),
     ("rows8.cu", [], "rows8.o"),
     ("i8_rows.cu", [], "i8_rows.o"),
+    ("i8_tiles.cu", [], "i8_tiles.o"),
 ]
 
 

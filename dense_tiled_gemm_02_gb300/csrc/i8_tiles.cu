@@ -1,0 +1,688 @@
+// i8_tiles.cu -- many rows times weights of 8-bit integers, with a scale for
+// each row and each output; dense or grouped by expert.
+//
+//   D[r,n] = x_scales[r] w_scales[e,n] sum_k X[r,k] W_e[n,k]
+//
+// sm_103a has no 8-bit integer form of tcgen05.mma, so the integers go through
+// the fp16 one, in which they and their products are exact and the fp32 sums
+// are up to 2^24.  Schedule, tiles and epilogue are those of grouped.cu's narrow
+// form (D's columns as the M dimension, D's rows as N); the weights are not
+// widened in memory: they come to shared memory as bytes, converter warps turn
+// them into fp16 and leave them in tensor memory, where the MMA reads its A
+// operand.  So HBM gives a byte a weight, and shared memory takes one write and
+// one read of it.  X, which every feature tile reads again, is widened once into
+// the workspace.
+//
+// A byte b of the sign-flipped word beside 0x64 is the fp16 number 1024 + b:
+// one byte permute makes two of them, one packed subtraction of 1152 the values.
+//
+// A stage goes round once: TMA, converters, MMA, TMA.  Its slot of tensor memory
+// goes with it, so that the converters, who see the stage filled, know the slot
+// free.  The converters' way through a stage is a chain of latencies (wait,
+// load, convert, store, wait, arrive: about 600 cycles of which the instructions
+// are a third), so two groups of warps take the stages in turn.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "grouped.cuh"
+#include "i8.cuh"
+#include "rows.h"
+
+namespace gb300 {
+
+namespace {
+
+constexpr int SLICE = 128;                    // K of a stage: a 128-byte row of W
+constexpr uint32_t W_BYTES = FT * SLICE;
+constexpr int TILE_EPI_WARPS = 4;
+constexpr int CONV_GROUPS = 2;                // of four warps, taking stages in turn
+// warp 0: TMA loads, 1: MMA issue, 2-5: epilogue, 6: schedule, from 7: converters
+constexpr int I8_THREADS = 32 * (7 + 4 * CONV_GROUPS);
+
+template <int QT, int STAGES>
+struct Cfg {
+  static constexpr uint32_t X_SUB = QT * BK * 2;  // 64 values of each row
+  static constexpr uint32_t X_BYTES = 2 * X_SUB;
+  // Tensor memory: two accumulators, then a slot of 128 values a row for each stage.
+  static constexpr uint32_t SLOT0 = 2 * QT;
+  static_assert(SLOT0 + 64 * STAGES <= 512, "tensor memory");
+  static constexpr uint32_t BAR_BYTES = 768;
+  static constexpr uint32_t SMEM = 1024 + STAGES * (W_BYTES + X_BYTES) + EPI_BYTES + BAR_BYTES +
+                                   4 * (2 * GEMM_MAX_EXPERTS + 2);
+  static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
+  static_assert(X_SUB % 1024 == 0, "stage alignment");
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's rows in the lanes, two 16-bit values of K
+// a column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Bytes 0, 1 (HIGH: 2, 3) of a word whose sign bits are flipped, as fp16.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t widen_pair(uint32_t flipped) {
+  const uint32_t v = __byte_perm(flipped, 0x64646464u, HIGH ? 0x4342 : 0x4140);
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v),
+                            __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  lo = widen_pair<false>(w);
+  hi = widen_pair<true>(w);
+}
+
+// ---------------------------------------------------------------- kernel
+template <int QT, int STAGES, int DT>
+__global__ void __launch_bounds__(I8_THREADS, 1)
+    i8_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                    const __grid_constant__ CUtensorMap tmX32,
+                    const __grid_constant__ CUtensorMap tmD, const GroupedParams p) {
+  using C = Cfg<QT, STAGES>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* const sW = smem;
+  uint8_t* const sX = smem + STAGES * W_BYTES;
+  uint8_t* const sE = sX + STAGES * C::X_BYTES;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(sE + EPI_BYTES);
+  constexpr int NBARS = 3 * STAGES + 5 + 2 * QUEUE;
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* const ep_go = abort_flag + 1;  // two, taken in turn
+  volatile int* const ep_last = abort_flag + 3;
+  Piece* const queue = reinterpret_cast<Piece*>(reinterpret_cast<uint8_t*>(bars) + 512);
+  static_assert(8 * NBARS + 20 <= 512 && 512 + QUEUE * sizeof(Piece) <= C::BAR_BYTES, "layout");
+  int* const lo = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + C::BAR_BYTES);
+  int* const prefix = lo + p.E + 1;
+
+  const uint32_t bar0 = smem_u32(bars);
+  auto full = [&](uint32_t s) { return bar0 + 8u * s; };                     // loaded
+  auto ready = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };         // and converted
+  auto empty = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + s); };
+  auto acc_full = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + b); };
+  auto acc_empty = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
+  const uint32_t done_bar = bar0 + 8u * (3 * STAGES + 4);
+  auto q_full = [&](uint32_t i) { return bar0 + 8u * (3 * STAGES + 5 + i); };
+  auto q_empty = [&](uint32_t i) { return bar0 + 8u * (3 * STAGES + 5 + QUEUE + i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(ready(s), 4);
+      mbar_init(empty(s), 1);
+    }
+    for (int i = 0; i < QUEUE; ++i) {
+      mbar_init(q_full(i), 1);
+      mbar_init(q_empty(i), 2 + TILE_EPI_WARPS + 4 * CONV_GROUPS);  // a warp's arrival each
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), TILE_EPI_WARPS);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmX32);
+    if (p.d_tma) tma_prefetch_desc(&tmD);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  for (int e = threadIdx.x; e <= p.E; e += I8_THREADS) {
+    // without offsets all rows are the one expert's
+    lo[e] = p.offsets ? p.offsets[e] : e * p.R;
+    if (p.offsets && e < p.E) expert_rows(p.offsets, e, p.R, p.status);
+  }
+  __syncthreads();
+  if (warp == 2) {  // the prefix: each lane a run of experts, then a warp scan
+    auto count = [&](int e) { return row_tiles<QT>(rows_of(p, lo, e)); };
+    const int len = (p.E + 31) / 32, b = min(p.E, lane * len), e1 = min(p.E, b + len);
+    int sum = 0;
+    for (int e = b; e < e1; ++e) sum += count(e);
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += u;
+    }
+    int at = inc - sum;
+    for (int e = b; e < e1; ++e) {
+      prefix[e] = at;
+      at += count(e);
+    }
+    if (lane == 31) prefix[p.E] = inc;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const uint64_t tmo = p.timeout_ns;
+  // The next piece of this CTA's work, taken by one warp for itself; false at
+  // its end or after a timeout.
+  uint32_t q_at = 0, q_ph = 0;
+  auto next_piece = [&](Piece& x) {
+    bool ok = true;
+    if (lane == 0)
+      ok = bounded_wait(q_full(q_at), q_ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    if (!ok) return false;
+    __syncwarp();
+    x = queue[q_at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_empty(q_at));
+    if (++q_at == QUEUE) {
+      q_at = 0;
+      q_ph ^= 1u;
+    }
+    return x.more != 0;
+  };
+  Piece x;
+
+  if (warp == 6) {
+    // ------------------------------------------------------------ schedule
+    Schedule<1, QT, SLICE> work(p, lo, prefix, blockIdx.x, gridDim.x);
+    if (lane == 0) {
+      for (bool more = true; more;) {
+        more = work.next(x);
+        x.more = more;
+        if (!bounded_wait(q_empty(q_at), q_ph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo)) break;
+        queue[q_at] = x;
+        mbar_arrive(q_full(q_at));
+        if (++q_at == QUEUE) {
+          q_at = 0;
+          q_ph ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    uint32_t it = 0, s = 0, ph = 0;
+    bool stop = false, skipped = false;
+    const bool skip = (p.debug_flags & DBG_SKIP_FIRST_FILL) ||
+                      ((p.debug_flags & DBG_SKIP_ONE_FILL) && blockIdx.x == 0);
+    const uint32_t sW0 = smem_u32(sW), sX0 = smem_u32(sX);
+    while (next_piece(x)) {
+      if (elect_one() && !stop) {
+        const int wrow = x.e * p.N + x.f0;
+        const bool big = x.nq > 32;
+        const uint32_t bytes = W_BYTES + 2u * (big ? C::X_SUB : 4096u);
+        auto slices = [&](const CUtensorMap* tm) {
+          for (int k = x.k; k < x.kend; k += SLICE) {
+            if (!bounded_wait(empty(s), ph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo)) {
+              stop = true;
+              return;
+            }
+            if (it == 0 && skip) {
+              skipped = true;  // test hook: the waits on the first stage expire
+            } else {
+              mbar_arrive_expect_tx(full(s), bytes);
+              tma_load_2d(sW0 + s * W_BYTES, &tmW, k, wrow, full(s));
+              tma_load_2d(sX0 + s * C::X_BYTES, tm, k, x.q0, full(s));
+              tma_load_2d(sX0 + s * C::X_BYTES + C::X_SUB, tm, k + BK, x.q0, full(s));
+            }
+            ++it;
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        };
+        if (big)
+          slices(&tmX);
+        else
+          slices(&tmX32);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) {
+      // copies in flight land before the CTA leaves
+      for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j)
+        if (!(skipped && j == 0)) drain_wait(full(j % STAGES), (j / STAGES) & 1u, 200000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t x_lo0 = sdesc_lo(smem_u32(sX), 16u);
+    const uint32_t dhi = sdesc_hi_sw128(1024u);
+    uint32_t s = 0, ph = 0, acc_it = 0;
+    bool ok = true;
+    while (next_piece(x)) {
+      if (elect_one() && ok && x.k < x.kend) {
+        const uint32_t buf = acc_it & 1u;
+        const uint32_t d_tmem = tmem_base + buf * QT;
+        const uint32_t idesc = p.idesc | (static_cast<uint32_t>(((x.nq + 31) & ~31) >> 3) << 17);
+        ok = bounded_wait(acc_empty(buf), ((acc_it >> 1) & 1u) ^ 1u, abort_flag, p.status,
+                          STATUS_TIMEOUT, tmo);
+        uint32_t accumulate = 0;
+        for (int k = x.k; ok && k < x.kend; k += SLICE) {
+          ok = bounded_wait(ready(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo) &&
+               bounded_wait(full(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = tmem_base + C::SLOT0 + s * 64u;
+          const uint32_t b = x_lo0 + s * (C::X_BYTES >> 4);
+          // (values past K are zeros on both sides)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            mma_ts(d_tmem, a + 8u * c, sdesc(dhi, b + 2u * c), idesc, accumulate | c);
+          if (x.kend - k > BK)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              mma_ts(d_tmem, a + 32u + 8u * c, sdesc(dhi, b + (C::X_SUB >> 4) + 2u * c), idesc, 1u);
+          accumulate = 1;
+          mma_commit(empty(s));
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) mma_commit(acc_full(buf));
+        ++acc_it;
+      }
+      __syncwarp();
+    }
+    if (elect_one()) {
+      mma_commit(done_bar);
+      drain_wait(done_bar, 0, 200000000ull);
+    }
+    __syncwarp();
+  } else if (warp > 6) {
+    // ------------------------------------------------------------ converters
+    // Lane = weight row = lane of tensor memory, of which a warp reaches its own
+    // quarter: 128 bytes of the row as eight 16-byte units (unit u of row r at
+    // u ^ r % 8: eight rows fall on all banks).
+    const int q = warp & 3, group = (warp - 7) >> 2, row = 32 * q + lane;
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + C::SLOT0;
+    const uint8_t* const src0 = sW + row * SLICE;
+    uint32_t s = 0, ph = 0;
+    int turn = 0;
+    bool ok = true;
+    while (next_piece(x)) {
+      for (int k = x.k; ok && k < x.kend; k += SLICE) {
+        if (turn == group) {
+          ok = bounded_wait(full(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint8_t* const src = src0 + s * W_BYTES;
+          auto convert = [&](int sub) {
+            uint32_t v[32];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint4 w = *reinterpret_cast<const uint4*>(
+                  src + (((4 * sub + u) ^ (row & 7)) << 4));
+              widen4(w.x, v[8 * u], v[8 * u + 1]);
+              widen4(w.y, v[8 * u + 2], v[8 * u + 3]);
+              widen4(w.z, v[8 * u + 4], v[8 * u + 5]);
+              widen4(w.w, v[8 * u + 6], v[8 * u + 7]);
+            }
+            tmem_st_32x32b_x32(taddr + s * 64u + sub * 32u, v);
+          };
+          convert(0);
+          if (x.kend - k > BK) convert(1);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready(s));
+        }
+        turn = turn + 1 == CONV_GROUPS ? 0 : turn + 1;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    // As in grouped.cu, with the scales: of features one or four a thread, of
+    // rows those of the chunk at hand.
+    const int q = warp & 3;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    const bool ep_leader = threadIdx.x == 64;
+    uint32_t acc_it = 0;
+    const int unit = blockIdx.x;
+    for (uint32_t turn = 0;; turn ^= 1u) {
+      const uint32_t buf = acc_it & 1u;
+      // One thread decides for all four warps whether there is a piece and its sums.
+      if (ep_leader) {
+        bool go = bounded_wait(q_full(q_at), q_ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
+        if (go && queue[q_at].more && queue[q_at].k < queue[q_at].kend)
+          go = bounded_wait(acc_full(buf), (acc_it >> 1) & 1u, abort_flag, p.status,
+                            STATUS_TIMEOUT, tmo);
+        ep_go[turn] = go ? 1 : 0;
+      }
+      named_barrier_sync(1, 32 * TILE_EPI_WARPS);
+      if (!ep_go[turn]) break;
+      x = queue[q_at];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty(q_at));
+      if (++q_at == QUEUE) {
+        q_at = 0;
+        q_ph ^= 1u;
+      }
+      if (!x.more) break;
+      tc_fence_after();
+      auto release = [&] {  // the accumulator has been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(buf));
+      };
+      const int f0 = x.f0 + q * 32;  // this warp's features
+      const int f = f0 + lane;
+      const float* const fs = p.w_scales + static_cast<long long>(x.e) * p.N;
+      const float* const rs = p.x_scales + x.q0;  // the tile's rows
+      auto f_scale = [&](int i) { return i < p.N ? fs[i] : 0.f; };
+      auto r_scale = [&](int i) { return i < x.nq ? rs[i] : 0.f; };
+      const long long row0 = x.q0;
+      const uint32_t taddr = tmem_base + lane_base + buf * QT;
+      auto c_last = [&](int c) { return c + 32 >= x.nq; };
+      const bool staged_store = DT != T_F32 && p.d_vec;
+      auto stage_at = [&](int row, int u) {
+        return sE + (u >> 3) * 4096 + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+      };
+      auto stage_free = [&] {  // the buffer's last chunk has left it
+        if (ep_leader) bulk_wait_read<0>();
+        named_barrier_sync(1, 128);
+      };
+      auto copy_out = [&](int c) {  // rows c .. c + 31 of the tile
+        const int fc = x.f0;
+        const bool box = p.d_tma && c + 32 <= x.nq;
+        if (box) fence_proxy_async_smem();
+        named_barrier_sync(1, 128);
+        if (box) {
+          if (ep_leader) {
+            const uint32_t src = smem_u32(sE);
+            const int y = x.q0 + c;
+            if (fc < p.N) store_3d(&tmD, src, fc, y, 0);
+            if (fc + 64 < p.N) store_3d(&tmD, src + 4096u, fc + 64, y, 0);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 8 * q + 2 * i + (lane >> 4), u = lane & 15;
+            const int f8 = fc + 8 * u;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage_at(row, u));
+            if (c + row < x.nq && f8 < p.N) {
+              uint16_t* const d = static_cast<uint16_t*>(p.D) + (row0 + c + row) * p.ldd + f8;
+              if (f8 + 8 <= p.N) {
+                *reinterpret_cast<uint4*>(d) = v;
+              } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int j = 0; j < p.N - f8; ++j)
+                  d[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+              }
+            }
+          }
+        }
+        // one bulk group a chunk, empty where the threads stored it
+        if (ep_leader) bulk_commit();
+      };
+      if (x.pieces == 1 && staged_store) {
+        // fragments of 16 features x 8 rows, scaled, and transposed into rows by stmatrix
+        if constexpr (DT != T_F32) {
+          float sf[4];  // features 16 h + 8 b + lane / 4 at 2 h + b
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sf[i] = f_scale(f0 + 8 * i + (lane >> 2));
+#pragma unroll 1
+          for (int c = 0; c < x.nq; c += 32) {
+            float sr[8];  // rows 8 i + 2 (lane % 4) + b at 2 i + b
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sr[i] = r_scale(c + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1));
+            uint32_t r[32];
+            tmem_ld_16x256b_x4(taddr + c, r);
+            tmem_ld_16x256b_x4(taddr + c + (16u << 16), r + 16);
+            tmem_ld_wait();
+            if (c_last(c)) release();
+            const int m = lane >> 3;
+            stage_free();
+            auto pair = [&](int h, int i, int b) {  // rows 2 (lane % 4), + 1 of fragment i
+              const uint32_t* const v = r + 16 * h + 4 * i + 2 * b;
+              const float s = sf[2 * h + b];
+              return pack2<DT>(__float_as_uint(__uint_as_float(v[0]) * sr[2 * i] * s),
+                               __float_as_uint(__uint_as_float(v[1]) * sr[2 * i + 1] * s));
+            };
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; i += 2)
+                stmatrix_x4_trans(
+                    smem_u32(stage_at(8 * (i + (m >> 1)) + (lane & 7), 4 * q + 2 * h + (m & 1))),
+                    pair(h, i, 0), pair(h, i, 1), pair(h, i + 1, 0), pair(h, i + 1, 1));
+            copy_out(c);
+          }
+        }
+        ++acc_it;
+        continue;
+      }
+      // Everything else: lane = feature, one D row at a time.  Partial sums of
+      // a shared tile: float4 of four D rows of a feature, features adjacent.
+      auto partial = [&](int piece_unit, int slot) {
+        return reinterpret_cast<float4*>(
+                   p.partial + static_cast<size_t>(2 * piece_unit + slot) * (QT * FT)) +
+               q * 32 + lane;
+      };
+      if (x.pieces > 1) {
+        // leave the sums, see who is last
+        float4* const mine = partial(unit, x.slot);
+#pragma unroll 1
+        for (int c = 0; c < x.nq; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(taddr + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            mine[(c / 4 + j) * FT] =
+                make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                            __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+        }
+        __threadfence();
+        named_barrier_sync(1, 32 * TILE_EPI_WARPS);
+        if (ep_leader) {
+          unsigned* const count = p.counters + x.first;
+          const bool last = atomicAdd(count, 1u) == static_cast<unsigned>(x.pieces) - 1u;
+          if (last) *count = 0u;  // ready for the next call
+          __threadfence();
+          *ep_last = last ? 1 : 0;
+        }
+        named_barrier_sync(1, 32 * TILE_EPI_WARPS);
+        const bool last = *ep_last != 0;
+        named_barrier_sync(1, 32 * TILE_EPI_WARPS);
+        if (!last) {
+          release();
+          ++acc_it;
+          continue;
+        }
+        __threadfence();
+      }
+      const float s = f_scale(f);
+#pragma unroll 1
+      for (int c = 0; c < x.nq; c += 32) {
+        float v[32];
+        {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(taddr + c, r);
+          tmem_ld_wait();
+          if (c_last(c)) release();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        }
+        if (x.pieces > 1) {
+          // in K order, this unit's own sums among them: the same bits
+          // whoever is last
+          float t[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) t[j] = 0.f;
+#pragma unroll 1
+          for (int i = 0; i < x.pieces; ++i) {
+            if (x.first + i == unit) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) t[j] += v[j];
+              continue;
+            }
+            const float4* const src = partial(x.first + i, i == 0 ? 1 : 0) + c / 4 * FT;
+            float4 w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __ldcg(src + j * FT);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              t[4 * j] += w[j].x;
+              t[4 * j + 1] += w[j].y;
+              t[4 * j + 2] += w[j].z;
+              t[4 * j + 3] += w[j].w;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = t[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = v[j] * r_scale(c + j) * s;
+        if (staged_store) {
+          stage_free();
+          if constexpr (DT != T_F32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              *reinterpret_cast<uint16_t*>(stage_at(j, 4 * q + (lane >> 3)) + 2 * (lane & 7)) =
+                  static_cast<uint16_t>(pack2<DT>(__float_as_uint(v[j]), 0u));
+          }
+          copy_out(c);
+        } else if (f < p.N) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c + j < x.nq) store_d<DT>(p.D, (row0 + c + j) * p.ldd + f, v[j]);
+        }
+        __syncwarp();
+      }
+      ++acc_it;
+    }
+    if (ep_leader) bulk_wait_all();  // shared memory outlives the stores that read it
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------- copies of rows
+// 16 values a thread and turn; ALIGNED as in i8_rows.cu.  A last unit that K
+// ends in is padded with whatever follows: the tensor maps end at K.
+template <bool ALIGNED, bool WIDEN>
+__global__ void __launch_bounds__(256)
+    i8_copy_kernel(const int8_t* src, long long ld_src, uint8_t* dst, long long ld_dst,
+                   long long rows, int cols) {
+  const int n = (cols + 15) / 16;
+  pdl_wait();
+  pdl_trigger();
+  for (long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; at < rows * n;
+       at += static_cast<long long>(gridDim.x) * 256) {
+    const long long row = at / n;
+    const int k = static_cast<int>(at - row * n) * 16;
+    const int8_t* const from = src + row * ld_src + k;
+    const uint4 w = ALIGNED ? *reinterpret_cast<const uint4*>(from)
+                            : load16_at(from, min(16, cols - k));
+    if constexpr (WIDEN) {
+      uint4* const to = reinterpret_cast<uint4*>(dst + 2 * (row * ld_dst + k));
+      uint4 a, b;
+      widen4(w.x, a.x, a.y);
+      widen4(w.y, a.z, a.w);
+      widen4(w.z, b.x, b.y);
+      widen4(w.w, b.z, b.w);
+      to[0] = a;
+      to[1] = b;
+    } else {
+      *reinterpret_cast<uint4*>(dst + row * ld_dst + k) = w;
+    }
+  }
+}
+
+template <bool WIDEN>
+cudaError_t copy_rows(const int8_t* src, long long ld_src, void* dst, long long ld_dst,
+                      long long rows, int cols, int num_sms, cudaStream_t st) {
+  const bool aligned = cols % 16 == 0 && ld_src % 16 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0;
+  const long long items = rows * ((cols + 15) / 16);
+  const dim3 grid(static_cast<unsigned>(std::min<long long>((items + 255) / 256, 16ll * num_sms)));
+  uint8_t* const d = static_cast<uint8_t*>(dst);
+  return aligned ? launch_pdl(i8_copy_kernel<true, WIDEN>, grid, dim3(256), 0, st, src, ld_src, d,
+                              ld_dst, rows, cols)
+                 : launch_pdl(i8_copy_kernel<false, WIDEN>, grid, dim3(256), 0, st, src, ld_src, d,
+                              ld_dst, rows, cols);
+}
+
+// ---------------------------------------------------------------- launches
+// Tiles of up to 64 rows, or up to 128.
+constexpr int STAGES64 = 6, STAGES128 = 4;
+
+template <int QT, int STAGES, int DT>
+int prepare(int num_sms) {
+  return cudaFuncSetAttribute(i8_tiles_kernel<QT, STAGES, DT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Cfg<QT, STAGES>::SMEM) == cudaSuccess
+             ? num_sms
+             : 0;
+}
+template <int DT>
+int prepare_typed(int rows, int num_sms) {
+  return rows == 128 ? prepare<128, STAGES128, DT>(num_sms) : prepare<64, STAGES64, DT>(num_sms);
+}
+template <int DT>
+cudaError_t launch_typed(int rows, const CUtensorMap& w, const CUtensorMap& x,
+                         const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
+                         int units, cudaStream_t st) {
+  return rows == 128 ? launch_pdl(i8_tiles_kernel<128, STAGES128, DT>, dim3(units), dim3(I8_THREADS),
+                                  Cfg<128, STAGES128>::SMEM, st, w, x, x32, d, p)
+                     : launch_pdl(i8_tiles_kernel<64, STAGES64, DT>, dim3(units), dim3(I8_THREADS),
+                                  Cfg<64, STAGES64>::SMEM, st, w, x, x32, d, p);
+}
+
+}  // namespace
+
+int prepare_i8_tiles(int rows, int d_type, int num_sms) {
+  return d_type == T_F32    ? prepare_typed<T_F32>(rows, num_sms)
+         : d_type == T_BF16 ? prepare_typed<T_BF16>(rows, num_sms)
+                            : prepare_typed<T_F16>(rows, num_sms);
+}
+
+size_t i8_tiles_partial_bytes(int rows, int units) {
+  return sizeof(float) * 2 * units * FT * rows;
+}
+
+cudaError_t launch_i8_tiles(int rows, const CUtensorMap& w, const CUtensorMap& x,
+                            const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
+                            int units, cudaStream_t st) {
+  return p.d_type == T_F32    ? launch_typed<T_F32>(rows, w, x, x32, d, p, units, st)
+         : p.d_type == T_BF16 ? launch_typed<T_BF16>(rows, w, x, x32, d, p, units, st)
+                              : launch_typed<T_F16>(rows, w, x, x32, d, p, units, st);
+}
+
+cudaError_t launch_i8_copy(const int8_t* src, long long ld_src, int8_t* dst, long long ld_dst,
+                           long long rows, int cols, int num_sms, cudaStream_t st) {
+  return copy_rows<false>(src, ld_src, dst, ld_dst, rows, cols, num_sms, st);
+}
+cudaError_t launch_i8_widen(const int8_t* src, long long ld_src, uint16_t* dst, long long ld_dst,
+                            long long rows, int cols, int num_sms, cudaStream_t st) {
+  return copy_rows<true>(src, ld_src, dst, ld_dst, rows, cols, num_sms, st);
+}
+
+}  // namespace gb300

@@ -145,6 +145,8 @@ struct GroupedParams {
   uint32_t* status;
   unsigned long long timeout_ns;
   int debug_flags;
+  const float* x_scales;  // products of 8-bit integers: of rows, of each expert's columns
+  const float* w_scales;
 };
 // Sets the kernel up on the current device; how many of its units (CTA pairs
 // when wide, else CTAs) run at once, 0 on failure.
@@ -157,6 +159,13 @@ size_t grouped_partial_bytes(bool wide, int units);
 cudaError_t launch_grouped(bool wide, const CUtensorMap& f, const CUtensorMap& x128,
                            const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
                            int units, cudaStream_t st);
+
+// The wide rows form with p.x_scales and p.w_scales (and p.offsets or, for one
+// expert, null), for integers widened to fp16.
+int prepare_scaled(int d_type, int num_sms);
+cudaError_t launch_scaled(const CUtensorMap& f, const CUtensorMap& x128, const CUtensorMap& x32,
+                          const CUtensorMap& d, const GroupedParams& p, int units,
+                          cudaStream_t st);
 
 // ---------------------------------------------------------------- 4-bit weights (w4.cu)
 struct W4Params {

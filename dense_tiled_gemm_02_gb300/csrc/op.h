@@ -64,6 +64,8 @@ struct gemm_op {
   size_t ws_b_off = 0, ws_partial_off = 0, ws_counters_off = 0, ws_maps_off = 0;
   size_t counters_bytes = 0;
   bool wide = false;
+  bool tiles = false;  // i8: on the tensor cores (wide, or tiles of tile_rows rows)
+  int tile_rows = 0;
   int units = 0;
   int grid = 0;  // route: blocks
   gemm_op* inner = nullptr;  // rows8_grad: the grouped product it ends in
@@ -134,7 +136,7 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
 // box_rows, zeros outside.  depth > 0: that many matrices of `rows` rows one
 // after another, as a third dimension.
 inline bool encode_rows(CUtensorMap* tm, const void* base, int64_t ld, int64_t cols, int64_t rows,
-                 int64_t depth, int box_cols, int box_rows) {
+                        int64_t depth, int box_cols, int box_rows) {
   EncodeFn enc = reinterpret_cast<EncodeFn>(tensor_map_encoder());
   if (!enc) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
@@ -143,6 +145,20 @@ inline bool encode_rows(CUtensorMap* tm, const void* base, int64_t ld, int64_t c
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, depth > 0 ? 3 : 2, const_cast<void*>(base), dims,
              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Map of a row-major 8-bit operand in 128-byte swizzled boxes of 128 x 128, zeros outside.
+inline bool encode_bytes(CUtensorMap* tm, const void* base, int64_t ld, int64_t cols, int64_t rows) {
+  EncodeFn enc = reinterpret_cast<EncodeFn>(tensor_map_encoder());
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {128, 128};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "common.h"
+#include "moe.h"
 
 namespace gb300 {
 
@@ -61,7 +62,7 @@ struct Rows8Params {
 cudaError_t launch_rows8_pack(const Rows8Params& p, int num_sms, cudaStream_t st);
 cudaError_t launch_rows8_unpack(const Rows8Params& p, int num_sms, cudaStream_t st);
 
-// ---------------------------------------------------------------- products (i8_rows.cu)
+// ---------------------------------------------------------------- products of few rows (i8_rows.cu)
 struct I8RowsParams {
   int E, R, K, N, d_type;
   long long ldx, ldw, ldd;
@@ -75,5 +76,21 @@ struct I8RowsParams {
   int num_sms;
 };
 cudaError_t launch_i8_rows(const I8RowsParams& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- products of many rows (i8_tiles.cu)
+// Tiles of up to `rows` (64 or 128) rows of X.
+int prepare_i8_tiles(int rows, int d_type, int num_sms);  // as prepare_grouped
+size_t i8_tiles_partial_bytes(int rows, int units);
+// Tensor maps: the weights' bytes in boxes of 128 x 128; X in fp16 in boxes of
+// 64 values x `rows` rows and x 32; D as for launch_grouped.  p: the rows form
+// with scales, offsets null for one expert with all rows.
+cudaError_t launch_i8_tiles(int rows, const CUtensorMap& w, const CUtensorMap& x,
+                            const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
+                            int units, cudaStream_t st);
+// rows x cols bytes to 16-byte aligned rows of ld_dst, as they are or widened to fp16.
+cudaError_t launch_i8_copy(const int8_t* src, long long ld_src, int8_t* dst, long long ld_dst,
+                           long long rows, int cols, int num_sms, cudaStream_t st);
+cudaError_t launch_i8_widen(const int8_t* src, long long ld_src, uint16_t* dst, long long ld_dst,
+                            long long rows, int cols, int num_sms, cudaStream_t st);
 
 }  // namespace gb300

@@ -9,6 +9,7 @@
 
 #include "op.h"
 #include "rows.h"
+#include "tc_launch.h"
 
 using namespace gb300;
 
@@ -275,16 +276,116 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
       !settle(d.ldd, d.N))
     return GEMM_ERR_INVALID_ARG;
   if (!is_float(d.d_type)) return GEMM_ERR_UNSUPPORTED;
+  int sms = 1, dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaGetLastError();
+  // Which kernel: by the rows of an expert on average (the host does not know
+  // the groups).
+  const bool some = d.K > 0 && d.R > 0 && d.N > 0;
+  const bool wide = some && planned("wide", d.R >= 512 * d.E);
+  const bool tiles = wide || (some && planned("tiles", d.R > 16 * d.E));
+  const int rows = wide ? 0 : planned("tall", d.R > 64 * d.E) ? 128 : 64;
+  // X in fp16; W in fp16 (wide), or a copy where the TMA unit cannot read its
+  // rows; partial sums and counters of shared tiles
+  const bool copy_w = wide || (tiles && d.ldw % 16 != 0);
+  const int most_units = std::max(1, wide ? sms / 2 : sms);
+  const int64_t ws_ldx = up(d.K, 64), ws_ldw = wide ? ws_ldx : up(d.K, 128);
+  const size_t x_bytes = tiles ? static_cast<size_t>(up(2 * d.R * ws_ldx, 256)) : 0;
+  const size_t w_bytes = copy_w ? static_cast<size_t>(d.E * d.N * ws_ldw * (wide ? 2 : 1)) : 0;
+  const size_t p_off = static_cast<size_t>(up(static_cast<int64_t>(x_bytes + w_bytes), 256));
+  const size_t partial = wide    ? grouped_partial_bytes(true, most_units)
+                         : tiles ? i8_tiles_partial_bytes(rows, most_units)
+                                 : 0;
+  const size_t counters = tiles ? 4 * static_cast<size_t>(most_units) * (wide ? 2 : 1) : 0;
   gemm_op* op = nullptr;
-  const int rc = make_op(Kind::kI8, 0, 0, 0, &op);
+  const int rc = make_op(Kind::kI8, p_off + partial + counters, p_off + partial, counters, &op);
   if (rc != GEMM_OK) return rc;
   op->i8 = d;
-  std::snprintf(op->plan, sizeof op->plan, "i8 E=%d R=%lld K=%lld N=%lld", d.E,
-                static_cast<long long>(d.R), static_cast<long long>(d.K),
-                static_cast<long long>(d.N));
+  if (tiles) {
+    op->units = std::min(most_units, wide ? prepare_scaled(d.d_type, op->num_sms)
+                                          : prepare_i8_tiles(rows, d.d_type, op->num_sms));
+    if (op->units <= 0) {
+      cudaGetLastError();
+      gemm_op_destroy(op);
+      return GEMM_ERR_CUDA;
+    }
+  }
+  op->tiles = tiles;
+  op->wide = wide;
+  op->tile_rows = rows;
+  op->copy_b = copy_w;
+  op->ws_lda = ws_ldx;
+  op->ws_ldb = copy_w ? ws_ldw : d.ldw;
+  op->ws_b_off = x_bytes;
+  op->ws_partial_off = p_off;
+  op->ws_counters_off = p_off + partial;
+  op->counters_bytes = counters;
+  std::snprintf(op->plan, sizeof op->plan, "i8 E=%d R=%lld K=%lld N=%lld form=%s rows=%d copy=%d units=%d",
+                d.E, static_cast<long long>(d.R), static_cast<long long>(d.K),
+                static_cast<long long>(d.N), wide ? "wide" : tiles ? "tiles" : "rows", rows, copy_w,
+                op->units);
   *out = op;
   return GEMM_OK;
 }
+
+}  // extern "C"
+
+namespace {
+
+int run_i8_tiles(gemm_op_t op, const int8_t* X, const float* x_scales, const int8_t* W,
+                 const float* w_scales, const int32_t* offsets, void* D, cudaStream_t st) {
+  const gemm_i8_desc_t& d = op->i8;
+  const bool wide = op->wide;
+  const int K = static_cast<int>(d.K);
+  const int64_t w_rows = d.E * d.N;
+  uint8_t* const ws = static_cast<uint8_t*>(op->ws);
+  uint16_t* const wx = reinterpret_cast<uint16_t*>(ws);
+  int rc = launched(launch_i8_widen(X, d.ldx, wx, op->ws_lda, d.R, K, op->num_sms, st));
+  const void* w = W;
+  if (rc == GEMM_OK && op->copy_b) {
+    void* const to = ws + op->ws_b_off;
+    rc = launched(wide ? launch_i8_widen(W, d.ldw, static_cast<uint16_t*>(to), op->ws_ldb, w_rows, K,
+                                         op->num_sms, st)
+                       : launch_i8_copy(W, d.ldw, static_cast<int8_t*>(to), op->ws_ldb, w_rows, K,
+                                        op->num_sms, st));
+    w = to;
+  }
+  if (rc != GEMM_OK) return rc;
+  CUtensorMap wm{}, x{}, x32{}, dm{};
+  if (!(wide ? encode_rows(&wm, w, op->ws_ldb, d.K, w_rows, 0, BK, 128)
+             : encode_bytes(&wm, w, op->ws_ldb, d.K, w_rows)) ||
+      !encode_rows(&x, wx, op->ws_lda, d.K, d.R, 0, BK, wide ? 128 : op->tile_rows) ||
+      !encode_rows(&x32, wx, op->ws_lda, d.K, d.R, 0, BK, 32))
+    return GEMM_ERR_CUDA;
+  GroupedParams p{};
+  p.E = d.E;
+  p.R = static_cast<int>(d.R);
+  p.K = K;
+  p.N = static_cast<int>(d.N);
+  p.idesc = idesc_f16(0, 0, 0, wide ? 256 : 128, 0);
+  p.offsets = offsets;
+  p.d_type = d.d_type;
+  p.d_vec = is_16bit(d.d_type) && d.ldd % 8 == 0 && aligned(D, 16);
+  p.d_tma = p.d_vec && d.N % 8 == 0;
+  if (p.d_tma && !encode_rows(&dm, D, d.ldd, d.N, d.R, 1, 64, 32)) return GEMM_ERR_CUDA;
+  p.ldd = d.ldd;
+  p.D = D;
+  p.partial = reinterpret_cast<float*>(ws + op->ws_partial_off);
+  p.counters = reinterpret_cast<unsigned*>(ws + op->ws_counters_off);
+  p.status = op->status;
+  p.timeout_ns = op->timeout_ns;
+  p.debug_flags = op->debug_flags;
+  op->debug_flags = 0;
+  p.x_scales = x_scales;
+  p.w_scales = w_scales;
+  return launched(wide ? launch_scaled(wm, x, x32, dm, p, op->units, st)
+                       : launch_i8_tiles(op->tile_rows, wm, x, x32, dm, p, op->units, st));
+}
+
+}  // namespace
+
+extern "C" {
 
 int gemm_i8_run(gemm_op_t op, const int8_t* X, const float* x_scales, const int8_t* W,
                 const float* w_scales, const int32_t* offsets, void* D, gemm_stream_t stream) {
@@ -294,8 +395,10 @@ int gemm_i8_run(gemm_op_t op, const int8_t* X, const float* x_scales, const int8
   if (!D || !x_scales || !w_scales || (d.K > 0 && (!X || !W)) || (d.E > 1 && !offsets))
     return GEMM_ERR_INVALID_ARG;
   if (!aligned(D, elem_size(d.d_type)) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
-      !aligned(offsets, 4))
+      !aligned(offsets, 4) || (d.ldw % 16 == 0 && !aligned(W, 16)))
     return GEMM_ERR_MISALIGNED;
+  if (op->tiles)
+    return run_i8_tiles(op, X, x_scales, W, w_scales, offsets, D, static_cast<cudaStream_t>(stream));
   I8RowsParams p{};
   p.E = d.E;
   p.R = static_cast<int>(d.R);

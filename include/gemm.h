@@ -671,8 +671,10 @@ GEMM_API int gemm_rows8_grad_run(gemm_op_t op, const int8_t* q, const uint8_t* E
  * X: R x K int8 (ldx); W: E matrices N x K int8 one after another, E * N rows
  * ldw apart; w_scales E x N fp32; D R x N (ldd), F16, BF16 or F32.  With E = 1
  * offsets may be NULL (all R rows); otherwise they group the rows as above,
- * and rows of no expert are not written.  The sums are exact as long as they
- * stay below 2^24 (always up to K = 1024), and beyond that off by at most
+ * and rows of no expert are not written.  W is 16-byte aligned where ldw is a
+ * multiple of 16 (else GEMM_ERR_MISALIGNED); other rows of W, when there are
+ * more than a few of X, are copied to aligned ones on each call.  The sums are
+ * exact as long as they stay below 2^24 (always up to K = 1024), and beyond that off by at most
  * K * 2^-24 of the sum of magnitudes; scaled in fp32 and rounded once.
  * K < 2^17.
  */

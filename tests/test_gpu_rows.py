@@ -489,38 +489,81 @@ SIZES = [(64, 16), (64, 64), (128, 256), (1000, 264), (33, 61), (1, 1), (15, 7),
          (4096, 512), (272, 1040)]
 
 
+# the few-rows kernel, the tensor-core tiles of 64 and of 128 rows, and of CTA pairs
+PLANS = ["tiles=0,wide=0", "tiles=1,wide=0,tall=0", "tiles=1,wide=0,tall=1", "wide=1"]
+
+
+@pytest.mark.parametrize("plan", PLANS)
 @pytest.mark.parametrize("R", [1, 2, 8, 9, 16, 17, 40, 64, 65, 130, 300])
 @pytest.mark.parametrize("K,N", SIZES)
-def test_i8_dense(R, K, N):
-    i8_check([R], K, N, [BF16, F16, F32][(R + K) % 3], seed=R + K)
+def test_i8_dense(R, K, N, plan):
+    i8_check([R], K, N, [BF16, F16, F32][(R + K) % 3], seed=R + K, plan=plan)
 
 
+@pytest.mark.parametrize("R,K,N", [(1, 640, 320), (16, 640, 320), (17, 640, 320), (64, 8192, 512),
+                                   (600, 512, 512), (1500, 2048, 2304), (4000, 256, 4096)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_i8_as_planned(R, K, N, out):
+    """Without a forced plan; more tiles than CTAs, and tiles shared by several."""
+    i8_check([R], K, N, out)
+
+
+@pytest.mark.parametrize("plan", PLANS)
 @pytest.mark.parametrize("counts", [[1, 0, 2, 0, 0, 1, 3, 0, 1, 0, 0, 0, 0, 0, 0, 1, 2],
                                     [0, 1, 33, 0, 256, 31, 32, 257, 0], [600, 5, 129], [0, 0, 0],
                                     [9, 20, 0, 17]])
 @pytest.mark.parametrize("K,N,out", [(64, 128, BF16), (200, 328, F16), (1000, 264, F32),
                                      (33, 61, BF16), (2048, 96, BF16)])
-def test_i8_experts(counts, K, N, out):
-    i8_check(counts, K, N, out)
+def test_i8_experts(counts, K, N, out, plan):
+    i8_check(counts, K, N, out, plan=plan)
 
 
+@pytest.mark.parametrize("plan", PLANS)
 @pytest.mark.parametrize("counts", [[3], [70], [5, 0, 90, 33]])
 @pytest.mark.parametrize("K,N,pad", [(128, 64, 16), (128, 64, 1), (100, 33, 12), (513, 72, 7)])
-def test_i8_strides_and_rows_of_no_expert(counts, K, N, pad):
-    i8_check(counts, K, N, BF16, pad=pad)
-    i8_check(counts, K, N, F16, pad=pad, first=5)
+def test_i8_strides_and_rows_of_no_expert(counts, K, N, pad, plan):
+    i8_check(counts, K, N, BF16, pad=pad, plan=plan)
+    i8_check(counts, K, N, F16, pad=pad, first=5, plan=plan)
 
 
+@pytest.mark.parametrize("plan", PLANS)
 @pytest.mark.parametrize("R", [1, 16, 64, 200])
-def test_i8_extremes(R):
+def test_i8_extremes(R, plan):
     """Every value -128 and every product 2^14: 1024 of them are 2^24, exactly."""
     K, N = 1024, 160
     x = torch.full((R, K), -128, dtype=torch.int8, device="cuda")
     w = torch.full((1, N, K), -128, dtype=torch.int8, device="cuda")
-    i8_check([R], K, N, F32, x=x, w=w)
+    i8_check([R], K, N, F32, x=x, w=w, plan=plan)
     w[:, ::2] = 127
     x[:, 1::2] = 127
-    i8_check([R], K, N, F32, x=x, w=w)
+    i8_check([R], K, N, F32, x=x, w=w, plan=plan)
+
+
+@pytest.mark.parametrize("plan", PLANS[1:])
+@pytest.mark.parametrize("flag", [pkg.GEMM_DEBUG_SKIP_FIRST_FILL, pkg.GEMM_DEBUG_SKIP_ONE_FILL])
+@pytest.mark.parametrize("counts", [[700], [40] * 20])
+def test_i8_after_a_timeout(plan, flag, counts):
+    """A wait that runs out is reported, and the next call starts afresh."""
+    R, K, N = sum(counts), 1536, 1000
+    off = offsets_of(counts) if len(counts) > 1 else None
+    X, W = ints((R, K), 1), ints((len(counts), N, K), 2)
+    xs, ws = torch.ones(R, device="cuda"), torch.ones((len(counts), N), device="cuda")
+    D = torch.zeros((R, N), device="cuda")
+    with forced_plan(plan):
+        op = pkg.I8Gemm.like(X, xs, W, ws, off, D)
+    op.run(X, xs, W, ws, off, D)
+    assert op.status() == pkg.GEMM_OK
+    first = D.clone()
+    for timeout_ns in (1_000_000, 10_000_000):
+        op.debug_set(flag, timeout_ns)
+        op.run(X, xs, W, ws, off, D)
+        assert op.status() == pkg.GEMM_ERR_DEVICE_TIMEOUT
+        op.debug_set(0)
+        D.fill_(7.0)
+        op.run(X, xs, W, ws, off, D)
+        assert op.status() == pkg.GEMM_OK
+        assert torch.equal(D, first)
+    op.close()
 
 
 @pytest.mark.parametrize("R", [1, 33])
