@@ -39,18 +39,23 @@ constexpr int SLICE = 128;                    // K of a stage: a 128-byte row of
 constexpr uint32_t W_BYTES = FT * SLICE;
 constexpr int TILE_EPI_WARPS = 4;
 constexpr int CONV_GROUPS = 2;                // of four warps, taking stages in turn
-// warp 0: TMA loads, 1: MMA issue, 2-5: epilogue, 6: schedule, from 7: converters
-constexpr int I8_THREADS = 32 * (7 + 4 * CONV_GROUPS);
+constexpr int X_WARP = 7 + 4 * CONV_GROUPS;
+// warp 0: W's loads, 1: MMA issue, 2-5: epilogue, 6: schedule, from 7: converters,
+// last: X's loads
+constexpr int I8_THREADS = 32 * (X_WARP + 1);
 
-template <int QT, int STAGES>
+// WS stages of W on their way; XS of X, each with a slot of tensor memory for
+// the W that meets it.
+template <int QT>
 struct Cfg {
+  static constexpr int WS = QT == 64 ? 9 : 6, XS = 3;
   static constexpr uint32_t X_SUB = QT * BK * 2;  // 64 values of each row
   static constexpr uint32_t X_BYTES = 2 * X_SUB;
-  // Tensor memory: two accumulators, then a slot of 128 values a row for each stage.
+  // Tensor memory: two accumulators, then the slots.
   static constexpr uint32_t SLOT0 = 2 * QT;
-  static_assert(SLOT0 + 64 * STAGES <= 512, "tensor memory");
+  static_assert(SLOT0 + 64 * XS <= 512, "tensor memory");
   static constexpr uint32_t BAR_BYTES = 768;
-  static constexpr uint32_t SMEM = 1024 + STAGES * (W_BYTES + X_BYTES) + EPI_BYTES + BAR_BYTES +
+  static constexpr uint32_t SMEM = 1024 + WS * W_BYTES + XS * X_BYTES + EPI_BYTES + BAR_BYTES +
                                    4 * (2 * GEMM_MAX_EXPERTS + 2);
   static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
   static_assert(X_SUB % 1024 == 0, "stage alignment");
@@ -83,20 +88,24 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 // ---------------------------------------------------------------- kernel
-template <int QT, int STAGES, int DT>
+// SPLIT: a cluster of `split` CTAs takes one tile, each its part of K, and they
+// add their sums up through shared memory; else CTAs take tiles by the schedule.
+template <int QT, int DT, bool SPLIT>
 __global__ void __launch_bounds__(I8_THREADS, 1)
     i8_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const __grid_constant__ CUtensorMap tmX32,
-                    const __grid_constant__ CUtensorMap tmD, const GroupedParams p) {
-  using C = Cfg<QT, STAGES>;
+                    const __grid_constant__ CUtensorMap tmD, const GroupedParams p,
+                    const int split) {
+  using C = Cfg<QT>;
+  constexpr int WS = C::WS, XS = C::XS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sW = smem;
-  uint8_t* const sX = smem + STAGES * W_BYTES;
-  uint8_t* const sE = sX + STAGES * C::X_BYTES;
+  uint8_t* const sX = smem + WS * W_BYTES;
+  uint8_t* const sE = sX + XS * C::X_BYTES;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sE + EPI_BYTES);
-  constexpr int NBARS = 3 * STAGES + 5 + 2 * QUEUE;
+  constexpr int NBARS = 2 * WS + 3 * XS + 5 + 2 * QUEUE;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* const ep_go = abort_flag + 1;  // two, taken in turn
@@ -107,31 +116,38 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
   int* const prefix = lo + p.E + 1;
 
   const uint32_t bar0 = smem_u32(bars);
-  auto full = [&](uint32_t s) { return bar0 + 8u * s; };                     // loaded
-  auto ready = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };         // and converted
-  auto empty = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + s); };
-  auto acc_full = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + b); };
-  auto acc_empty = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
-  const uint32_t done_bar = bar0 + 8u * (3 * STAGES + 4);
-  auto q_full = [&](uint32_t i) { return bar0 + 8u * (3 * STAGES + 5 + i); };
-  auto q_empty = [&](uint32_t i) { return bar0 + 8u * (3 * STAGES + 5 + QUEUE + i); };
+  auto w_full = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto w_empty = [&](uint32_t s) { return bar0 + 8u * (WS + s); };
+  auto x_full = [&](uint32_t c) { return bar0 + 8u * (2 * WS + c); };
+  auto ready = [&](uint32_t c) { return bar0 + 8u * (2 * WS + XS + c); };  // W in the slot
+  auto done = [&](uint32_t c) { return bar0 + 8u * (2 * WS + 2 * XS + c); };
+  constexpr uint32_t REST = 2 * WS + 3 * XS;
+  auto acc_full = [&](uint32_t b) { return bar0 + 8u * (REST + b); };
+  auto acc_empty = [&](uint32_t b) { return bar0 + 8u * (REST + 2 + b); };
+  const uint32_t end_bar = bar0 + 8u * (REST + 4);
+  auto q_full = [&](uint32_t i) { return bar0 + 8u * (REST + 5 + i); };
+  auto q_empty = [&](uint32_t i) { return bar0 + 8u * (REST + 5 + QUEUE + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(ready(s), 4);
-      mbar_init(empty(s), 1);
+    for (int s = 0; s < WS; ++s) {
+      mbar_init(w_full(s), 1);
+      mbar_init(w_empty(s), 4);  // a converter warp's arrival each
+    }
+    for (int c = 0; c < XS; ++c) {
+      mbar_init(x_full(c), 1);
+      mbar_init(ready(c), 4);
+      mbar_init(done(c), 1);
     }
     for (int i = 0; i < QUEUE; ++i) {
       mbar_init(q_full(i), 1);
-      mbar_init(q_empty(i), 2 + TILE_EPI_WARPS + 4 * CONV_GROUPS);  // a warp's arrival each
+      mbar_init(q_empty(i), 3 + TILE_EPI_WARPS + 4 * CONV_GROUPS);  // a warp's arrival each
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
       mbar_init(acc_empty(b), TILE_EPI_WARPS);
     }
-    mbar_init(done_bar, 1);
+    mbar_init(end_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -146,41 +162,72 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
   }
-  pdl_wait();
-  pdl_trigger();
-  for (int e = threadIdx.x; e <= p.E; e += I8_THREADS) {
-    // without offsets all rows are the one expert's
-    lo[e] = p.offsets ? p.offsets[e] : e * p.R;
-    if (p.offsets && e < p.E) expert_rows(p.offsets, e, p.R, p.status);
-  }
-  __syncthreads();
-  if (warp == 2) {  // the prefix: each lane a run of experts, then a warp scan
-    auto count = [&](int e) { return row_tiles<QT>(rows_of(p, lo, e)); };
-    const int len = (p.E + 31) / 32, b = min(p.E, lane * len), e1 = min(p.E, b + len);
-    int sum = 0;
-    for (int e = b; e < e1; ++e) sum += count(e);
-    int inc = sum;
+  if (!p.offsets) {  // one expert has all rows: nothing to read
+    if (threadIdx.x == 0) {
+      lo[0] = prefix[0] = 0;
+      lo[1] = p.R;
+      prefix[1] = row_tiles<QT>(p.R);
+    }
+  } else {
+    pdl_wait();
+    for (int e = threadIdx.x; e <= p.E; e += I8_THREADS) {
+      lo[e] = p.offsets[e];
+      if (e < p.E) expert_rows(p.offsets, e, p.R, p.status);
+    }
+    __syncthreads();
+    if (warp == 2) {  // the prefix: each lane a run of experts, then a warp scan
+      auto count = [&](int e) { return row_tiles<QT>(rows_of(p, lo, e)); };
+      const int len = (p.E + 31) / 32, b = min(p.E, lane * len), e1 = min(p.E, b + len);
+      int sum = 0;
+      for (int e = b; e < e1; ++e) sum += count(e);
+      int inc = sum;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-      if (lane >= d) inc += u;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+        if (lane >= d) inc += u;
+      }
+      int at = inc - sum;
+      for (int e = b; e < e1; ++e) {
+        prefix[e] = at;
+        at += count(e);
+      }
+      if (lane == 31) prefix[p.E] = inc;
     }
-    int at = inc - sum;
-    for (int e = b; e < e1; ++e) {
-      prefix[e] = at;
-      at += count(e);
-    }
-    if (lane == 31) prefix[p.E] = inc;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const uint64_t tmo = p.timeout_ns;
+  pdl_trigger();
   // The next piece of this CTA's work, taken by one warp for itself; false at
   // its end or after a timeout.
   uint32_t q_at = 0, q_ph = 0;
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  bool taken = false;
   auto next_piece = [&](Piece& x) {
+    if constexpr (SPLIT) {  // the cluster's tile, and this CTA's slices of it
+      const int ft = (p.N + FT - 1) / FT, tile = blockIdx.x / split;
+      if (taken || tile >= prefix[p.E] * ft) return false;
+      taken = true;
+      int a = 0, b = p.E;  // the expert: prefix[a] * ft <= tile < prefix[a + 1] * ft
+      while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (prefix[m] * ft <= tile)
+          a = m;
+        else
+          b = m;
+      }
+      const int rows = rows_of(p, lo, a), rt = prefix[a + 1] - prefix[a], w = tile_width(rows, rt);
+      const int t = tile - prefix[a] * ft, q = t % rt * w, slices = slices_of<SLICE>(p.K);
+      x.e = a;
+      x.f0 = t / rt * FT;
+      x.q0 = lo[a] + q;
+      x.nq = min(w, rows - q);
+      x.k = rank * slices / split * SLICE;
+      x.kend = min(p.K, (rank + 1) * slices / split * SLICE);
+      return true;
+    }
     bool ok = true;
     if (lane == 0)
       ok = bounded_wait(q_full(q_at), q_ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
@@ -198,7 +245,9 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
   };
   Piece x;
 
-  if (warp == 6) {
+  if (warp == 6 && SPLIT) {
+    // (each warp finds its one piece itself)
+  } else if (warp == 6) {
     // ------------------------------------------------------------ schedule
     Schedule<1, QT, SLICE> work(p, lo, prefix, blockIdx.x, gridDim.x);
     if (lane == 0) {
@@ -216,56 +265,79 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ loads of W
     uint32_t it = 0, s = 0, ph = 0;
     bool stop = false, skipped = false;
     const bool skip = (p.debug_flags & DBG_SKIP_FIRST_FILL) ||
                       ((p.debug_flags & DBG_SKIP_ONE_FILL) && blockIdx.x == 0);
-    const uint32_t sW0 = smem_u32(sW), sX0 = smem_u32(sX);
+    const uint32_t sW0 = smem_u32(sW);
+    pdl_wait();
     while (next_piece(x)) {
       if (elect_one() && !stop) {
         const int wrow = x.e * p.N + x.f0;
-        const bool big = x.nq > 32;
-        const uint32_t bytes = W_BYTES + 2u * (big ? C::X_SUB : 4096u);
-        auto slices = [&](const CUtensorMap* tm) {
-          for (int k = x.k; k < x.kend; k += SLICE) {
-            if (!bounded_wait(empty(s), ph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo)) {
-              stop = true;
-              return;
-            }
-            if (it == 0 && skip) {
-              skipped = true;  // test hook: the waits on the first stage expire
-            } else {
-              mbar_arrive_expect_tx(full(s), bytes);
-              tma_load_2d(sW0 + s * W_BYTES, &tmW, k, wrow, full(s));
-              tma_load_2d(sX0 + s * C::X_BYTES, tm, k, x.q0, full(s));
-              tma_load_2d(sX0 + s * C::X_BYTES + C::X_SUB, tm, k + BK, x.q0, full(s));
-            }
-            ++it;
-            if (++s == STAGES) {
-              s = 0;
-              ph ^= 1u;
-            }
+        for (int k = x.k; k < x.kend; k += SLICE) {
+          if (!bounded_wait(w_empty(s), ph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo)) {
+            stop = true;
+            break;
           }
-        };
-        if (big)
-          slices(&tmX);
-        else
-          slices(&tmX32);
+          if (it == 0 && skip) {
+            skipped = true;  // test hook: the converters' wait on the first stage expires
+          } else {
+            mbar_arrive_expect_tx(w_full(s), W_BYTES);
+            tma_load_2d(sW0 + s * W_BYTES, &tmW, k, wrow, w_full(s));
+          }
+          ++it;
+          if (++s == WS) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
       }
       __syncwarp();
     }
     if (elect_one()) {
       // copies in flight land before the CTA leaves
-      for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j)
-        if (!(skipped && j == 0)) drain_wait(full(j % STAGES), (j / STAGES) & 1u, 200000000ull);
+      for (uint32_t j = it > WS ? it - WS : 0; j < it; ++j)
+        if (!(skipped && j == 0)) drain_wait(w_full(j % WS), (j / WS) & 1u, 200000000ull);
     }
+    __syncwarp();
+  } else if (warp == X_WARP) {
+    // ------------------------------------------------------------ loads of X
+    uint32_t it = 0, c = 0, ph = 0;
+    bool stop = false;
+    const uint32_t sX0 = smem_u32(sX);
+    pdl_wait();
+    while (next_piece(x)) {
+      if (elect_one() && !stop) {
+        const bool big = x.nq > 32;
+        const uint32_t bytes = 2u * (big ? C::X_SUB : 4096u);
+        const CUtensorMap* const tm = big ? &tmX : &tmX32;
+        for (int k = x.k; k < x.kend; k += SLICE) {
+          if (!bounded_wait(done(c), ph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo)) {
+            stop = true;
+            break;
+          }
+          mbar_arrive_expect_tx(x_full(c), bytes);
+          tma_load_2d(sX0 + c * C::X_BYTES, tm, k, x.q0, x_full(c));
+          tma_load_2d(sX0 + c * C::X_BYTES + C::X_SUB, tm, k + BK, x.q0, x_full(c));
+          ++it;
+          if (++c == XS) {
+            c = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      __syncwarp();
+    }
+    if (elect_one())
+      for (uint32_t j = it > XS ? it - XS : 0; j < it; ++j)
+        drain_wait(x_full(j % XS), (j / XS) & 1u, 200000000ull);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t x_lo0 = sdesc_lo(smem_u32(sX), 16u);
     const uint32_t dhi = sdesc_hi_sw128(1024u);
-    uint32_t s = 0, ph = 0, acc_it = 0;
+    uint32_t c = 0, ph = 0, acc_it = 0;
     bool ok = true;
     while (next_piece(x)) {
       if (elect_one() && ok && x.k < x.kend) {
@@ -276,24 +348,24 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
                           STATUS_TIMEOUT, tmo);
         uint32_t accumulate = 0;
         for (int k = x.k; ok && k < x.kend; k += SLICE) {
-          ok = bounded_wait(ready(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo) &&
-               bounded_wait(full(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
+          ok = bounded_wait(x_full(c), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo) &&
+               bounded_wait(ready(c), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = tmem_base + C::SLOT0 + s * 64u;
-          const uint32_t b = x_lo0 + s * (C::X_BYTES >> 4);
+          const uint32_t a = tmem_base + C::SLOT0 + c * 64u;
+          const uint32_t b = x_lo0 + c * (C::X_BYTES >> 4);
           // (values past K are zeros on both sides)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            mma_ts(d_tmem, a + 8u * c, sdesc(dhi, b + 2u * c), idesc, accumulate | c);
+          for (int i = 0; i < 4; ++i)
+            mma_ts(d_tmem, a + 8u * i, sdesc(dhi, b + 2u * i), idesc, accumulate | i);
           if (x.kend - k > BK)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              mma_ts(d_tmem, a + 32u + 8u * c, sdesc(dhi, b + (C::X_SUB >> 4) + 2u * c), idesc, 1u);
+            for (int i = 0; i < 4; ++i)
+              mma_ts(d_tmem, a + 32u + 8u * i, sdesc(dhi, b + (C::X_SUB >> 4) + 2u * i), idesc, 1u);
           accumulate = 1;
-          mma_commit(empty(s));
-          if (++s == STAGES) {
-            s = 0;
+          mma_commit(done(c));
+          if (++c == XS) {
+            c = 0;
             ph ^= 1u;
           }
         }
@@ -303,8 +375,8 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
       __syncwarp();
     }
     if (elect_one()) {
-      mma_commit(done_bar);
-      drain_wait(done_bar, 0, 200000000ull);
+      mma_commit(end_bar);
+      drain_wait(end_bar, 0, 200000000ull);
     }
     __syncwarp();
   } else if (warp > 6) {
@@ -315,13 +387,14 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
     const int q = warp & 3, group = (warp - 7) >> 2, row = 32 * q + lane;
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + C::SLOT0;
     const uint8_t* const src0 = sW + row * SLICE;
-    uint32_t s = 0, ph = 0;
+    uint32_t s = 0, ph = 0, c = 0, cph = 0;
     int turn = 0;
     bool ok = true;
     while (next_piece(x)) {
       for (int k = x.k; ok && k < x.kend; k += SLICE) {
         if (turn == group) {
-          ok = bounded_wait(full(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
+          ok = bounded_wait(w_full(s), ph, abort_flag, p.status, STATUS_TIMEOUT, tmo) &&
+               bounded_wait(done(c), cph ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, tmo);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -337,22 +410,31 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
               widen4(w.z, v[8 * u + 4], v[8 * u + 5]);
               widen4(w.w, v[8 * u + 6], v[8 * u + 7]);
             }
-            tmem_st_32x32b_x32(taddr + s * 64u + sub * 32u, v);
+            tmem_st_32x32b_x32(taddr + c * 64u + sub * 32u, v);
           };
           convert(0);
           if (x.kend - k > BK) convert(1);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(ready(s));
+          if (lane == 0) {
+            mbar_arrive(ready(c));
+            mbar_arrive(w_empty(s));
+          }
         }
         turn = turn + 1 == CONV_GROUPS ? 0 : turn + 1;
-        if (++s == STAGES) {
+        if (++s == WS) {
           s = 0;
           ph ^= 1u;
         }
+        if (++c == XS) {
+          c = 0;
+          cph ^= 1u;
+        }
       }
     }
+  } else if constexpr (SPLIT) {
+    // ------------------------------------------------------------ epilogue: below
   } else {
     // ------------------------------------------------------------ epilogue
     // As in grouped.cu, with the scales: of features one or four a thread, of
@@ -362,18 +444,16 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
     const bool ep_leader = threadIdx.x == 64;
     uint32_t acc_it = 0;
     const int unit = blockIdx.x;
-    for (uint32_t turn = 0;; turn ^= 1u) {
+    pdl_wait();
+    for (;;) {
       const uint32_t buf = acc_it & 1u;
-      // One thread decides for all four warps whether there is a piece and its sums.
-      if (ep_leader) {
-        bool go = bounded_wait(q_full(q_at), q_ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
-        if (go && queue[q_at].more && queue[q_at].k < queue[q_at].kend)
-          go = bounded_wait(acc_full(buf), (acc_it >> 1) & 1u, abort_flag, p.status,
-                            STATUS_TIMEOUT, tmo);
-        ep_go[turn] = go ? 1 : 0;
-      }
+      // One thread decides for all four warps whether there is a piece, and
+      // then whether it has its sums; the scales of its features and first rows
+      // come in between.
+      if (ep_leader)
+        ep_go[0] = bounded_wait(q_full(q_at), q_ph, abort_flag, p.status, STATUS_TIMEOUT, tmo);
       named_barrier_sync(1, 32 * TILE_EPI_WARPS);
-      if (!ep_go[turn]) break;
+      if (!ep_go[0]) break;
       x = queue[q_at];
       __syncwarp();
       if (lane == 0) mbar_arrive(q_empty(q_at));
@@ -382,7 +462,6 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
         q_ph ^= 1u;
       }
       if (!x.more) break;
-      tc_fence_after();
       auto release = [&] {  // the accumulator has been read
         tc_fence_before();
         __syncwarp();
@@ -394,6 +473,22 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
       const float* const rs = p.x_scales + x.q0;  // the tile's rows
       auto f_scale = [&](int i) { return i < p.N ? fs[i] : 0.f; };
       auto r_scale = [&](int i) { return i < x.nq ? rs[i] : 0.f; };
+      // of features 8 i + lane / 4 of the warp's 32, and of rows 8 (i / 2) +
+      // 2 (lane % 4) + i % 2 of a chunk: as the fragments of the accumulator lie
+      float sf[4], sr[8];
+      auto load_sr = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sr[i] = r_scale(c + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1));
+      };
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sf[i] = f_scale(f0 + 8 * i + (lane >> 2));
+      load_sr(0);
+      if (ep_leader)
+        ep_go[1] = bounded_wait(acc_full(buf), (acc_it >> 1) & 1u, abort_flag, p.status,
+                                STATUS_TIMEOUT, tmo);
+      named_barrier_sync(1, 32 * TILE_EPI_WARPS);
+      if (!ep_go[1]) break;
+      tc_fence_after();
       const long long row0 = x.q0;
       const uint32_t taddr = tmem_base + lane_base + buf * QT;
       auto c_last = [&](int c) { return c + 32 >= x.nq; };
@@ -441,14 +536,9 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
       if (x.pieces == 1 && staged_store) {
         // fragments of 16 features x 8 rows, scaled, and transposed into rows by stmatrix
         if constexpr (DT != T_F32) {
-          float sf[4];  // features 16 h + 8 b + lane / 4 at 2 h + b
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sf[i] = f_scale(f0 + 8 * i + (lane >> 2));
 #pragma unroll 1
           for (int c = 0; c < x.nq; c += 32) {
-            float sr[8];  // rows 8 i + 2 (lane % 4) + b at 2 i + b
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sr[i] = r_scale(c + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1));
+            if (c > 0) load_sr(c);
             uint32_t r[32];
             tmem_ld_16x256b_x4(taddr + c, r);
             tmem_ld_16x256b_x4(taddr + c + (16u << 16), r + 16);
@@ -575,7 +665,75 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
       }
       ++acc_it;
     }
-    if (ep_leader) bulk_wait_all();  // shared memory outlives the stores that read it
+    if (ep_leader) bulk_wait_read<0>();  // shared memory outlives the stores that read it
+  }
+  if constexpr (SPLIT) {
+    // Each CTA finishes QT / split of the tile's rows and gets the others' sums
+    // of them, [CTA][four rows][feature] float4, in what was the stages' shared
+    // memory: all MMAs of the cluster are done and all copies have landed once
+    // its threads meet.
+    const int rows = QT / split, groups = rows / 4 * FT;
+    float4* const sums = reinterpret_cast<float4*>(smem);
+    taken = false;
+    const bool tile = next_piece(x);
+    pdl_wait();
+    // the scales of this thread's first four outputs, on their way meanwhile
+    const int f1 = x.f0 + threadIdx.x % FT, r1 = rank * rows + threadIdx.x / FT * 4;
+    float sw = 0.f, sx[4] = {};
+    if (tile && f1 < p.N) {
+      sw = p.w_scales[static_cast<long long>(x.e) * p.N + f1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r1 + j < x.nq) sx[j] = p.x_scales[x.q0 + r1 + j];
+    }
+    __syncwarp();
+    cluster_sync_all();
+    tc_fence_after();
+    const bool join = tile && *abort_flag == 0;
+    if (join && warp >= 2 && warp != 6 && warp != X_WARP) {
+      // twelve warps, three to a quarter of tensor memory, in turn over 16 rows
+      const int q = warp & 3, part = warp < 6 ? 0 : (warp - 3) >> 2;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      const uint32_t mine = smem_u32(sums + rank * groups + q * 32 + lane);
+#pragma unroll 1
+      for (int c = 16 * part; c < x.nq; c += 48) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(taddr + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = c + 4 * j;  // of the tile, of its owner's row % rows
+          const uint32_t at = map_shared_rank(mine, row / rows) + row % rows / 4 * (FT * 16);
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[4 * j]),
+                       "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3])
+                       : "memory");
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    if (join) {
+      for (int i = threadIdx.x; i < groups; i += I8_THREADS) {
+        const int f = x.f0 + i % FT, r0 = rank * rows + i / FT * 4;
+        if (f >= p.N || r0 >= x.nq) continue;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < split; ++c) {  // in K order
+          const float4 v = sums[c * groups + i];
+          t.x += v.x;
+          t.y += v.y;
+          t.z += v.z;
+          t.w += v.w;
+        }
+        const bool first = i == threadIdx.x;
+        const float s = first ? sw : p.w_scales[static_cast<long long>(x.e) * p.N + f];
+        const float v[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (r0 + j < x.nq)
+            store_d<DT>(p.D, static_cast<long long>(x.q0 + r0 + j) * p.ldd + f,
+                        v[j] * (first ? sx[j] : p.x_scales[x.q0 + r0 + j]) * s);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -631,37 +789,55 @@ cudaError_t copy_rows(const int8_t* src, long long ld_src, void* dst, long long 
 }
 
 // ---------------------------------------------------------------- launches
-// Tiles of up to 64 rows, or up to 128.
-constexpr int STAGES64 = 6, STAGES128 = 4;
-
-template <int QT, int STAGES, int DT>
-int prepare(int num_sms) {
-  return cudaFuncSetAttribute(i8_tiles_kernel<QT, STAGES, DT>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<QT, STAGES>::SMEM) == cudaSuccess
-             ? num_sms
-             : 0;
+template <int QT, int DT>
+cudaError_t set_smem(bool split) {
+  return split ? cudaFuncSetAttribute(i8_tiles_kernel<QT, DT, true>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<QT>::SMEM)
+               : cudaFuncSetAttribute(i8_tiles_kernel<QT, DT, false>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<QT>::SMEM);
 }
+template <int QT, int DT>
+cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
+                   const CUtensorMap& d, const GroupedParams& p, int units, int split,
+                   cudaStream_t st) {
+  if (split == 1)
+    return launch_pdl(i8_tiles_kernel<QT, DT, false>, dim3(units), dim3(I8_THREADS),
+                      Cfg<QT>::SMEM, st, w, x, x32, d, p, 1);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * split));
+  cfg.blockDim = dim3(I8_THREADS);
+  cfg.dynamicSmemBytes = Cfg<QT>::SMEM;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, i8_tiles_kernel<QT, DT, true>, w, x, x32, d, p, split);
+}
+
 template <int DT>
-int prepare_typed(int rows, int num_sms) {
-  return rows == 128 ? prepare<128, STAGES128, DT>(num_sms) : prepare<64, STAGES64, DT>(num_sms);
+cudaError_t prepare_typed(int rows, bool split) {
+  return rows == 128 ? set_smem<128, DT>(split) : set_smem<64, DT>(split);
 }
 template <int DT>
 cudaError_t launch_typed(int rows, const CUtensorMap& w, const CUtensorMap& x,
                          const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
-                         int units, cudaStream_t st) {
-  return rows == 128 ? launch_pdl(i8_tiles_kernel<128, STAGES128, DT>, dim3(units), dim3(I8_THREADS),
-                                  Cfg<128, STAGES128>::SMEM, st, w, x, x32, d, p)
-                     : launch_pdl(i8_tiles_kernel<64, STAGES64, DT>, dim3(units), dim3(I8_THREADS),
-                                  Cfg<64, STAGES64>::SMEM, st, w, x, x32, d, p);
+                         int units, int split, cudaStream_t st) {
+  return rows == 128 ? launch<128, DT>(w, x, x32, d, p, units, split, st)
+                     : launch<64, DT>(w, x, x32, d, p, units, split, st);
 }
 
 }  // namespace
 
-int prepare_i8_tiles(int rows, int d_type, int num_sms) {
-  return d_type == T_F32    ? prepare_typed<T_F32>(rows, num_sms)
-         : d_type == T_BF16 ? prepare_typed<T_BF16>(rows, num_sms)
-                            : prepare_typed<T_F16>(rows, num_sms);
+cudaError_t prepare_i8_tiles(int rows, int d_type, bool split) {
+  return d_type == T_F32    ? prepare_typed<T_F32>(rows, split)
+         : d_type == T_BF16 ? prepare_typed<T_BF16>(rows, split)
+                            : prepare_typed<T_F16>(rows, split);
 }
 
 size_t i8_tiles_partial_bytes(int rows, int units) {
@@ -670,10 +846,10 @@ size_t i8_tiles_partial_bytes(int rows, int units) {
 
 cudaError_t launch_i8_tiles(int rows, const CUtensorMap& w, const CUtensorMap& x,
                             const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
-                            int units, cudaStream_t st) {
-  return p.d_type == T_F32    ? launch_typed<T_F32>(rows, w, x, x32, d, p, units, st)
-         : p.d_type == T_BF16 ? launch_typed<T_BF16>(rows, w, x, x32, d, p, units, st)
-                              : launch_typed<T_F16>(rows, w, x, x32, d, p, units, st);
+                            int units, int split, cudaStream_t st) {
+  return p.d_type == T_F32    ? launch_typed<T_F32>(rows, w, x, x32, d, p, units, split, st)
+         : p.d_type == T_BF16 ? launch_typed<T_BF16>(rows, w, x, x32, d, p, units, split, st)
+                              : launch_typed<T_F16>(rows, w, x, x32, d, p, units, split, st);
 }
 
 cudaError_t launch_i8_copy(const int8_t* src, long long ld_src, int8_t* dst, long long ld_dst,

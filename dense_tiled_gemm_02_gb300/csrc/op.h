@@ -65,7 +65,7 @@ struct gemm_op {
   size_t counters_bytes = 0;
   bool wide = false;
   bool tiles = false;  // i8: on the tensor cores (wide, or tiles of tile_rows rows)
-  int tile_rows = 0;
+  int tile_rows = 0, split = 1;
   int units = 0;
   int grid = 0;  // route: blocks
   gemm_op* inner = nullptr;  // rows8_grad: the grouped product it ends in

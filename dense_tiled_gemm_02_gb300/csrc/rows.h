@@ -42,6 +42,7 @@ struct NormBackwardParams {
   void* dx;
   float* dweight;     // may be null
   float* partial;     // norm_partial_rows() x H
+  uint32_t* status;
 };
 // Blocks of the backward kernel, each of which leaves a row of partial sums of dweight.
 int norm_partial_rows(long long T, int num_sms);
@@ -79,14 +80,16 @@ cudaError_t launch_i8_rows(const I8RowsParams& p, cudaStream_t st);
 
 // ---------------------------------------------------------------- products of many rows (i8_tiles.cu)
 // Tiles of up to `rows` (64 or 128) rows of X.
-int prepare_i8_tiles(int rows, int d_type, int num_sms);  // as prepare_grouped
+cudaError_t prepare_i8_tiles(int rows, int d_type, bool split);
 size_t i8_tiles_partial_bytes(int rows, int units);
 // Tensor maps: the weights' bytes in boxes of 128 x 128; X in fp16 in boxes of
 // 64 values x `rows` rows and x 32; D as for launch_grouped.  p: the rows form
-// with scales, offsets null for one expert with all rows.
+// with scales, offsets null for one expert with all rows.  split 1: `units` CTAs
+// share out the tiles (and p.partial, p.counters are needed); split 2, 4 or 8:
+// `units` clusters of as many CTAs, which must be at least as many as the tiles.
 cudaError_t launch_i8_tiles(int rows, const CUtensorMap& w, const CUtensorMap& x,
                             const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
-                            int units, cudaStream_t st);
+                            int units, int split, cudaStream_t st);
 // rows x cols bytes to 16-byte aligned rows of ld_dst, as they are or widened to fp16.
 cudaError_t launch_i8_copy(const int8_t* src, long long ld_src, int8_t* dst, long long ld_dst,
                            long long rows, int cols, int num_sms, cudaStream_t st);

@@ -128,6 +128,7 @@ int gemm_norm_backward(gemm_op_t op, const void* dy, const void* h, const uint8_
   p.dx = dx;
   p.dweight = dweight;
   p.partial = static_cast<float*>(op->ws);
+  p.status = op->status;
   return launched(launch_norm_backward(p, op->num_sms, st));
 }
 
@@ -294,17 +295,29 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
   const size_t x_bytes = tiles ? static_cast<size_t>(up(2 * d.R * ws_ldx, 256)) : 0;
   const size_t w_bytes = copy_w ? static_cast<size_t>(d.E * d.N * ws_ldw * (wide ? 2 : 1)) : 0;
   const size_t p_off = static_cast<size_t>(up(static_cast<int64_t>(x_bytes + w_bytes), 256));
-  const size_t partial = wide    ? grouped_partial_bytes(true, most_units)
-                         : tiles ? i8_tiles_partial_bytes(rows, most_units)
-                                 : 0;
-  const size_t counters = tiles ? 4 * static_cast<size_t>(most_units) * (wide ? 2 : 1) : 0;
+  // Fewer tiles than CTAs: clusters of CTAs share one each.  (The groups' tiles
+  // are not known: at most one more for each expert with rows.)
+  const int64_t experts = std::min<int64_t>(d.E, d.R);
+  const int64_t row_tiles =
+      rows ? (d.E == 1 ? (d.R + rows - 1) / rows : d.R / rows + experts) : 0;
+  const int64_t most_tiles = row_tiles * ((d.N + 127) / 128);
+  int split = 1;
+  if (tiles && !wide)
+    while (split < 8 && 2 * split * most_tiles <= sms && 2 * split <= (d.K + 127) / 128) split *= 2;
+  if (!planned("csk", split > 1)) split = 1;
+  const size_t partial = wide                  ? grouped_partial_bytes(true, most_units)
+                         : tiles && split == 1 ? i8_tiles_partial_bytes(rows, most_units)
+                                               : 0;
+  const size_t counters = tiles && split == 1 ? 4 * static_cast<size_t>(most_units) * (wide ? 2 : 1) : 0;
   gemm_op* op = nullptr;
   const int rc = make_op(Kind::kI8, p_off + partial + counters, p_off + partial, counters, &op);
   if (rc != GEMM_OK) return rc;
   op->i8 = d;
   if (tiles) {
-    op->units = std::min(most_units, wide ? prepare_scaled(d.d_type, op->num_sms)
-                                          : prepare_i8_tiles(rows, d.d_type, op->num_sms));
+    if (wide)
+      op->units = std::min(most_units, prepare_scaled(d.d_type, op->num_sms));
+    else if (prepare_i8_tiles(rows, d.d_type, split > 1) == cudaSuccess)
+      op->units = split > 1 ? static_cast<int>(most_tiles) : most_units;
     if (op->units <= 0) {
       cudaGetLastError();
       gemm_op_destroy(op);
@@ -314,6 +327,7 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
   op->tiles = tiles;
   op->wide = wide;
   op->tile_rows = rows;
+  op->split = split;
   op->copy_b = copy_w;
   op->ws_lda = ws_ldx;
   op->ws_ldb = copy_w ? ws_ldw : d.ldw;
@@ -321,10 +335,10 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
   op->ws_partial_off = p_off;
   op->ws_counters_off = p_off + partial;
   op->counters_bytes = counters;
-  std::snprintf(op->plan, sizeof op->plan, "i8 E=%d R=%lld K=%lld N=%lld form=%s rows=%d copy=%d units=%d",
+  std::snprintf(op->plan, sizeof op->plan, "i8 E=%d R=%lld K=%lld N=%lld form=%s rows=%d split=%d copy=%d units=%d",
                 d.E, static_cast<long long>(d.R), static_cast<long long>(d.K),
-                static_cast<long long>(d.N), wide ? "wide" : tiles ? "tiles" : "rows", rows, copy_w,
-                op->units);
+                static_cast<long long>(d.N), wide ? "wide" : tiles ? "tiles" : "rows", rows, split,
+                copy_w, op->units);
   *out = op;
   return GEMM_OK;
 }
@@ -380,7 +394,7 @@ int run_i8_tiles(gemm_op_t op, const int8_t* X, const float* x_scales, const int
   p.x_scales = x_scales;
   p.w_scales = w_scales;
   return launched(wide ? launch_scaled(wm, x, x32, dm, p, op->units, st)
-                       : launch_i8_tiles(op->tile_rows, wm, x, x32, dm, p, op->units, st));
+                       : launch_i8_tiles(op->tile_rows, wm, x, x32, dm, p, op->units, op->split, st));
 }
 
 }  // namespace

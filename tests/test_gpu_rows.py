@@ -489,8 +489,10 @@ SIZES = [(64, 16), (64, 64), (128, 256), (1000, 264), (33, 61), (1, 1), (15, 7),
          (4096, 512), (272, 1040)]
 
 
-# the few-rows kernel, the tensor-core tiles of 64 and of 128 rows, and of CTA pairs
-PLANS = ["tiles=0,wide=0", "tiles=1,wide=0,tall=0", "tiles=1,wide=0,tall=1", "wide=1"]
+# the few-rows kernel; tensor-core tiles of 64 and of 128 rows, shared by clusters where they are few,
+# and by the schedule; CTA pairs over widened operands
+PLANS = ["tiles=0,wide=0", "tiles=1,wide=0,tall=0", "tiles=1,wide=0,tall=1",
+         "tiles=1,wide=0,tall=0,csk=0", "tiles=1,wide=0,tall=1,csk=0", "wide=1"]
 
 
 @pytest.mark.parametrize("plan", PLANS)
