@@ -62,7 +62,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 // RT 16-row weight tiles a warp takes against NT tiles of 8 rows; U steps in
 // flight.  ALIGNED: rows of X and W are 16-byte multiples apart and start so.
 template <int RT, int NT, bool ALIGNED>
-__global__ void __launch_bounds__(32 * SM_WARPS) i8_rows_kernel(const I8RowsParams p) {
+__global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel(const I8RowsParams p) {
   constexpr int U = RT == 1 ? 4 : 2;
   __shared__ int red[SM_WARPS][16 * RT][8 * NT + 1];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(32 * SM_WARPS) i8_rows_kernel(const I8RowsPara
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (r < r1 && k < p.K) {
             if constexpr (ALIGNED) {
-              v = __ldg(reinterpret_cast<const uint4*>(src + u * STEP));
+              v = ld_global_v4_pinned(src + u * STEP);
             } else {
               const int n = min(16, p.K - k);  // what follows in W meets zeros here
               v = load16_at(src + u * STEP, n);

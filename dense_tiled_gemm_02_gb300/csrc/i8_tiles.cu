@@ -790,20 +790,7 @@ cudaError_t copy_rows(const int8_t* src, long long ld_src, void* dst, long long 
 
 // ---------------------------------------------------------------- launches
 template <int QT, int DT>
-cudaError_t set_smem(bool split) {
-  return split ? cudaFuncSetAttribute(i8_tiles_kernel<QT, DT, true>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<QT>::SMEM)
-               : cudaFuncSetAttribute(i8_tiles_kernel<QT, DT, false>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<QT>::SMEM);
-}
-template <int QT, int DT>
-cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
-                   const CUtensorMap& d, const GroupedParams& p, int units, int split,
-                   cudaStream_t st) {
-  if (split == 1)
-    return launch_pdl(i8_tiles_kernel<QT, DT, false>, dim3(units), dim3(I8_THREADS),
-                      Cfg<QT>::SMEM, st, w, x, x32, d, p, 1);
-  cudaLaunchAttribute attr[2];
+cudaLaunchConfig_t config(int units, int split, cudaStream_t st, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * split));
   cfg.blockDim = dim3(I8_THREADS);
@@ -816,13 +803,35 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, i8_tiles_kernel<QT, DT, true>, w, x, x32, d, p, split);
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cfg;
+}
+
+template <int QT, int DT>
+int prepare(int split, int num_sms) {
+  auto* const kernel = split > 1 ? i8_tiles_kernel<QT, DT, true> : i8_tiles_kernel<QT, DT, false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<QT>::SMEM) !=
+      cudaSuccess)
+    return 0;
+  if (split == 1) return num_sms;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = config<QT, DT>(1, split, nullptr, attr);
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+template <int QT, int DT>
+cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
+                   const CUtensorMap& d, const GroupedParams& p, int units, int split,
+                   cudaStream_t st) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = config<QT, DT>(units, split, st, attr);
+  return split > 1 ? cudaLaunchKernelEx(&cfg, i8_tiles_kernel<QT, DT, true>, w, x, x32, d, p, split)
+                   : cudaLaunchKernelEx(&cfg, i8_tiles_kernel<QT, DT, false>, w, x, x32, d, p, split);
 }
 
 template <int DT>
-cudaError_t prepare_typed(int rows, bool split) {
-  return rows == 128 ? set_smem<128, DT>(split) : set_smem<64, DT>(split);
+int prepare_typed(int rows, int split, int num_sms) {
+  return rows == 128 ? prepare<128, DT>(split, num_sms) : prepare<64, DT>(split, num_sms);
 }
 template <int DT>
 cudaError_t launch_typed(int rows, const CUtensorMap& w, const CUtensorMap& x,
@@ -834,10 +843,10 @@ cudaError_t launch_typed(int rows, const CUtensorMap& w, const CUtensorMap& x,
 
 }  // namespace
 
-cudaError_t prepare_i8_tiles(int rows, int d_type, bool split) {
-  return d_type == T_F32    ? prepare_typed<T_F32>(rows, split)
-         : d_type == T_BF16 ? prepare_typed<T_BF16>(rows, split)
-                            : prepare_typed<T_F16>(rows, split);
+int prepare_i8_tiles(int rows, int d_type, int split, int num_sms) {
+  return d_type == T_F32    ? prepare_typed<T_F32>(rows, split, num_sms)
+         : d_type == T_BF16 ? prepare_typed<T_BF16>(rows, split, num_sms)
+                            : prepare_typed<T_F16>(rows, split, num_sms);
 }
 
 size_t i8_tiles_partial_bytes(int rows, int units) {

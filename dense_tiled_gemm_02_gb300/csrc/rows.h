@@ -79,8 +79,10 @@ struct I8RowsParams {
 cudaError_t launch_i8_rows(const I8RowsParams& p, cudaStream_t st);
 
 // ---------------------------------------------------------------- products of many rows (i8_tiles.cu)
-// Tiles of up to `rows` (64 or 128) rows of X.
-cudaError_t prepare_i8_tiles(int rows, int d_type, bool split);
+// Tiles of up to `rows` (64 or 128) rows of X.  Sets the kernel up on the
+// current device; how many of its CTAs (split 1) or clusters of `split` CTAs run
+// at once, 0 on failure.
+int prepare_i8_tiles(int rows, int d_type, int split, int num_sms);
 size_t i8_tiles_partial_bytes(int rows, int units);
 // Tensor maps: the weights' bytes in boxes of 128 x 128; X in fp16 in boxes of
 // 64 values x `rows` rows and x 32; D as for launch_grouped.  p: the rows form

@@ -281,12 +281,21 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
   if (cudaGetDevice(&dev) == cudaSuccess)
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaGetLastError();
-  // Which kernel: by the rows of an expert on average (the host does not know
-  // the groups).
+  // Which kernel, by the rows of an expert on average (the host does not know
+  // the groups).  The few-rows kernel takes eight rows a pass for the weights'
+  // bytes, and nine to sixteen at the rate of the integer instruction: 2 us and
+  // 0.33 us a million weights and pass, against 6.5 and 0.19 of the tiles (16
+  // rows of 4096 x 4096 8.4 and 10.9 us, of 8192 x 8192 23.7 and 19.0; 32 of
+  // 1024 x 4096 5.3 and 7.6, of 4096 x 4096 14.4 and 10.9).  Tiles of 128 rows
+  // against the wide form: 4096 rows of 8192 x 8192 359 and 361 us, 8192 rows
+  // 716 and 623.
   const bool some = d.K > 0 && d.R > 0 && d.N > 0;
-  const bool wide = some && planned("wide", d.R >= 512 * d.E);
-  const bool tiles = wide || (some && planned("tiles", d.R > 16 * d.E));
-  const int rows = wide ? 0 : planned("tall", d.R > 64 * d.E) ? 128 : 64;
+  const int64_t mean = (d.R + d.E - 1) / d.E, passes = (mean + 15) / 16;
+  const double weights = static_cast<double>(d.E) * d.N * d.K;
+  const bool few = mean <= 8 || (0.33 * passes - 0.19) * weights < 4.5e6;
+  const bool wide = some && planned("wide", d.R >= 6144ll * d.E);
+  const bool tiles = wide || (some && planned("tiles", !few));
+  const int rows = wide ? 0 : planned("tall", mean > 64) ? 128 : 64;
   // X in fp16; W in fp16 (wide), or a copy where the TMA unit cannot read its
   // rows; partial sums and counters of shared tiles
   const bool copy_w = wide || (tiles && d.ldw % 16 != 0);
@@ -295,16 +304,19 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
   const size_t x_bytes = tiles ? static_cast<size_t>(up(2 * d.R * ws_ldx, 256)) : 0;
   const size_t w_bytes = copy_w ? static_cast<size_t>(d.E * d.N * ws_ldw * (wide ? 2 : 1)) : 0;
   const size_t p_off = static_cast<size_t>(up(static_cast<int64_t>(x_bytes + w_bytes), 256));
-  // Fewer tiles than CTAs: clusters of CTAs share one each.  (The groups' tiles
-  // are not known: at most one more for each expert with rows.)
+  // Fewer tiles than CTAs: clusters of CTAs share one each, all tiles in one
+  // wave.  (The groups' tiles are not known: at most one more for each expert
+  // with rows.)
   const int64_t experts = std::min<int64_t>(d.E, d.R);
-  const int64_t row_tiles =
-      rows ? (d.E == 1 ? (d.R + rows - 1) / rows : d.R / rows + experts) : 0;
+  const int64_t row_tiles = rows ? (d.E == 1 ? (d.R + rows - 1) / rows : d.R / rows + experts) : 0;
   const int64_t most_tiles = row_tiles * ((d.N + 127) / 128);
   int split = 1;
-  if (tiles && !wide)
+  if (tiles && !wide && planned("csk", true)) {
     while (split < 8 && 2 * split * most_tiles <= sms && 2 * split <= (d.K + 127) / 128) split *= 2;
-  if (!planned("csk", split > 1)) split = 1;
+    // a cluster's CTAs are neighbours: fewer of them fit than CTAs alone
+    while (split > 1 && prepare_i8_tiles(rows, d.d_type, split, sms) < most_tiles) split /= 2;
+    cudaGetLastError();
+  }
   const size_t partial = wide                  ? grouped_partial_bytes(true, most_units)
                          : tiles && split == 1 ? i8_tiles_partial_bytes(rows, most_units)
                                                : 0;
@@ -316,7 +328,7 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
   if (tiles) {
     if (wide)
       op->units = std::min(most_units, prepare_scaled(d.d_type, op->num_sms));
-    else if (prepare_i8_tiles(rows, d.d_type, split > 1) == cudaSuccess)
+    else if (prepare_i8_tiles(rows, d.d_type, split, op->num_sms) > 0)
       op->units = split > 1 ? static_cast<int>(most_tiles) : most_units;
     if (op->units <= 0) {
       cudaGetLastError();
