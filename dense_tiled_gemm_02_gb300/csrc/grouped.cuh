@@ -151,9 +151,10 @@ struct alignas(16) Piece {
   int more;          // 0: the end of the work
 };
 
-// The work of unit c of `units`, in slices of SLICE values of K.  prefix[e]: rows form, row tiles of the
+// The work of unit c of `units`, in slices of SLICE values of K; a tile is split
+// where that gains GAIN slices of 64.  prefix[e]: rows form, row tiles of the
 // experts before e; grad, K slices of one tile of each of them.
-template <int CG, int QT, int SLICE = BK>
+template <int CG, int QT, int SLICE = BK, int GAIN = SPLIT_GAIN>
 struct Schedule {
   const GroupedParams& p;
   const int* lo;      // [E + 1] offsets
@@ -182,7 +183,7 @@ struct Schedule {
     const int64_t gain = (waves + 1) * tile_kb - all / units;
     const bool split =
         tiles % units != 0 &&
-        gain >= (CG == 2 && waves == 0 ? 3 * SPLIT_GAIN : SPLIT_GAIN) * BK / SLICE;
+        gain >= (CG == 2 && waves == 0 ? 3 * GAIN : GAIN) * BK / SLICE;
     whole = !split ? tiles : (waves > 1 ? waves - 1 : 0) * units;
     s0 = p.grad ? slices_before(whole) : static_cast<int64_t>(whole) * kb;
     len = all - s0;

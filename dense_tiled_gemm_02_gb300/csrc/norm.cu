@@ -66,10 +66,10 @@ __device__ __forceinline__ void store_y(const NormParams& p, long long row, cons
   float w[VEC];
   load_weight<T, VEC>(p.weight, p.weight_type == T_F32, i, w);
   if constexpr (I8) {
-    Vec<int8_t, VEC> y;
+    float v[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) y.v[j] = row_integer(widen(h.v[j]) * w[j], q);
-    store_vec(static_cast<int8_t*>(p.y) + row * p.ldy + i, y);
+    for (int j = 0; j < VEC; ++j) v[j] = widen(h.v[j]) * w[j];
+    store_row_integers(static_cast<int8_t*>(p.y) + row * p.ldy + i, v, q);
   } else {
     Vec<T, VEC> y;
 #pragma unroll
@@ -182,14 +182,6 @@ struct HRow {
     }
   }
 };
-
-// 2^23 + 128 + the integer j of a vector: its byte, sign flipped, as the last of
-// that fp32 number (a conversion instruction has a quarter of the rate).
-template <int VEC>
-__device__ __forceinline__ float from_byte(const Vec<int8_t, VEC>& v, int j) {
-  const uint32_t w = reinterpret_cast<const uint32_t*>(&v)[j >> 2] ^ 0x80808080u;
-  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (j & 3)));
-}
 
 template <typename T, int VEC>
 __device__ __forceinline__ void store_dx(const NormBackwardParams& p, long long row, int i,
@@ -391,7 +383,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         if constexpr (HELD)
-          h[j] = fmaf(from_byte(v, j), scale[k], scale[k] * -8388736.f);
+          h[j] = fmaf(from_byte(v, j), scale[k], scale[k] * -BYTE_BIAS);
         else
           h[j] = widen(v.v[j]);
       }
@@ -484,8 +476,8 @@ cudaError_t launch_forward(const NormParams& p, int num_sms, cudaStream_t st) {
   const int n = (p.H + VEC - 1) / VEC;
   // Vectors a thread: four keep enough in flight where there are rows for all
   // SMs; few rows are spread over more threads.
-  const int most = p.T >= 4ll * num_sms ? 4 : p.T >= num_sms ? 2 : 1;
   constexpr int MOST = VEC == 1 ? 8 : 4;  // by the registers of 1024 threads
+  const int most = p.T >= 4ll * num_sms ? MOST : p.T >= num_sms ? MOST / 2 : 1;
   int nv = 1;
   while (nv < most && n > 32 * nv) nv *= 2;
   while (nv < MOST && n > 1024 * nv) nv *= 2;

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cstring>
 #include <type_traits>
 
 #include "moe.h"
@@ -73,6 +74,74 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int warps,
   }
 }
 
+// The largest magnitude of a vector, as the bits of an fp32 number.  Those of
+// 16-bit types are compared two at a time before they are widened.
+template <typename T, int VEC>
+__device__ __forceinline__ uint32_t vec_top(const Vec<T, VEC>& x) {
+  if constexpr (sizeof(T) == 2 && VEC >= 2) {
+    const uint32_t* const w = reinterpret_cast<const uint32_t*>(&x);
+    uint32_t top = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int j = 1; j < VEC / 2; ++j)
+      asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(w[j] & 0x7FFF7FFFu));
+    const unsigned short one = static_cast<unsigned short>(max(top & 0xFFFFu, top >> 16));
+    T t;
+    memcpy(&t, &one, 2);
+    return __float_as_uint(widen(t));
+  } else {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) top = max(top, magnitude(widen(x.v[j])));
+    return top;
+  }
+}
+
+// ---------------------------------------------------------------- integers
+// v * inverse to the nearest integer, ties to even: the last bits of its sum with
+// 1.5 * 2^23, whose unit in the last place is 1 (a conversion instruction has a
+// quarter of the rate).  The last byte is the integer's.
+__device__ __forceinline__ uint32_t nearest(float v, float inverse) {
+  return __float_as_uint(fmaf(v, inverse, 12582912.f));
+}
+
+// The last bytes of n, or zeros.
+template <int VEC>
+__device__ __forceinline__ void store_bytes(int8_t* p, const uint32_t (&n)[VEC], bool zero) {
+  if constexpr (VEC == 1) {
+    *p = zero ? int8_t(0) : static_cast<int8_t>(n[0]);
+  } else {
+    Vec<uint32_t, VEC / 4> w;
+#pragma unroll
+    for (int j = 0; j < VEC / 4; ++j) {
+      const uint32_t v = __byte_perm(__byte_perm(n[4 * j], n[4 * j + 1], 0x0040),
+                                     __byte_perm(n[4 * j + 2], n[4 * j + 3], 0x0040), 0x5410);
+      w.v[j] = zero ? 0u : v;
+    }
+    store_vec(reinterpret_cast<uint32_t*>(p), w);
+  }
+}
+
+// 2^23 + 128 + the integer j of a vector: its byte, sign flipped, as the last of
+// that fp32 number.
+template <int VEC>
+__device__ __forceinline__ float from_byte(const Vec<int8_t, VEC>& v, int j) {
+  const uint32_t w = reinterpret_cast<const uint32_t*>(&v)[j >> 2] ^ 0x80808080u;
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (j & 3)));
+}
+constexpr float BYTE_BIAS = 8388736.f;
+
+// The integers of a vector.
+template <int VEC>
+__device__ __forceinline__ void integers(const Vec<int8_t, VEC>& q, float (&o)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    if constexpr (VEC % 4 == 0)
+      o[j] = from_byte(q, j) - BYTE_BIAS;
+    else
+      o[j] = static_cast<float>(q.v[j]);
+  }
+}
+
 // ---------------------------------------------------------------- scaled rows
 // From the largest magnitude of a row: v * pre * inv are its integers, and
 // scale * integer its values times `unit`.  Where 127 / top would overflow, v
@@ -87,9 +156,13 @@ __device__ __forceinline__ RowScale row_scale(float top, float unit) {
   r.inv = top > 0.f && magnitude(r.scale) < 0x7F800000u ? 127.f / (top * r.pre) : 0.f;
   return r;
 }
-// (inv 0: also what is infinite or NaN in v gives 0)
-__device__ __forceinline__ int8_t row_integer(float v, const RowScale& r) {
-  return static_cast<int8_t>(r.inv > 0.f ? __float2int_rn(v * r.pre * r.inv) : 0);
+// The integers of VEC values (see nearest); 0 for a scale that is not finite.
+template <int VEC>
+__device__ __forceinline__ void store_row_integers(int8_t* p, const float (&v)[VEC], const RowScale& r) {
+  uint32_t n[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) n[j] = nearest(v[j] * r.pre, r.inv);
+  store_bytes(p, n, !(r.inv > 0.f));
 }
 
 // ---------------------------------------------------------------- block rows
@@ -114,8 +187,12 @@ __device__ __forceinline__ float block_step(uint32_t e) {
 __device__ __forceinline__ float block_inverse(uint32_t e) {
   return e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
 }
-__device__ __forceinline__ int8_t block_integer(float v, float inverse) {
-  return static_cast<int8_t>(inverse > 0.f ? __float2int_rn(v * inverse) : 0);
+template <int VEC>
+__device__ __forceinline__ void store_block_integers(int8_t* p, const float (&v)[VEC], float inverse) {
+  uint32_t n[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) n[j] = nearest(v[j], inverse);
+  store_bytes(p, n, !(inverse > 0.f));
 }
 
 }  // namespace gb300

@@ -1,9 +1,16 @@
 // rows8.cu -- rows to 8 bits and back: blocks of 32 values with a power of two,
 // and whole rows with one fp32 scale.
 //
-// Bound by HBM: 16 values a thread and turn (two or four 16-byte loads, one
-// 16-byte store, or the reverse), so that two threads share a block's exponent
-// and one shuffle finds its largest magnitude.
+// Bound by HBM: 16 values a thread and turn (16-byte accesses on both sides:
+// with 8 of a 16-bit type, 8-byte ones on the 8-bit side, unpacking takes 44
+// instead of 33 us), several turns in flight; two lanes share a block's exponent
+// and find its largest magnitude by a shuffle.  Integers are made and read by
+// additions in the last place and byte permutes, since conversion instructions,
+// at a quarter of the rate, bounded the first form (40 us; 64-bit divisions for
+// an item's row another 5).
+//
+// Measured (one GB300, 16384 x 4096 bf16, floor 30.1 us each way): block rows 30
+// us and back 33, scaled rows 29 and back 34.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -16,69 +23,135 @@ namespace gb300 {
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
+
+// n / d for n < 2^31, by a multiplication (a 64-bit division would take longer
+// than the rest of an item).
+struct Divisor {
+  uint32_t d, m, s;
+};
+Divisor divisor(int d) {
+  uint32_t s = 0;
+  while ((1ull << s) < static_cast<uint64_t>(d)) ++s;
+  return {static_cast<uint32_t>(d),
+          static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1), s};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& d) {
+  return (__umulhi(n, d.m) + n) >> d.s;
+}
+
+// A block's items (VEC values each, `lanes` of them a row): `rows` whole rows,
+// or one of the `parts` of a row.
+struct Deal {
+  int rows;
+  uint32_t chunk;  // items of a part
+  Divisor parts, lanes;
+};
+struct Items {
+  long long row;
+  uint32_t at, n;  // the first item within that row; items of the block
+};
+__device__ __forceinline__ Items block_items(long long T, const Deal& d) {
+  if (d.parts.d == 1) {
+    const long long row = static_cast<long long>(blockIdx.x) * d.rows;
+    return {row, 0u, static_cast<uint32_t>(min(static_cast<long long>(d.rows), T - row)) * d.lanes.d};
+  }
+  const uint32_t row = divide(blockIdx.x, d.parts), at = (blockIdx.x - row * d.parts.d) * d.chunk;
+  return {row, at, min(d.chunk, d.lanes.d - at)};
+}
 
 // ---------------------------------------------------------------- block rows
-// VEC 16: two lanes a block.  VEC 1 (rows that do not allow vectors): a warp.
+// LANES lanes to 32 values; VEC 1 (rows that do not allow vectors): a warp.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(THREADS) pack_blocks_kernel(const Rows8Params p) {
+__global__ void __launch_bounds__(THREADS)
+    pack_blocks_kernel(const Rows8Params p, const Deal deal) {
   const int blocks = (p.H + ROW_BLOCK - 1) / ROW_BLOCK;
-  constexpr int LANES = ROW_BLOCK / VEC;
-  const long long all = p.T * blocks * LANES;
+  constexpr int LANES = ROW_BLOCK / VEC, U = 4;
+  const Items all = block_items(p.T, deal);
+  const Divisor& lanes = deal.lanes;
   pdl_wait();
   pdl_trigger();
-  // (whole warps stay together: `all` counts lanes of whole blocks, and the
-  // last warp's lanes past it load nothing but shuffle)
-  for (long long at = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
-       at - (threadIdx.x & 31) < all; at += static_cast<long long>(gridDim.x) * THREADS) {
-    const long long item = at / LANES, row = item / blocks;
-    const int b = static_cast<int>(item - row * blocks);
-    const int i = b * ROW_BLOCK + static_cast<int>(at % LANES) * VEC;
-    const bool ok = at < all && i < p.H;
-    Vec<T, VEC> x{};
-    if (ok) x = load_vec<T, VEC>(static_cast<const T*>(p.X) + row * p.ldx + i);
-    uint32_t top = 0u;
+  // (whole warps stay together: lanes past the last item load nothing but shuffle)
+  for (uint32_t at0 = threadIdx.x; at0 - (threadIdx.x & 31) < all.n; at0 += U * THREADS) {
+    Vec<T, VEC> x[U];
+    long long row[U];
+    int i[U];
+    bool ok[U];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) top = max(top, magnitude(widen(x.v[j])));
+    for (int u = 0; u < U; ++u) {
+      const uint32_t at = all.at + at0 + u * THREADS, r = divide(at, lanes);
+      row[u] = all.row + r;
+      i[u] = static_cast<int>(at - r * lanes.d) * VEC;
+      ok[u] = at0 + u * THREADS < all.n && i[u] < p.H;
+      x[u] = Vec<T, VEC>{};
+      if (ok[u]) x[u] = load_vec<T, VEC>(static_cast<const T*>(p.X) + row[u] * p.ldx + i[u]);
+    }
 #pragma unroll
-    for (int d = LANES / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const uint32_t e = block_exponent(top, least_exponent<T>());
-    const float inverse = block_inverse(e);
-    if (ok) {
-      Vec<int8_t, VEC> q;
+    for (int u = 0; u < U; ++u) {
+      uint32_t top = vec_top(x[u]);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) q.v[j] = block_integer(widen(x.v[j]), inverse);
-      store_vec(p.q_out + row * p.ldq + i, q);
-      if (at % LANES == 0) static_cast<uint8_t*>(p.scales_out)[row * blocks + b] = e;
+      for (int d = LANES / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      const uint32_t e = block_exponent(top, least_exponent<T>());
+      const float inverse = block_inverse(e);
+      if (ok[u]) {
+        float v[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = widen(x[u].v[j]);
+        store_block_integers(p.q_out + row[u] * p.ldq + i[u], v, inverse);
+        if (i[u] % ROW_BLOCK == 0)
+          static_cast<uint8_t*>(p.scales_out)[row[u] * blocks + i[u] / ROW_BLOCK] = e;
+      }
     }
   }
 }
 
 template <typename T, int VEC, bool BLOCKS>
-__global__ void __launch_bounds__(THREADS) unpack_kernel(const Rows8Params p) {
-  const int blocks = (p.H + ROW_BLOCK - 1) / ROW_BLOCK, n = p.H / VEC;
-  const long long all = p.T * n;
+__global__ void __launch_bounds__(THREADS)
+    unpack_kernel(const Rows8Params p, const Deal deal) {
+  const int blocks = (p.H + ROW_BLOCK - 1) / ROW_BLOCK;
+  const Items all = block_items(p.T, deal);
+  const Divisor& lanes = deal.lanes;
   pdl_wait();
   pdl_trigger();
-  for (long long at = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x; at < all;
-       at += static_cast<long long>(gridDim.x) * THREADS) {
-    const long long row = at / n;
-    const int i = static_cast<int>(at - row * n) * VEC;
-    const auto q = load_vec<int8_t, VEC>(p.q + row * p.ldq + i);
-    const float step =
-        BLOCKS ? block_step(static_cast<const uint8_t*>(p.scales)[row * blocks + i / ROW_BLOCK])
-               : static_cast<const float*>(p.scales)[row];
-    Vec<T, VEC> x;
+  constexpr int U = 2;
+  for (uint32_t at0 = threadIdx.x; at0 < all.n; at0 += U * THREADS) {
+    Vec<int8_t, VEC> q[U];
+    float step[U];
+    T* to[U];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) narrow_finite(static_cast<float>(q.v[j]) * step, x.v[j]);
-    store_vec(static_cast<T*>(p.X_out) + row * p.ldx + i, x);
+    for (int u = 0; u < U; ++u) {
+      const uint32_t at = all.at + at0 + u * THREADS, r = divide(at, lanes);
+      const long long row = all.row + r;
+      const int i = static_cast<int>(at - r * lanes.d) * VEC;
+      to[u] = static_cast<T*>(p.X_out) + row * p.ldx + i;
+      if (at0 + u * THREADS < all.n) {
+        q[u] = load_vec<int8_t, VEC>(p.q + row * p.ldq + i);
+        step[u] = BLOCKS ? block_step(static_cast<const uint8_t*>(p.scales)[row * blocks + i / ROW_BLOCK])
+                         : static_cast<const float*>(p.scales)[row];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at0 + u * THREADS < all.n) {
+        float v[VEC];
+        integers(q[u], v);
+        Vec<T, VEC> x;
+        if (step[u] < largest<T>() / 256.f) {  // nothing can round past the finite values
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) narrow(v[j] * step[u], x.v[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) narrow_finite(v[j] * step[u], x.v[j]);
+        }
+        store_vec(to[u], x);
+      }
   }
 }
 
 // ---------------------------------------------------------------- scaled rows
-// A block (or, blockDim.x = 32, a warp) a row, which is read a second time for
-// its integers, from L1 or L2.
-template <typename T, int VEC>
+// A block (or, blockDim.x = 32, a warp) a row, whose threads hold NV vectors
+// each, or with NV = 0 (rows too long) read them again.
+template <typename T, int VEC, int NV>
 __global__ void __launch_bounds__(1024) pack_rows_kernel(const Rows8Params p) {
   __shared__ float2 part[32];
   const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -87,59 +160,98 @@ __global__ void __launch_bounds__(1024) pack_rows_kernel(const Rows8Params p) {
   pdl_trigger();
   if (row >= p.T) return;
   const T* const X = static_cast<const T*>(p.X) + row * p.ldx;
+  constexpr int N = NV > 0 ? NV : 1;
+  Vec<T, VEC> x[N];
   uint32_t top = 0u;
   float sum = 0.f;
-#pragma unroll 2
-  for (int i = first; i < p.H; i += step) {
-    const auto x = load_vec<T, VEC>(X + i);
+  auto largest_of = [&](const Vec<T, VEC>& v) { top = max(top, vec_top(v)); };
+  if constexpr (NV > 0) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) top = max(top, magnitude(widen(x.v[j])));
+    for (int k = 0; k < NV; ++k)
+      if (first + k * step < p.H) x[k] = load_vec<T, VEC>(X + first + k * step);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (first + k * step < p.H) largest_of(x[k]);
+  } else {
+    for (int i = first; i < p.H; i += step) largest_of(load_vec<T, VEC>(X + i));
   }
   row_reduce(sum, top, blockDim.x >> 5, part);
   const RowScale s = row_scale(__uint_as_float(top), 1.f);
   if (threadIdx.x == 0) static_cast<float*>(p.scales_out)[row] = s.scale;
-#pragma unroll 2
-  for (int i = first; i < p.H; i += step) {
-    const auto x = load_vec<T, VEC>(X + i);
-    Vec<int8_t, VEC> q;
+  auto store = [&](const Vec<T, VEC>& v, int i) {
+    float f[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) q.v[j] = row_integer(widen(x.v[j]), s);
-    store_vec(p.q_out + row * p.ldq + i, q);
+    for (int j = 0; j < VEC; ++j) f[j] = widen(v.v[j]);
+    store_row_integers(p.q_out + row * p.ldq + i, f, s);
+  };
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (first + k * step < p.H) store(x[k], first + k * step);
+  } else {
+    for (int i = first; i < p.H; i += step) store(load_vec<T, VEC>(X + i), i);
   }
 }
 
 // ---------------------------------------------------------------- launches
-// Blocks of a grid-stride kernel over n threads' items.
-dim3 stride_grid(long long n, int num_sms) {
-  return dim3(static_cast<unsigned>(std::min<long long>((n + THREADS - 1) / THREADS, 16ll * num_sms)));
+// Four items a thread, fewer where that leaves SMs without work.  (A part is a
+// multiple of 32 values' lanes.)
+Deal deal_of(long long T, int lanes, int num_sms, dim3& grid) {
+  uint32_t n = 4 * THREADS;
+  while (n > THREADS && T * lanes < 2ll * num_sms * n) n /= 2;
+  const uint32_t parts = (lanes + n - 1) / n;
+  const int rows = parts > 1 ? 1 : static_cast<int>(n / lanes);
+  grid = dim3(static_cast<unsigned>(parts > 1 ? T * parts : (T + rows - 1) / rows));
+  return {rows, n, divisor(static_cast<int>(parts)), divisor(lanes)};
 }
 
 template <typename T, int VEC>
 cudaError_t pack_as(const Rows8Params& p, int num_sms, cudaStream_t st) {
   if (p.block) {
-    const long long n = p.T * ((p.H + ROW_BLOCK - 1) / ROW_BLOCK) * (ROW_BLOCK / VEC);
-    return launch_pdl(pack_blocks_kernel<T, VEC>, stride_grid(n, num_sms), dim3(THREADS), 0, st, p);
+    const int lanes = (p.H + ROW_BLOCK - 1) / ROW_BLOCK * (ROW_BLOCK / VEC);
+    dim3 grid;
+    const Deal deal = deal_of(p.T, lanes, num_sms, grid);
+    return launch_pdl(pack_blocks_kernel<T, VEC>, grid, dim3(THREADS), 0, st, p, deal);
   }
+  // few rows are spread over more threads
+  constexpr int MOST = VEC == 1 ? 8 : VEC == 16 ? 2 : 4;
   const int n = (p.H + VEC - 1) / VEC;
-  const int threads = std::min(1024, (n + 31) / 32 * 32), rows = threads == 32 ? 4 : 1;
-  return launch_pdl(pack_rows_kernel<T, VEC>, dim3(static_cast<unsigned>((p.T + rows - 1) / rows)),
-                    dim3(threads, rows), 0, st, p);
+  int nv = p.T >= num_sms ? MOST : 1;
+  while (nv > 1 && n <= 16 * nv) nv /= 2;
+  if (nv == 1 && n > 1024) nv = MOST;
+  const bool again = n > 1024 * nv;
+  const int threads = again ? 1024 : (((n + nv - 1) / nv) + 31) / 32 * 32, rows = threads == 32 ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>((p.T + rows - 1) / rows)), block(threads, rows);
+  if (again) return launch_pdl(pack_rows_kernel<T, VEC, 0>, grid, block, 0, st, p);
+  if (nv == 1) return launch_pdl(pack_rows_kernel<T, VEC, 1>, grid, block, 0, st, p);
+  if constexpr (MOST == 8)
+    if (nv == 8) return launch_pdl(pack_rows_kernel<T, VEC, 8>, grid, block, 0, st, p);
+  if constexpr (MOST >= 4)
+    if (nv == 4) return launch_pdl(pack_rows_kernel<T, VEC, 4>, grid, block, 0, st, p);
+  return launch_pdl(pack_rows_kernel<T, VEC, 2>, grid, block, 0, st, p);
 }
 template <typename T, int VEC>
 cudaError_t unpack_as(const Rows8Params& p, int num_sms, cudaStream_t st) {
-  const dim3 grid = stride_grid(p.T * (p.H / VEC), num_sms);
-  return p.block ? launch_pdl(unpack_kernel<T, VEC, true>, grid, dim3(THREADS), 0, st, p)
-                 : launch_pdl(unpack_kernel<T, VEC, false>, grid, dim3(THREADS), 0, st, p);
+  const int lanes = p.H / VEC;
+  dim3 grid;
+  const Deal deal = deal_of(p.T, lanes, num_sms, grid);
+  return p.block ? launch_pdl(unpack_kernel<T, VEC, true>, grid, dim3(THREADS), 0, st, p, deal)
+                 : launch_pdl(unpack_kernel<T, VEC, false>, grid, dim3(THREADS), 0, st, p, deal);
 }
 
 template <typename T>
 cudaError_t typed(const Rows8Params& p, bool pack, int num_sms, cudaStream_t st) {
   const void* const X = pack ? p.X : p.X_out;
   const void* const q = pack ? p.q_out : p.q;
-  const bool vec = p.H % 16 == 0 && p.ldq % 16 == 0 && p.ldx * sizeof(T) % 16 == 0 &&
-                   reinterpret_cast<uintptr_t>(X) % 16 == 0 && reinterpret_cast<uintptr_t>(q) % 16 == 0;
-  if (pack) return vec ? pack_as<T, 16>(p, num_sms, st) : pack_as<T, 1>(p, num_sms, st);
-  return vec ? unpack_as<T, 16>(p, num_sms, st) : unpack_as<T, 1>(p, num_sms, st);
+  // values a thread, by what the rows' lengths and places allow
+  auto fits = [&](int vec, int bytes) {  // bytes: of an access to X
+    return p.H % vec == 0 && p.ldq % vec == 0 && p.ldx * sizeof(T) % bytes == 0 &&
+           reinterpret_cast<uintptr_t>(X) % bytes == 0 && reinterpret_cast<uintptr_t>(q) % vec == 0;
+  };
+  constexpr int HALF = 16 / sizeof(T);
+  if (fits(16, 16)) return pack ? pack_as<T, 16>(p, num_sms, st) : unpack_as<T, 16>(p, num_sms, st);
+  if (fits(HALF, 16)) return pack ? pack_as<T, HALF>(p, num_sms, st) : unpack_as<T, HALF>(p, num_sms, st);
+  return pack ? pack_as<T, 1>(p, num_sms, st) : unpack_as<T, 1>(p, num_sms, st);
 }
 
 cudaError_t launch(const Rows8Params& p, bool pack, int num_sms, cudaStream_t st) {
