@@ -71,3 +71,52 @@ def test_check_reports_every_product(name):
     layer.forward(X, Y)
     layer.backward(X, Y, dX)
     layer.check()
+
+
+def norm_of(H=64, dtype=torch.float32, device="cpu"):
+    return torch.ones(H, dtype=dtype, device=device)
+
+
+@pytest.mark.parametrize("cls", [el.ExpertLayer, el.ExpertDecoder])
+@pytest.mark.parametrize("norm,match", [
+    (norm_of(63), "norm must be 64 weights"),
+    (norm_of(dtype=torch.float16), "norm must be 64 weights"),   # neither the weights' nor fp32
+    (norm_of(device="meta"), "norm is on meta"),
+])
+def test_norm_agrees_with_the_weights(cls, norm, match):
+    with pytest.raises(ValueError, match=match):
+        cls(8, k=2, norm=norm, **weights())
+
+
+def test_decoder_bits():
+    with pytest.raises(ValueError, match="4 or 8 bits, not 6"):
+        el.ExpertDecoder(8, k=2, bits=6, **weights())
+
+
+@pytest.mark.gpu
+def test_the_stream_goes_with_a_norm():
+    w = {name: t.cuda() for name, t in weights().items()}
+    X = torch.zeros(8, 64, dtype=BF16, device="cuda")
+    plain = el.ExpertLayer(8, k=2, **w)
+    with pytest.raises(ValueError, match="go with a norm"):
+        plain.forward(X, X, residual=X, h=X)
+    with pytest.raises(ValueError, match="go with a norm"):
+        plain.backward(X, X, X, dh=X)
+    normed = el.ExpertLayer(8, k=2, norm=norm_of(device="cuda"), **w)
+    for kw in ({}, {"residual": X}, {"h": X}):
+        with pytest.raises(ValueError, match="go with a norm"):
+            normed.forward(X, X, **kw)
+    with pytest.raises(ValueError, match="residual: planned"):
+        normed.forward(X, X, residual=X[:7], h=X)
+    with pytest.raises(ValueError, match="h: planned"):
+        normed.forward(X, X, residual=X, h=X.float())
+    with pytest.raises(ValueError, match="go with a norm"):
+        normed.backward(X, X, X, h=X)
+    kept = el.ExpertLayer(8, k=2, norm=norm_of(device="cuda"), keep8=True, **w)
+    with pytest.raises(ValueError, match="h is kept"):
+        kept.backward(X, X, X, h=X, dh=X)
+    decoder = el.ExpertDecoder(8, k=2, bits=8, norm=norm_of(device="cuda"), **w)
+    with pytest.raises(ValueError, match="residual goes with a norm"):
+        decoder.step(X)
+    with pytest.raises(ValueError, match="residual: planned"):
+        decoder.step(X, X[:1])
