@@ -59,6 +59,44 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
+// Pass y of all experts' passes of `rows` rows, in their order: its expert, first
+// and end row; empty past the last (every thread of the block calls it).
+__device__ __forceinline__ int3 nth_pass(const int* offsets, int E, int R, uint32_t* status, int y,
+                                         int rows) {
+  __shared__ int sums[32];
+  __shared__ int found[3];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (threadIdx.x == 0) found[1] = found[2] = 0;
+  int before = 0;
+  for (int e0 = 0; e0 < E && before <= y; e0 += blockDim.x) {
+    const int e = e0 + threadIdx.x;
+    int2 r = make_int2(0, 0);
+    if (e < E) r = expert_rows(offsets, e, R, status);
+    const int n = (r.y - r.x + rows - 1) / rows;
+    int inc = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += u;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    int at = before + inc - n, all = before;
+    for (int i = 0; i < warps; ++i) {
+      if (i < warp) at += sums[i];
+      all += sums[i];
+    }
+    if (y >= at && y < at + n) {
+      found[0] = e;
+      found[1] = r.x + (y - at) * rows;
+      found[2] = min(r.y, found[1] + rows);
+    }
+    before = all;
+    __syncthreads();
+  }
+  return make_int3(found[0], found[1], found[2]);
+}
+
 // RT 16-row weight tiles a warp takes against NT tiles of 8 rows; U steps in
 // flight.  ALIGNED: rows of X and W are 16-byte multiples apart and start so.
 template <int RT, int NT, bool ALIGNED>
@@ -67,27 +105,28 @@ __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel
   __shared__ int red[SM_WARPS][16 * RT][8 * NT + 1];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  const int tiles = (p.N + 16 * RT - 1) / (16 * RT);  // passes one after another, tiles fastest
+  const int pass = blockIdx.x / tiles, n0 = (blockIdx.x - pass * tiles) * 16 * RT;
   if (!p.offsets && p.K <= warps * U * STEP) {
     // The weights on their way to L2 while the kernel before this one ends
     // (nothing is read before that), where a warp has a single run of them:
     // two lines of a row.  (1 x 4096 x 4096: 5.5 -> 4.9 us; with more runs it
     // is in the way, 1 x 8192 x 8192: 14.9 -> 16.8.)
-    const int n = blockIdx.x * 16 * RT + g, k = warp * U * STEP + 128 * t;
+    const int n = n0 + g, k = warp * U * STEP + 128 * t;
 #pragma unroll
     for (int i = 0; i < 2 * RT; ++i)
       if (128 * t < U * STEP && k < p.K && n + 8 * i < p.N) prefetch_l2(p.W + (n + 8 * i) * p.ldw + k);
   }
   pdl_wait();
   pdl_trigger();
-  int e = 0, r0 = 0, r1 = p.R;
+  int e = 0, rb = pass * 8 * NT, r1 = min(p.R, rb + 8 * NT);
   if (p.offsets) {
-    e = p.E > 1 ? nth_expert(p.offsets, p.E, p.R, p.status, blockIdx.y) : 0;
-    if (e < 0) return;
-    const int2 r = expert_rows(p.offsets, e, p.R, p.status);
-    r0 = r.x;
-    r1 = r.y;
+    const int3 rows = nth_pass(p.offsets, p.E, p.R, p.status, pass, 8 * NT);
+    e = rows.x;
+    rb = rows.y;
+    r1 = rows.z;
+    if (rb >= r1) return;
   }
-  const int n0 = blockIdx.x * 16 * RT;
   // this thread's first weight row, and how far on the others are; rows past
   // N read the first again and are not stored
   const int left = p.N - n0 - g;
@@ -95,7 +134,7 @@ __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel
       p.W + (static_cast<long long>(e) * p.N + n0 + (left > 0 ? g : 0)) * p.ldw + 16 * t;
   auto rows_on = [&](int i, int h) { return 16 * i + 8 * h < left ? 16 * i + 8 * h : 0; };
   const int steps = (p.K + STEP - 1) / STEP;
-  for (int rb = r0; rb < r1; rb += 8 * NT) {
+  {
     int acc[RT][NT][4] = {};
     // the scales of the first output this thread will store, on their way
     // beside the sums (not multiplied here: that would wait for them)
@@ -155,7 +194,6 @@ __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel
                    x[j][u].w);
           }
     }
-    __syncthreads();  // the previous rows' sums have been read
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -181,13 +219,16 @@ __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel
 
 template <int RT, int NT, bool ALIGNED>
 cudaError_t launch_as(const I8RowsParams& p, cudaStream_t st) {
-  const int tiles = (p.N + 16 * RT - 1) / (16 * RT), experts = p.E > 1 ? std::min(p.E, p.R) : 1;
+  const int tiles = (p.N + 16 * RT - 1) / (16 * RT);
+  // passes: at most one that is not full for each expert with rows
+  const int experts = p.offsets ? std::min(p.E, p.R) : 1;
+  const int passes = p.offsets ? experts + p.R / (8 * NT) : (p.R + 8 * NT - 1) / (8 * NT);
   const int steps = (p.K + STEP - 1) / STEP;
   int warps = 4;
   while (warps < SM_WARPS && 2 * warps <= steps / 2 &&
          static_cast<long long>(tiles) * experts * warps < SM_WARPS * p.num_sms)
     warps *= 2;
-  return launch_pdl(i8_rows_kernel<RT, NT, ALIGNED>, dim3(tiles, experts), dim3(32 * warps), 0, st, p);
+  return launch_pdl(i8_rows_kernel<RT, NT, ALIGNED>, dim3(static_cast<unsigned>(static_cast<long long>(tiles) * passes)), dim3(32 * warps), 0, st, p);
 }
 
 template <bool ALIGNED>

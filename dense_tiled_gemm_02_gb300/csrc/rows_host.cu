@@ -292,7 +292,7 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
   const bool some = d.K > 0 && d.R > 0 && d.N > 0;
   const int64_t mean = (d.R + d.E - 1) / d.E, passes = (mean + 15) / 16;
   const double weights = static_cast<double>(d.E) * d.N * d.K;
-  const bool few = mean <= 8 || (0.33 * passes - 0.19) * weights < 4.5e6;
+  const bool few = mean <= 8 || (passes <= 2 && (0.33 * passes - 0.19) * weights < 4.5e6);
   const bool wide = some && planned("wide", d.R >= 6144ll * d.E);
   const bool tiles = wide || (some && planned("tiles", !few));
   const int rows = wide ? 0 : planned("tall", mean > 64) ? 128 : 64;

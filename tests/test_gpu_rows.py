@@ -638,3 +638,22 @@ def test_a_layer_from_norm_to_gradient():
     near(dg, dg_ref, (T + 4) * U * dg_size)
     for op in (norm, product, train, keep, grad):
         done(op)
+
+
+@pytest.mark.parametrize("plan", PLANS)
+def test_i8_experts_with_most_of_the_rows(plan):
+    """Few rows an expert on average, but one has nearly all of them."""
+    i8_check([0] * 20 + [150] + [0] * 30 + [1] + [0] * 12, 256, 136, BF16, plan=plan)
+
+
+def test_i8_many_rows_without_k():
+    """More rows than a grid's second dimension has blocks of eight."""
+    R = 8 * 70000
+    D = torch.full((R, 8), 7.0, dtype=BF16, device="cuda")
+    X = torch.empty((R, 0), dtype=torch.int8, device="cuda")
+    W = torch.empty((1, 8, 0), dtype=torch.int8, device="cuda")
+    xs, ws = torch.ones(R, device="cuda"), torch.ones((1, 8), device="cuda")
+    op = pkg.I8Gemm.like(X, xs, W, ws, None, D)
+    op.run(X, xs, W, ws, None, D)
+    done(op)
+    assert not D.any()
