@@ -29,7 +29,7 @@
 
 #include "grouped.cuh"
 #include "i8.cuh"
-#include "rows.h"
+#include "rows.cuh"
 
 namespace gb300 {
 
@@ -745,48 +745,79 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
 }
 
 // ---------------------------------------------------------------- copies of rows
-// 16 values a thread and turn; ALIGNED as in i8_rows.cu.  A last unit that K
-// ends in is padded with whatever follows: the tensor maps end at K.
-template <bool ALIGNED, bool WIDEN>
-__global__ void __launch_bounds__(256)
-    i8_copy_kernel(const int8_t* src, long long ld_src, uint8_t* dst, long long ld_dst,
-                   long long rows, int cols) {
-  const int n = (cols + 15) / 16;
+// 16 values an item.  A last unit that K ends in is padded with whatever
+// follows: the tensor maps end at K.  Up to two jobs a launch (one after the
+// other they take 3 us more of 4096 x 4096 x 4096).
+struct CopyJob {
+  const int8_t* src;
+  uint8_t* dst;
+  long long ld_src, ld_dst, rows;
+  int cols, aligned;  // rows of src are 16-byte multiples apart and start so
+  unsigned blocks;
+  Deal deal;
+};
+
+template <bool WIDEN>
+__global__ void __launch_bounds__(DEAL_THREADS) i8_copy_kernel(const CopyJob first, const CopyJob second) {
+  constexpr int U = 4;
+  const bool two = blockIdx.x >= first.blocks;
+  const CopyJob& job = two ? second : first;
+  const Items all = block_items(job.rows, job.deal, blockIdx.x - (two ? first.blocks : 0u));
   pdl_wait();
   pdl_trigger();
-  for (long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; at < rows * n;
-       at += static_cast<long long>(gridDim.x) * 256) {
-    const long long row = at / n;
-    const int k = static_cast<int>(at - row * n) * 16;
-    const int8_t* const from = src + row * ld_src + k;
-    const uint4 w = ALIGNED ? *reinterpret_cast<const uint4*>(from)
-                            : load16_at(from, min(16, cols - k));
-    if constexpr (WIDEN) {
-      uint4* const to = reinterpret_cast<uint4*>(dst + 2 * (row * ld_dst + k));
-      uint4 a, b;
-      widen4(w.x, a.x, a.y);
-      widen4(w.y, a.z, a.w);
-      widen4(w.z, b.x, b.y);
-      widen4(w.w, b.z, b.w);
-      to[0] = a;
-      to[1] = b;
-    } else {
-      *reinterpret_cast<uint4*>(dst + row * ld_dst + k) = w;
+  for (uint32_t at0 = threadIdx.x; at0 < all.n; at0 += U * DEAL_THREADS) {
+    uint4 w[U];
+    uint8_t* to[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t at = all.at + at0 + u * DEAL_THREADS, r = divide(at, job.deal.lanes);
+      const long long row = all.row + r;
+      const int k = static_cast<int>(at - r * job.deal.lanes.d) * 16;
+      const int8_t* const from = job.src + row * job.ld_src + k;
+      to[u] = job.dst + (WIDEN ? 2 : 1) * (row * job.ld_dst + k);
+      if (at0 + u * DEAL_THREADS < all.n)
+        w[u] = job.aligned ? *reinterpret_cast<const uint4*>(from) : load16_at(from, min(16, job.cols - k));
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at0 + u * DEAL_THREADS < all.n) {
+        uint4* const d = reinterpret_cast<uint4*>(to[u]);
+        if constexpr (WIDEN) {
+          uint4 a, b;
+          widen4(w[u].x, a.x, a.y);
+          widen4(w[u].y, a.z, a.w);
+          widen4(w[u].z, b.x, b.y);
+          widen4(w[u].w, b.z, b.w);
+          d[0] = a;
+          d[1] = b;
+        } else {
+          d[0] = w[u];
+        }
+      }
   }
 }
 
+CopyJob job_of(const I8Copy& c, int num_sms) {
+  CopyJob j = {};
+  if (c.rows == 0 || c.cols == 0) return j;
+  j.src = c.src;
+  j.dst = static_cast<uint8_t*>(c.dst);
+  j.ld_src = c.ld_src;
+  j.ld_dst = c.ld_dst;
+  j.rows = c.rows;
+  j.cols = c.cols;
+  j.aligned = c.cols % 16 == 0 && c.ld_src % 16 == 0 && reinterpret_cast<uintptr_t>(c.src) % 16 == 0;
+  dim3 grid;
+  j.deal = deal_of(c.rows, (c.cols + 15) / 16, num_sms, grid);
+  j.blocks = grid.x;
+  return j;
+}
+
 template <bool WIDEN>
-cudaError_t copy_rows(const int8_t* src, long long ld_src, void* dst, long long ld_dst,
-                      long long rows, int cols, int num_sms, cudaStream_t st) {
-  const bool aligned = cols % 16 == 0 && ld_src % 16 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0;
-  const long long items = rows * ((cols + 15) / 16);
-  const dim3 grid(static_cast<unsigned>(std::min<long long>((items + 255) / 256, 16ll * num_sms)));
-  uint8_t* const d = static_cast<uint8_t*>(dst);
-  return aligned ? launch_pdl(i8_copy_kernel<true, WIDEN>, grid, dim3(256), 0, st, src, ld_src, d,
-                              ld_dst, rows, cols)
-                 : launch_pdl(i8_copy_kernel<false, WIDEN>, grid, dim3(256), 0, st, src, ld_src, d,
-                              ld_dst, rows, cols);
+cudaError_t copy_rows(const I8Copy& first, const I8Copy& second, int num_sms, cudaStream_t st) {
+  const CopyJob a = job_of(first, num_sms), b = job_of(second, num_sms);
+  if (a.blocks + b.blocks == 0) return cudaSuccess;
+  return launch_pdl(i8_copy_kernel<WIDEN>, dim3(a.blocks + b.blocks), dim3(DEAL_THREADS), 0, st, a, b);
 }
 
 // ---------------------------------------------------------------- launches
@@ -862,13 +893,11 @@ cudaError_t launch_i8_tiles(int rows, const CUtensorMap& w, const CUtensorMap& x
                               : launch_typed<T_F16>(rows, w, x, x32, d, p, units, split, st);
 }
 
-cudaError_t launch_i8_copy(const int8_t* src, long long ld_src, int8_t* dst, long long ld_dst,
-                           long long rows, int cols, int num_sms, cudaStream_t st) {
-  return copy_rows<false>(src, ld_src, dst, ld_dst, rows, cols, num_sms, st);
+cudaError_t launch_i8_copy(const I8Copy& c, int num_sms, cudaStream_t st) {
+  return copy_rows<false>(c, I8Copy{}, num_sms, st);
 }
-cudaError_t launch_i8_widen(const int8_t* src, long long ld_src, uint16_t* dst, long long ld_dst,
-                            long long rows, int cols, int num_sms, cudaStream_t st) {
-  return copy_rows<true>(src, ld_src, dst, ld_dst, rows, cols, num_sms, st);
+cudaError_t launch_i8_widen(const I8Copy& first, const I8Copy& second, int num_sms, cudaStream_t st) {
+  return copy_rows<true>(first, second, num_sms, st);
 }
 
 }  // namespace gb300

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstring>
 #include <type_traits>
 
@@ -193,6 +194,55 @@ __device__ __forceinline__ void store_block_integers(int8_t* p, const float (&v)
 #pragma unroll
   for (int j = 0; j < VEC; ++j) n[j] = nearest(v[j], inverse);
   store_bytes(p, n, !(inverse > 0.f));
+}
+
+// ---------------------------------------------------------------- items of rows
+constexpr int DEAL_THREADS = 128;  // of a block whose threads take items in turn
+
+// n / d for n < 2^31, by a multiplication (a 64-bit division would take longer
+// than the rest of an item).
+struct Divisor {
+  uint32_t d, m, s;
+};
+inline Divisor divisor(int d) {
+  uint32_t s = 0;
+  while ((1ull << s) < static_cast<uint64_t>(d)) ++s;
+  return {static_cast<uint32_t>(d),
+          static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1), s};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& d) {
+  return (__umulhi(n, d.m) + n) >> d.s;
+}
+
+// A block's items (`lanes` of them a row): `rows` whole rows,
+// or one of the `parts` of a row.
+struct Deal {
+  int rows;
+  uint32_t chunk;  // items of a part
+  Divisor parts, lanes;
+};
+struct Items {
+  long long row;
+  uint32_t at, n;  // the first item within that row; items of the block
+};
+__device__ __forceinline__ Items block_items(long long T, const Deal& d, uint32_t block) {
+  if (d.parts.d == 1) {
+    const long long row = static_cast<long long>(block) * d.rows;
+    return {row, 0u, static_cast<uint32_t>(min(static_cast<long long>(d.rows), T - row)) * d.lanes.d};
+  }
+  const uint32_t row = divide(block, d.parts), at = (block - row * d.parts.d) * d.chunk;
+  return {row, at, min(d.chunk, d.lanes.d - at)};
+}
+
+// Four items a thread, fewer where that leaves SMs without work.  (A part is a
+// multiple of DEAL_THREADS.)
+inline Deal deal_of(long long T, int lanes, int num_sms, dim3& grid) {
+  uint32_t n = 4 * DEAL_THREADS;
+  while (n > DEAL_THREADS && T * lanes < 2ll * num_sms * n) n /= 2;
+  const uint32_t parts = (lanes + n - 1) / n;
+  const int rows = parts > 1 ? 1 : static_cast<int>(n / lanes);
+  grid = dim3(static_cast<unsigned>(parts > 1 ? T * parts : (T + rows - 1) / rows));
+  return {rows, n, divisor(static_cast<int>(parts)), divisor(lanes)};
 }
 
 }  // namespace gb300

@@ -92,10 +92,16 @@ size_t i8_tiles_partial_bytes(int rows, int units);
 cudaError_t launch_i8_tiles(int rows, const CUtensorMap& w, const CUtensorMap& x,
                             const CUtensorMap& x32, const CUtensorMap& d, const GroupedParams& p,
                             int units, int split, cudaStream_t st);
-// rows x cols bytes to 16-byte aligned rows of ld_dst, as they are or widened to fp16.
-cudaError_t launch_i8_copy(const int8_t* src, long long ld_src, int8_t* dst, long long ld_dst,
-                           long long rows, int cols, int num_sms, cudaStream_t st);
-cudaError_t launch_i8_widen(const int8_t* src, long long ld_src, uint16_t* dst, long long ld_dst,
-                            long long rows, int cols, int num_sms, cudaStream_t st);
+// rows x cols bytes to 16-byte aligned rows of ld_dst elements, as they are or
+// widened to fp16 (two operands in one launch; an empty one is left out).
+struct I8Copy {
+  const int8_t* src;
+  long long ld_src;
+  void* dst;
+  long long ld_dst, rows;
+  int cols;
+};
+cudaError_t launch_i8_copy(const I8Copy& c, int num_sms, cudaStream_t st);
+cudaError_t launch_i8_widen(const I8Copy& first, const I8Copy& second, int num_sms, cudaStream_t st);
 
 }  // namespace gb300

@@ -23,42 +23,7 @@ namespace gb300 {
 
 namespace {
 
-constexpr int THREADS = 128;
-
-// n / d for n < 2^31, by a multiplication (a 64-bit division would take longer
-// than the rest of an item).
-struct Divisor {
-  uint32_t d, m, s;
-};
-Divisor divisor(int d) {
-  uint32_t s = 0;
-  while ((1ull << s) < static_cast<uint64_t>(d)) ++s;
-  return {static_cast<uint32_t>(d),
-          static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1), s};
-}
-__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& d) {
-  return (__umulhi(n, d.m) + n) >> d.s;
-}
-
-// A block's items (VEC values each, `lanes` of them a row): `rows` whole rows,
-// or one of the `parts` of a row.
-struct Deal {
-  int rows;
-  uint32_t chunk;  // items of a part
-  Divisor parts, lanes;
-};
-struct Items {
-  long long row;
-  uint32_t at, n;  // the first item within that row; items of the block
-};
-__device__ __forceinline__ Items block_items(long long T, const Deal& d) {
-  if (d.parts.d == 1) {
-    const long long row = static_cast<long long>(blockIdx.x) * d.rows;
-    return {row, 0u, static_cast<uint32_t>(min(static_cast<long long>(d.rows), T - row)) * d.lanes.d};
-  }
-  const uint32_t row = divide(blockIdx.x, d.parts), at = (blockIdx.x - row * d.parts.d) * d.chunk;
-  return {row, at, min(d.chunk, d.lanes.d - at)};
-}
+constexpr int THREADS = DEAL_THREADS;
 
 // ---------------------------------------------------------------- block rows
 // LANES lanes to 32 values; VEC 1 (rows that do not allow vectors): a warp.
@@ -67,7 +32,7 @@ __global__ void __launch_bounds__(THREADS)
     pack_blocks_kernel(const Rows8Params p, const Deal deal) {
   const int blocks = (p.H + ROW_BLOCK - 1) / ROW_BLOCK;
   constexpr int LANES = ROW_BLOCK / VEC, U = 4;
-  const Items all = block_items(p.T, deal);
+  const Items all = block_items(p.T, deal, blockIdx.x);
   const Divisor& lanes = deal.lanes;
   pdl_wait();
   pdl_trigger();
@@ -109,7 +74,7 @@ template <typename T, int VEC, bool BLOCKS>
 __global__ void __launch_bounds__(THREADS)
     unpack_kernel(const Rows8Params p, const Deal deal) {
   const int blocks = (p.H + ROW_BLOCK - 1) / ROW_BLOCK;
-  const Items all = block_items(p.T, deal);
+  const Items all = block_items(p.T, deal, blockIdx.x);
   const Divisor& lanes = deal.lanes;
   pdl_wait();
   pdl_trigger();
@@ -194,17 +159,6 @@ __global__ void __launch_bounds__(1024) pack_rows_kernel(const Rows8Params p) {
 }
 
 // ---------------------------------------------------------------- launches
-// Four items a thread, fewer where that leaves SMs without work.  (A part is a
-// multiple of 32 values' lanes.)
-Deal deal_of(long long T, int lanes, int num_sms, dim3& grid) {
-  uint32_t n = 4 * THREADS;
-  while (n > THREADS && T * lanes < 2ll * num_sms * n) n /= 2;
-  const uint32_t parts = (lanes + n - 1) / n;
-  const int rows = parts > 1 ? 1 : static_cast<int>(n / lanes);
-  grid = dim3(static_cast<unsigned>(parts > 1 ? T * parts : (T + rows - 1) / rows));
-  return {rows, n, divisor(static_cast<int>(parts)), divisor(lanes)};
-}
-
 template <typename T, int VEC>
 cudaError_t pack_as(const Rows8Params& p, int num_sms, cudaStream_t st) {
   if (p.block) {

@@ -367,16 +367,11 @@ int run_i8_tiles(gemm_op_t op, const int8_t* X, const float* x_scales, const int
   const int64_t w_rows = d.E * d.N;
   uint8_t* const ws = static_cast<uint8_t*>(op->ws);
   uint16_t* const wx = reinterpret_cast<uint16_t*>(ws);
-  int rc = launched(launch_i8_widen(X, d.ldx, wx, op->ws_lda, d.R, K, op->num_sms, st));
-  const void* w = W;
-  if (rc == GEMM_OK && op->copy_b) {
-    void* const to = ws + op->ws_b_off;
-    rc = launched(wide ? launch_i8_widen(W, d.ldw, static_cast<uint16_t*>(to), op->ws_ldb, w_rows, K,
-                                         op->num_sms, st)
-                       : launch_i8_copy(W, d.ldw, static_cast<int8_t*>(to), op->ws_ldb, w_rows, K,
-                                        op->num_sms, st));
-    w = to;
-  }
+  const void* w = op->copy_b ? ws + op->ws_b_off : static_cast<const void*>(W);
+  const I8Copy copy_x = {X, d.ldx, wx, op->ws_lda, d.R, K};
+  const I8Copy copy_w = {W, d.ldw, ws + op->ws_b_off, op->ws_ldb, w_rows, K};
+  int rc = launched(launch_i8_widen(copy_x, wide ? copy_w : I8Copy{}, op->num_sms, st));
+  if (rc == GEMM_OK && op->copy_b && !wide) rc = launched(launch_i8_copy(copy_w, op->num_sms, st));
   if (rc != GEMM_OK) return rc;
   CUtensorMap wm{}, x{}, x32{}, dm{};
   if (!(wide ? encode_rows(&wm, w, op->ws_ldb, d.K, w_rows, 0, BK, 128)
