@@ -614,7 +614,7 @@ def test_a_layer_from_norm_to_gradient():
     product = pkg.I8Gemm.like(y8, s, W, ws, None, D)
     norm.run(x, g, y8, scales=s, residual=res, h=h)
     product.run(y8, s, W, ws, None, D)
-    ref = (y8.double() * s.double()[:, None]) @ (W[0].double() * ws[0].double()[:, None]).t()
+    ref = y8.double() @ W[0].double().t() * s.double()[:, None] * ws[0].double()
     near(D, ref, 4 * U * ref.abs())
     # training: what the norm gave is kept in 8 bits, and so is h
     y, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
