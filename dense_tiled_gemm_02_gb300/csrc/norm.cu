@@ -26,33 +26,49 @@ constexpr int RING_MOST = 4;        // stages of a block's ring
 constexpr int RING_BYTES = 212 * 1024;  // of all blocks of an SM
 constexpr uint64_t RING_TIMEOUT_NS = 2000000000ull;
 
-// VEC weights of the rows' type or of fp32, from column i.
-template <typename T, int VEC>
-__device__ __forceinline__ void load_weight(const void* w, bool f32, int i, float (&o)[VEC]) {
-  if (f32) {
-    const auto v = load_vec<float, VEC>(static_cast<const float*>(w) + i);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] = v.v[j];
-  } else {
-    const auto v = load_vec<T, VEC>(static_cast<const T*>(w) + i);
+// VEC weights of the rows' type or of fp32, from column i; with ANY of any
+// alignment, from columns before the row's as well, and zeros outside it.
+template <typename T, int VEC, bool ANY>
+__device__ __forceinline__ void load_weight(const void* w, bool f32, int i, int H, float (&o)[VEC]) {
+  auto load = [&](auto* p) {
+    using W = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    Vec<W, VEC> v;
+    if constexpr (ANY) {
+      Around<W, VEC> x;
+      const Range n = elements_at<VEC, true>(i, H);
+      fetch(x, p + i, n, inside<VEC>(i, 1, 0, H));
+      v = shifted<true>(x, n);
+    } else {
+      v = load_vec<W, VEC>(p + i);
+    }
 #pragma unroll
     for (int j = 0; j < VEC; ++j) o[j] = widen(v.v[j]);
-  }
+  };
+  if (f32)
+    load(static_cast<const float*>(w));
+  else
+    load(static_cast<const T*>(w));
 }
 
-// h = x + residual in T, and its sum of squares and largest |h w|.
-template <typename T, int VEC, bool I8>
+// A row's sum of squares and (I8) largest |h w|; if KEEP with what the store needs
+// of the weights: h w, or w.
+template <typename T, int VEC, bool I8, bool ANY, bool KEEP>
 __device__ __forceinline__ void row_sums(const NormParams& p, const Vec<T, VEC>& h, int i,
-                                         float& sum, uint32_t& top) {
+                                         float& sum, uint32_t& top, float (&kept)[VEC]) {
   float w[VEC];
-  if constexpr (I8) load_weight<T, VEC>(p.weight, p.weight_type == T_F32, i, w);
+  if constexpr (I8 || KEEP) load_weight<T, VEC, ANY>(p.weight, p.weight_type == T_F32, i, p.H, w);
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
     const float v = widen(h.v[j]);
     sum = fmaf(v, v, sum);
     if constexpr (I8) top = max(top, magnitude(v * w[j]));
+    if constexpr (KEEP) kept[j] = I8 ? v * w[j] : w[j];
   }
 }
+
+// What a thread's elements are loaded as.
+template <typename T, int VEC, bool ANY>
+using WordsOf = std::conditional_t<ANY, Around<T, VEC>, Vec<T, VEC>>;
 
 template <typename T, int VEC>
 __device__ __forceinline__ void add_residual(Vec<T, VEC>& h, const Vec<T, VEC>& r) {
@@ -60,28 +76,39 @@ __device__ __forceinline__ void add_residual(Vec<T, VEC>& h, const Vec<T, VEC>& 
   for (int j = 0; j < VEC; ++j) narrow(widen(h.v[j]) + widen(r.v[j]), h.v[j]);
 }
 
-template <typename T, int VEC, bool I8>
+template <typename T, int VEC, bool ANY>
+__device__ __forceinline__ void store_row(T* p, int i, int H, const Vec<T, VEC>& x) {
+  if constexpr (ANY)
+    store_shifted<true>(p, i, elements_at<VEC, true>(i, H), x);
+  else if (i < H)
+    store_vec(p, x);
+}
+
+template <typename T, int VEC, bool I8, bool ANY, bool KEEP>
 __device__ __forceinline__ void store_y(const NormParams& p, long long row, const Vec<T, VEC>& h,
-                                        int i, float r, const RowScale& q) {
+                                        int i, float r, const RowScale& q, const float (&kept)[VEC]) {
   float w[VEC];
-  load_weight<T, VEC>(p.weight, p.weight_type == T_F32, i, w);
+  if (!KEEP && i < p.H) load_weight<T, VEC, ANY>(p.weight, p.weight_type == T_F32, i, p.H, w);
   if constexpr (I8) {
     float v[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = widen(h.v[j]) * w[j];
-    store_row_integers(static_cast<int8_t*>(p.y) + row * p.ldy + i, v, q);
+    for (int j = 0; j < VEC; ++j) v[j] = KEEP ? kept[j] : widen(h.v[j]) * w[j];
+    store_row<int8_t, VEC, ANY>(static_cast<int8_t*>(p.y) + row * p.ldy + i, i, p.H, row_integers(v, q));
   } else {
     Vec<T, VEC> y;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) narrow(widen(h.v[j]) * r * w[j], y.v[j]);
-    store_vec(static_cast<T*>(p.y) + row * p.ldy + i, y);
+    for (int j = 0; j < VEC; ++j) narrow(widen(h.v[j]) * r * (KEEP ? kept[j] : w[j]), y.v[j]);
+    store_row<T, VEC, ANY>(static_cast<T*>(p.y) + row * p.ldy + i, i, p.H, y);
   }
 }
 
 // A row's blockDim.x threads hold NV vectors each, or with NV = 0 (rows too
 // long for that) read them again, from h where there is a residual.  blockDim.y
-// rows a block, more than one only with one warp a row.
-template <typename T, int VEC, int NV, bool I8>
+// rows a block, more than one only with one warp a row.  ANY: rows of any
+// alignment; a row's vectors then begin up to VEC - 1 elements before it, where
+// x's words do, so that only operands aligned otherwise (the weight, 8-bit y) are
+// shifted.
+template <typename T, int VEC, int NV, bool I8, bool ANY>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
   __shared__ float2 part[MAX_WARPS];
   const int warps = blockDim.x >> 5;
@@ -89,44 +116,86 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
   pdl_wait();
   pdl_trigger();
   if (row >= p.T) return;  // (a whole warp, which shares nothing)
-  const T* const x = static_cast<const T*>(p.x) + row * p.ldx;
-  const T* const res = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
+  const int lead = ANY ? static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(p.x) + row * p.ldx) %
+                                          (VEC * sizeof(T)) / sizeof(T))
+                       : 0;
+  const int step = blockDim.x * VEC, first = threadIdx.x * VEC - lead;
+  const int warp_first = (threadIdx.x & ~31) * VEC - lead;  // whole warps store
   T* const hout = static_cast<T*>(p.h) + row * p.ldh;
-  const int step = blockDim.x * VEC, first = threadIdx.x * VEC;
   constexpr int N = NV > 0 ? NV : 1;
+  using Words = WordsOf<T, VEC, ANY>;
+  auto load = [&](const void* from, long long ld, int i, Words& v) {
+    const Range n = elements_at<VEC, ANY>(i, p.H);
+    const T* const at = static_cast<const T*>(from) + row * ld + i;
+    if (n.to == 0) return;
+    if constexpr (ANY)
+      fetch(v, at, n, inside<VEC>(row * ld + i, p.T, ld, p.H));
+    else
+      v = load_vec<T, VEC>(at);
+  };
+  auto settle = [&](const Words& v, int i) {
+    if constexpr (ANY)
+      return shifted<true>(v, elements_at<VEC, true>(i, p.H));
+    else
+      return v;
+  };
+  // (shifted weights are fetched once, and before the barrier, where registers hold them)
+  constexpr bool KEEP = ANY && NV > 0 && NV <= 2;
   Vec<T, VEC> h[N];
+  float kept[N][VEC];
   float sum = 0.f;
   uint32_t top = 0u;
   if constexpr (NV > 0) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (first + k * step < p.H) h[k] = load_vec<T, VEC>(x + first + k * step);
-    if (res) {
-      Vec<T, VEC> r[NV];
+    auto chunk = [&](int k, const Words& x, const Words& r) {
+      const int i = first + k * step;
+      h[k] = settle(x, i);
+      if (p.residual) {
+        add_residual(h[k], settle(r, i));
+        store_row<T, VEC, ANY>(hout + i, i, p.H, h[k]);
+      }
+    };
+    if constexpr (ANY && NV > 2) {  // (a vector's words take two vectors' registers)
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        if (first + k * step < p.H) r[k] = load_vec<T, VEC>(res + first + k * step);
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (first + k * step < p.H) {
-          add_residual(h[k], r[k]);
-          store_vec(hout + first + k * step, h[k]);
+        if (warp_first + k * step < p.H) {
+          Words x, r;
+          load(p.x, p.ldx, first + k * step, x);
+          if (p.residual) load(p.residual, p.ldr, first + k * step, r);
+          chunk(k, x, r);
         }
+    } else {
+      Words x[NV];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) load(p.x, p.ldx, first + k * step, x[k]);
+      if (p.residual) {
+        Words r[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) load(p.residual, p.ldr, first + k * step, r[k]);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if ((ANY ? warp_first : first) + k * step < p.H) chunk(k, x[k], r[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) h[k] = settle(x[k], first + k * step);
+      }
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (first + k * step < p.H) row_sums<T, VEC, I8>(p, h[k], first + k * step, sum, top);
+      if (first + k * step < p.H) row_sums<T, VEC, I8, ANY, KEEP>(p, h[k], first + k * step, sum, top, kept[k]);
   } else {
-    for (int i = first; i < p.H; i += step) {
-      h[0] = load_vec<T, VEC>(x + i);
-      if (res) {
-        add_residual(h[0], load_vec<T, VEC>(res + i));
-        store_vec(hout + i, h[0]);
+    for (int i = first, i0 = warp_first; i0 < p.H; i += step, i0 += step) {
+      Words v;
+      load(p.x, p.ldx, i, v);
+      h[0] = settle(v, i);
+      if (p.residual) {
+        load(p.residual, p.ldr, i, v);
+        add_residual(h[0], settle(v, i));
+        store_row<T, VEC, ANY>(hout + i, i, p.H, h[0]);
       }
-      row_sums<T, VEC, I8>(p, h[0], i, sum, top);
+      if (i < p.H) row_sums<T, VEC, I8, ANY, KEEP>(p, h[0], i, sum, top, kept[0]);
     }
   }
-  row_reduce(sum, top, warps, part);
+  row_reduce<I8>(sum, top, warps, part);
   const float r = 1.f / sqrtf(sum / static_cast<float>(p.H) + p.eps);
   const RowScale q = I8 ? row_scale(__uint_as_float(top), r) : RowScale{};
   if (threadIdx.x == 0) {
@@ -136,179 +205,134 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
   if constexpr (NV > 0) {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (first + k * step < p.H) store_y<T, VEC, I8>(p, row, h[k], first + k * step, r, q);
+      if ((ANY ? warp_first : first) + k * step < p.H)
+        store_y<T, VEC, I8, ANY, KEEP>(p, row, h[k], first + k * step, r, q, kept[k]);
   } else {
-    const T* const from = res ? hout : x;  // this thread's own stores
-    for (int i = first; i < p.H; i += step)
-      store_y<T, VEC, I8>(p, row, load_vec<T, VEC>(from + i), i, r, q);
+    // h's or x's row again (with ANY a thread reads what its warp's lanes and, one
+    // word at either end, other warps stored before the barrier of the sum)
+    for (int i = first, i0 = warp_first; i0 < p.H; i += step, i0 += step) {
+      Words v;
+      load(p.residual ? p.h : p.x, p.residual ? p.ldh : p.ldx, i, v);
+      store_y<T, VEC, I8, ANY, KEEP>(p, row, settle(v, i), i, r, q, kept[0]);
+    }
   }
 }
 
 // ---------------------------------------------------------------- backward
-// VEC values of h from column i of a row: of type T, or block rows.
-template <typename T, int VEC, bool HELD>
-struct HRow {
-  const T* h;
-  const int8_t* q;
-  const uint8_t* e;
-  __device__ __forceinline__ HRow(const NormBackwardParams& p, long long row) {
-    if constexpr (HELD) {
-      q = static_cast<const int8_t*>(p.h) + row * p.ldh;
-      e = p.E + row * ((p.H + ROW_BLOCK - 1) / ROW_BLOCK);
-    } else {
-      h = static_cast<const T*>(p.h) + row * p.ldh;
-    }
-  }
-  struct Raw {
-    Vec<std::conditional_t<HELD, int8_t, T>, VEC> v;
-    uint8_t e;
-  };
-  __device__ __forceinline__ void load(int i, Raw& r) const {
-    if constexpr (HELD) {
-      r.v = load_vec<int8_t, VEC>(q + i);
-      r.e = e[i / ROW_BLOCK];
-    } else {
-      r.v = load_vec<T, VEC>(h + i);
-    }
-  }
-  static __device__ __forceinline__ void widen_to(const Raw& r, float (&o)[VEC]) {
-    if constexpr (HELD) {
-      const float step = block_step(r.e);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = static_cast<float>(r.v.v[j]) * step;
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = widen(r.v.v[j]);
-    }
-  }
-};
-
 template <typename T, int VEC>
-__device__ __forceinline__ void store_dx(const NormBackwardParams& p, long long row, int i,
-                                         const float (&dy)[VEC], const float (&h)[VEC],
-                                         const float (&w)[VEC], float r, float c,
-                                         const Vec<T, VEC>& res) {
+__device__ __forceinline__ Vec<T, VEC> dx_of(const float (&dy)[VEC], const float (&h)[VEC],
+                                             const float (&w)[VEC], float r, float c,
+                                             const Vec<T, VEC>& res, bool residual) {
   Vec<T, VEC> o;
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
     float v = r * (dy[j] * w[j] - h[j] * c);
-    if (p.dresidual) v += widen(res.v[j]);
+    if (residual) v += widen(res.v[j]);
     narrow(v, o.v[j]);
   }
-  store_vec(static_cast<T*>(p.dx) + row * p.ldx + i, o);
+  return o;
 }
 
-// Blocks take rows in turn; a thread's columns are the same in all of them, so
-// that it sums their dweight in registers (NV = 0: in the block's own row of
-// `partial`) and no two threads share a sum.
-template <typename T, int VEC, int NV, bool HELD>
+// Threads of an SM that the ring kernels' registers are for: by the sums of
+// dweight, and by what is shifted with ANY.
+constexpr int ring_room(bool any, int nv, int sums) {
+  return any ? (nv == 1 ? 640 : 512) : sums > 8 ? 512 : 1024;
+}
+
+// Bytes of a row's slot in the ring.
+template <bool ANY>
+__host__ __device__ constexpr uint32_t ring_slot(uint32_t bytes) {
+  return ANY ? (bytes + 15u) / 16u * 16u + 16u : bytes;
+}
+
+// VEC values of h: of type T, or of block rows with this exponent's step.
+template <typename T, int VEC>
+__device__ __forceinline__ void widen_h(const Vec<T, VEC>& v, float, float (&h)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) h[j] = widen(v.v[j]);
+}
+template <int VEC>
+__device__ __forceinline__ void widen_h(const Vec<int8_t, VEC>& v, float step, float (&h)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) h[j] = fmaf(from_byte(v, j), step, step * -BYTE_BIAS);
+}
+
+// Rows too long for the kernel below.  Blocks take rows in turn and read each
+// twice; a thread's columns are the same in all of them, so that no two threads
+// share a sum of dweight in the block's own row of `partial`.
+template <typename T, int VEC, bool HELD, bool ANY>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardParams p) {
+  using HT = std::conditional_t<HELD, int8_t, T>;
   __shared__ float2 part[2][MAX_WARPS];
-  constexpr int N = NV > 0 ? NV : 1;
   const int warps = blockDim.x >> 5;
   const int step = blockDim.x * VEC, first = threadIdx.x * VEC;
+  const int warp_first = (threadIdx.x & ~31) * VEC;  // whole warps store
+  const int blocks = (p.H + ROW_BLOCK - 1) / ROW_BLOCK;
   const bool w32 = p.weight_type == T_F32;
   float* const mine = p.partial + static_cast<long long>(blockIdx.x) * p.H;
-  float dw[N][VEC] = {};
   pdl_wait();
   pdl_trigger();
-  if constexpr (NV == 0) {
-    if (p.dweight)
-      for (int i = first; i < p.H; i += step)
-        for (int j = 0; j < VEC; ++j) mine[i + j] = 0.f;
-  }
+  if (p.dweight)
+    for (int i = first; i < p.H; i += step)
+      for (int j = 0; j < VEC; ++j)
+        if (i + j < p.H) mine[i + j] = 0.f;
   int turn = 0;
   for (long long row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
-    const HRow<T, VEC, HELD> hrow(p, row);
-    const T* const dyrow = static_cast<const T*>(p.dy) + row * p.ldy;
-    const T* const resrow = static_cast<const T*>(p.dresidual) + row * p.ldr;
     const float r = p.rstd[row];
+    auto load = [&](auto* base, long long ld, int i) {
+      using E = std::remove_const_t<std::remove_pointer_t<decltype(base)>>;
+      if constexpr (ANY) {
+        Around<E, VEC> v;
+        const Range n = elements_at<VEC>(i, p.H);
+        fetch(v, base + row * ld + i, n, inside<VEC>(row * ld + i, p.T, ld, p.H));
+        return shifted<true>(v, n);
+      } else {
+        return load_vec<E, VEC>(base + row * ld + i);
+      }
+    };
+    float dy[VEC], h[VEC], w[VEC];
+    auto load_row = [&](int i) {
+      const auto dyv = load(static_cast<const T*>(p.dy), p.ldy, i);
+      const auto hv = load(static_cast<const HT*>(p.h), p.ldh, i);
+      widen_h(hv, HELD ? block_step(p.E[row * blocks + i / ROW_BLOCK]) : 1.f, h);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) dy[j] = widen(dyv.v[j]);
+      load_weight<T, VEC, ANY>(p.weight, w32, i, p.H, w);
+    };
     float sum = 0.f;
     uint32_t top = 0u;
-    auto dot = [&](const float (&dy)[VEC], const float (&h)[VEC], int i) {
-      float w[VEC];
-      load_weight<T, VEC>(p.weight, w32, i, w);
+    for (int i = first; i < p.H; i += step) {
+      load_row(i);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) sum = fmaf(dy[j] * w[j], h[j], sum);
-    };
-    if constexpr (NV > 0) {
-      Vec<T, VEC> dyv[NV], res[NV];
-      typename HRow<T, VEC, HELD>::Raw hv[NV];
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (first + k * step < p.H) {
-          dyv[k] = load_vec<T, VEC>(dyrow + first + k * step);
-          hrow.load(first + k * step, hv[k]);
-          if (p.dresidual) res[k] = load_vec<T, VEC>(resrow + first + k * step);
-        }
-      float dy[VEC], h[VEC], w[VEC];
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (first + k * step < p.H) {
-          HRow<T, VEC, HELD>::widen_to(hv[k], h);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            dy[j] = widen(dyv[k].v[j]);
-            dw[k][j] = fmaf(dy[j], h[j] * r, dw[k][j]);
-          }
-          dot(dy, h, first + k * step);
-        }
-      row_reduce(sum, top, warps, part[turn]);
-      const float c = r * r * (sum / static_cast<float>(p.H));
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (first + k * step < p.H) {
-          HRow<T, VEC, HELD>::widen_to(hv[k], h);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) dy[j] = widen(dyv[k].v[j]);
-          load_weight<T, VEC>(p.weight, w32, first + k * step, w);
-          store_dx<T, VEC>(p, row, first + k * step, dy, h, w, r, c, res[k]);
-        }
-    } else {
-      float dy[VEC], h[VEC], w[VEC];
-      typename HRow<T, VEC, HELD>::Raw raw;
-      auto load = [&](int i) {
-        const Vec<T, VEC> v = load_vec<T, VEC>(dyrow + i);
-        hrow.load(i, raw);
-        HRow<T, VEC, HELD>::widen_to(raw, h);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dy[j] = widen(v.v[j]);
-      };
-      for (int i = first; i < p.H; i += step) {
-        load(i);
-        dot(dy, h, i);
-        if (p.dweight)
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) mine[i + j] = fmaf(dy[j], h[j] * r, mine[i + j]);
-      }
-      row_reduce(sum, top, warps, part[turn]);
-      const float c = r * r * (sum / static_cast<float>(p.H));
-      for (int i = first; i < p.H; i += step) {
-        load(i);
-        load_weight<T, VEC>(p.weight, w32, i, w);
-        Vec<T, VEC> res{};
-        if (p.dresidual) res = load_vec<T, VEC>(resrow + i);
-        store_dx<T, VEC>(p, row, i, dy, h, w, r, c, res);
+      for (int j = 0; j < VEC; ++j) {
+        const float t = dy[j] * h[j];
+        sum = fmaf(t, w[j], sum);
+        if (p.dweight && (!ANY || i + j < p.H)) mine[i + j] = fmaf(t, r, mine[i + j]);
       }
     }
-  }
-  if constexpr (NV > 0) {
-    if (p.dweight) {
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (first + k * step < p.H)
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) mine[first + k * step + j] = dw[k][j];
+    row_reduce<false>(sum, top, warps, part[turn]);
+    const float c = r * r * (sum / static_cast<float>(p.H));
+    for (int i = first, i0 = warp_first; i0 < p.H; i += step, i0 += step) {
+      Vec<T, VEC> res{};
+      if (i < p.H) {
+        load_row(i);
+        if (p.dresidual) res = load(static_cast<const T*>(p.dresidual), p.ldr, i);
+      }
+      store_row<T, VEC, ANY>(static_cast<T*>(p.dx) + row * p.ldx + i, i, p.H,
+                             dx_of(dy, h, w, r, c, res, p.dresidual != nullptr));
     }
   }
 }
 
-// The same with rows on their way: each block keeps the next rows of its turn in
-// a ring in shared memory (bulk copies: dy, h and dresidual of a row are one
-// stage), so that what is in flight does not depend on registers or on where a
-// block is between its two passes over a row.  The passes read the stage twice.
-template <typename T, int NV, bool HELD>
-__global__ void __launch_bounds__(512)
+// Rows whose dweight fits the threads' registers, on their way ahead: each block
+// keeps the next rows of its turn in a ring in shared memory (bulk copies: dy, h
+// and dresidual of a row are one stage), so that what is in flight does not
+// depend on registers or on where a block is between its two passes over a row.
+// The passes read the stage twice.  With ANY the copies are of the aligned words
+// around a row, less those that are not all the operand's, whose bytes the copying
+// thread stores.
+template <typename T, int NV, bool HELD, bool ANY>
+__global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(sizeof(T))))
     norm_backward_ring_kernel(const NormBackwardParams p, const int stages) {
   constexpr int VEC = 16 / sizeof(T);
   using HT = std::conditional_t<HELD, int8_t, T>;
@@ -318,11 +342,12 @@ __global__ void __launch_bounds__(512)
   __shared__ int abort_flag;
   const int warps = blockDim.x >> 5;
   const int step = blockDim.x * VEC, first = threadIdx.x * VEC;
-  const uint32_t dy_bytes = p.H * sizeof(T), h_bytes = p.H * sizeof(HT);
+  const int warp_first = (threadIdx.x & ~31) * VEC;  // whole warps store
+  const uint32_t dy_bytes = ring_slot<ANY>(p.H * sizeof(T)), h_bytes = ring_slot<ANY>(p.H * sizeof(HT));
   const uint32_t stage_bytes = dy_bytes + h_bytes + (p.dresidual ? dy_bytes : 0u);
-  const uint32_t ring0 = smem_u32(ring), bar0 = smem_u32(bars);
+  const uint32_t bar0 = smem_u32(bars);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8 * s, 1);
+    for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8 * s, p.dresidual ? 3 : 2);
     abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -330,20 +355,43 @@ __global__ void __launch_bounds__(512)
   pdl_wait();
   pdl_trigger();
   __syncthreads();
-  auto load_row = [&](long long row, int s) {  // one thread
-    const uint32_t bar = bar0 + 8 * s, to = ring0 + s * stage_bytes;
-    mbar_arrive_expect_tx(bar, stage_bytes);
-    bulk_load_1d(to, static_cast<const T*>(p.dy) + row * p.ldy, dy_bytes, bar);
-    bulk_load_1d(to + dy_bytes, static_cast<const HT*>(p.h) + row * p.ldh, h_bytes, bar);
-    if (p.dresidual)
-      bulk_load_1d(to + dy_bytes + h_bytes, static_cast<const T*>(p.dresidual) + row * p.ldr,
-                   dy_bytes, bar);
+  // bytes of a row's first word that are not its own
+  auto lead = [&](const void* row) {
+    return ANY ? static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) : 0;
   };
-  if (threadIdx.x == 0)
-    for (int s = 0; s < stages; ++s) {
-      const long long row = blockIdx.x + static_cast<long long>(s) * gridDim.x;
-      if (row < p.T) load_row(row, s);
+  // lane l of the first warp copies operand l: dy, h, dresidual
+  const int operands = p.dresidual ? 3 : 2;
+  const uint8_t* const base =
+      static_cast<const uint8_t*>(threadIdx.x == 0 ? p.dy : threadIdx.x == 1 ? p.h : p.dresidual);
+  const int size = threadIdx.x == 1 ? sizeof(HT) : sizeof(T), length = p.H * size;
+  const long long stride = (threadIdx.x == 0 ? p.ldy : threadIdx.x == 1 ? p.ldh : p.ldr) * size;
+  const uint32_t slot = threadIdx.x == 0 ? 0u : threadIdx.x == 1 ? dy_bytes : dy_bytes + h_bytes;
+  auto load_row = [&](long long row, int s) {
+    if (threadIdx.x >= operands) return;
+    const uint32_t bar = bar0 + 8 * s;
+    uint8_t* const to = ring + s * stage_bytes + slot;
+    const uint8_t* const from = base + row * stride;
+    if constexpr (ANY) {
+      const int a = lead(from), end = a + length;
+      // the words that are all the operand's: bytes [w0, w1) of the slot
+      const int w0 = row * stride >= a ? 0 : 16;
+      int w1 = (end + 15) & ~15;
+      if ((p.T - 1 - row) * stride + end < w1) w1 -= 16;
+      w1 = max(w0, w1);
+      if (w0 > a)
+        for (int i = a; i < min(w0, end); ++i) to[i] = from[i - a];
+      for (int i = max(w1, a); i < end; ++i) to[i] = from[i - a];
+      mbar_arrive_expect_tx(bar, w1 - w0);
+      if (w1 > w0) bulk_load_1d(smem_u32(to) + w0, from - a + w0, w1 - w0, bar);
+    } else {
+      mbar_arrive_expect_tx(bar, length);
+      bulk_load_1d(smem_u32(to), from, length, bar);
     }
+  };
+  for (int s = 0; s < stages; ++s) {
+    const long long row = blockIdx.x + static_cast<long long>(s) * gridDim.x;
+    if (row < p.T) load_row(row, s);
+  }
   const int blocks = (p.H + ROW_BLOCK - 1) / ROW_BLOCK;
   float dw[NV][VEC] = {};
   float w[NV][VEC];
@@ -362,7 +410,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
   for (int k = 0; k < NV; ++k)
     if (first + k * step < p.H)
-      load_weight<T, VEC>(p.weight, p.weight_type == T_F32, first + k * step, w[k]);
+      load_weight<T, VEC, ANY>(p.weight, p.weight_type == T_F32, first + k * step, p.H, w[k]);
   int s = 0, turn = 0;
   uint32_t ph = 0;
   long long row = blockIdx.x;
@@ -375,27 +423,40 @@ __global__ void __launch_bounds__(512)
     // (a thread that gives up raises the flag before the barrier in row_reduce,
     // after which all see it)
     bounded_wait(bar0 + 8 * s, ph, &abort_flag, p.status, STATUS_TIMEOUT, RING_TIMEOUT_NS);
-    const T* const dyrow = reinterpret_cast<const T*>(ring + s * stage_bytes);
-    const HT* const hrow = reinterpret_cast<const HT*>(ring + s * stage_bytes + dy_bytes);
-    const T* const resrow = reinterpret_cast<const T*>(ring + s * stage_bytes + dy_bytes + h_bytes);
-    auto widen_h = [&](int k, float (&h)[VEC]) {
-      const auto v = load_vec<HT, VEC>(hrow + first + k * step);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if constexpr (HELD)
-          h[j] = fmaf(from_byte(v, j), scale[k], scale[k] * -BYTE_BIAS);
-        else
-          h[j] = widen(v.v[j]);
+    const uint8_t* const stage = ring + s * stage_bytes;
+    const T* const dyrow = reinterpret_cast<const T*>(
+        stage + lead(static_cast<const T*>(p.dy) + row * p.ldy));
+    const HT* const hrow = reinterpret_cast<const HT*>(
+        stage + dy_bytes + lead(static_cast<const HT*>(p.h) + row * p.ldh));
+    const T* const resrow = reinterpret_cast<const T*>(
+        stage + dy_bytes + h_bytes + lead(static_cast<const T*>(p.dresidual) + row * p.ldr));
+    auto load = [&](auto* from, int i) {
+      using E = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
+      if constexpr (ANY) {
+        Around<E, VEC> v;
+        fetch(v, from + i, {0, VEC}, true);  // (its slot ends no earlier)
+        return shifted<true>(v, elements_at<VEC>(i, p.H));
+      } else {
+        return load_vec<E, VEC>(from + i);
       }
     };
     float sum = 0.f;
     uint32_t top = 0u;
+    // (a shifted row stays in registers for the second pass where there are enough)
+    constexpr bool KEEP = ANY && NV == 1;
+    Vec<HT, VEC> hv[NV];
+    Vec<T, VEC> dyv[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (first + k * step < p.H) {
         float h[VEC];
-        widen_h(k, h);
-        const auto dy = load_vec<T, VEC>(dyrow + first + k * step);
+        const auto hk = load(hrow, first + k * step);
+        widen_h(hk, scale[k], h);
+        const auto dy = load(dyrow, first + k * step);
+        if constexpr (KEEP) {
+          hv[k] = hk;
+          dyv[k] = dy;
+        }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           const float t = widen(dy.v[j]) * h[j];
@@ -404,27 +465,32 @@ __global__ void __launch_bounds__(512)
         }
       }
     if (warps == 1) __syncwarp();
-    row_reduce(sum, top, warps, part[turn]);
+    row_reduce<false>(sum, top, warps, part[turn]);
     if (*const_cast<volatile int*>(&abort_flag)) break;
     // every thread is past its second pass over the previous row: its stage
     // takes the row after those under way
-    if (threadIdx.x == 0 && row >= gridDim.x) {
+    if (row >= gridDim.x) {
       const long long next = row + static_cast<long long>(stages - 1) * gridDim.x;
       if (next < p.T) load_row(next, s == 0 ? stages - 1 : s - 1);
     }
     const float c = r * r * (sum / static_cast<float>(p.H));
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (first + k * step < p.H) {
+    for (int k = 0; k < NV; ++k) {
+      const int i = first + k * step;
+      if (ANY ? warp_first + k * step < p.H : i < p.H) {
         float h[VEC], d[VEC];
-        widen_h(k, h);
-        const auto dy = load_vec<T, VEC>(dyrow + first + k * step);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) d[j] = widen(dy.v[j]);
         Vec<T, VEC> res{};
-        if (p.dresidual) res = load_vec<T, VEC>(resrow + first + k * step);
-        store_dx<T, VEC>(p, row, first + k * step, d, h, w[k], r, c, res);
+        if (i < p.H) {
+          widen_h(KEEP ? hv[k] : load(hrow, i), scale[k], h);
+          const auto dy = KEEP ? dyv[k] : load(dyrow, i);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) d[j] = widen(dy.v[j]);
+          if (p.dresidual) res = load(resrow, i);
+        }
+        store_row<T, VEC, ANY>(static_cast<T*>(p.dx) + row * p.ldx + i, i, p.H,
+                               dx_of(d, h, w[k], r, c, res, p.dresidual != nullptr));
       }
+    }
     if (++s == stages) {
       s = 0;
       ph ^= 1u;
@@ -434,9 +500,9 @@ __global__ void __launch_bounds__(512)
     float* const mine = p.partial + static_cast<long long>(blockIdx.x) * p.H;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (first + k * step < p.H)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) mine[first + k * step + j] = dw[k][j];
+      for (int j = 0; j < VEC; ++j)
+        if (first + k * step + (ANY ? j : 0) < p.H) mine[first + k * step + j] = dw[k][j];
   }
   // after a wait that ran out: copies still under way land before the block leaves
   if (row < p.T && threadIdx.x == 0) {
@@ -471,26 +537,27 @@ __global__ void __launch_bounds__(1024)
 // ---------------------------------------------------------------- launches
 int up32(long long n) { return static_cast<int>((n + 31) / 32 * 32); }
 
-template <typename T, int VEC, bool I8>
+template <typename T, int VEC, bool I8, bool ANY>
 cudaError_t launch_forward(const NormParams& p, int num_sms, cudaStream_t st) {
-  const int n = (p.H + VEC - 1) / VEC;
+  const int n = (p.H + (ANY ? 2 : 1) * (VEC - 1)) / VEC;
   // Vectors a thread: four keep enough in flight where there are rows for all
-  // SMs; few rows are spread over more threads.
-  constexpr int MOST = VEC == 1 ? 8 : 4;  // by the registers of 1024 threads
+  // SMs; few rows are spread over more threads.  With ANY, two as far as blocks
+  // of 512 threads go, since four are loaded one after the other (8192 rows of
+  // 5001 bf16 79 us with two, 98 with four; of 5001 fp32 224 with two in 640
+  // threads, 139 with four).
+  constexpr int MOST = 4;  // by the registers of 1024 threads
   const int most = p.T >= 4ll * num_sms ? MOST : p.T >= num_sms ? MOST / 2 : 1;
   int nv = 1;
-  while (nv < most && n > 32 * nv) nv *= 2;
+  while (nv < most && n > (ANY && nv > 1 ? 512 : 32) * nv) nv *= 2;
   while (nv < MOST && n > 1024 * nv) nv *= 2;
   const bool again = n > 1024 * nv;
   const int threads = again ? 1024 : up32((n + nv - 1) / nv);
   const int rows = threads == 32 ? 4 : 1;
   const dim3 grid(static_cast<unsigned>((p.T + rows - 1) / rows)), block(threads, rows);
-  if (again) return launch_pdl(norm_kernel<T, VEC, 0, I8>, grid, block, 0, st, p);
-  if constexpr (MOST >= 8)
-    if (nv == 8) return launch_pdl(norm_kernel<T, VEC, 8, I8>, grid, block, 0, st, p);
-  if (nv == 4) return launch_pdl(norm_kernel<T, VEC, 4, I8>, grid, block, 0, st, p);
-  if (nv == 2) return launch_pdl(norm_kernel<T, VEC, 2, I8>, grid, block, 0, st, p);
-  return launch_pdl(norm_kernel<T, VEC, 1, I8>, grid, block, 0, st, p);
+  if (again) return launch_pdl(norm_kernel<T, VEC, 0, I8, ANY>, grid, block, 0, st, p);
+  if (nv == 4) return launch_pdl(norm_kernel<T, VEC, 4, I8, ANY>, grid, block, 0, st, p);
+  if (nv == 2) return launch_pdl(norm_kernel<T, VEC, 2, I8, ANY>, grid, block, 0, st, p);
+  return launch_pdl(norm_kernel<T, VEC, 1, I8, ANY>, grid, block, 0, st, p);
 }
 
 // Threads and vectors a thread of a ring block: as many vectors as its sums of
@@ -500,25 +567,25 @@ cudaError_t launch_forward(const NormParams& p, int num_sms, cudaStream_t st) {
 template <typename T>
 int ring_threads(int H, int& nv) {
   constexpr int VEC = 16 / sizeof(T);
-  const int n = H / VEC;
+  const int n = (H + VEC - 1) / VEC;
   for (nv = 1; nv < 4 && n > 128 * nv;) nv *= 2;
   return n <= 512 * nv ? up32((n + nv - 1) / nv) : 0;
 }
 
 // A ring kernel's blocks an SM, by registers and shared memory, and stages a
 // block; false where two stages do not fit.
-bool ring_shape(int stage_bytes, int threads, int sums, int& blocks, int& stages) {
-  for (blocks = std::min(BACKWARD_BLOCKS, (sums > 8 ? 512 : 1024) / threads); blocks > 0; --blocks) {
-    stages = std::min(RING_MOST, RING_BYTES / blocks / stage_bytes);
+bool ring_shape(int64_t stage_bytes, int threads, int room, int& blocks, int& stages) {
+  for (blocks = std::min(BACKWARD_BLOCKS, room / threads); blocks > 0; --blocks) {
+    stages = static_cast<int>(std::min<int64_t>(RING_MOST, RING_BYTES / blocks / stage_bytes));
     if (stages >= 2) return true;
   }
   return false;
 }
 
-template <typename T, int NV, bool HELD>
+template <typename T, int NV, bool HELD, bool ANY>
 cudaError_t launch_ring(const NormBackwardParams& p, int threads, int blocks, int stages,
                         int stage_bytes, cudaStream_t st) {
-  auto* const kernel = norm_backward_ring_kernel<T, NV, HELD>;
+  auto* const kernel = norm_backward_ring_kernel<T, NV, HELD, ANY>;
   const int bytes = stages * stage_bytes;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES);
@@ -526,37 +593,25 @@ cudaError_t launch_ring(const NormBackwardParams& p, int threads, int blocks, in
   return launch_pdl(kernel, dim3(blocks), dim3(threads), bytes, st, p, stages);
 }
 
-// Rows that allow vectors and fit the ring; launched (with *blocks set) or not.
-template <typename T, bool HELD>
-bool try_ring(const NormBackwardParams& p, int num_sms, int& blocks, cudaError_t& e,
-              cudaStream_t st) {
+template <typename T, bool HELD, bool ANY>
+cudaError_t launch_backward(const NormBackwardParams& p, int num_sms, int& blocks, cudaStream_t st) {
   constexpr int S = sizeof(T);
-  if (HELD && p.H % 16 != 0) return false;  // bulk copies are of 16 bytes
   int nv, per_sm, stages;
   const int threads = ring_threads<T>(p.H, nv);
-  const int stage_bytes = p.H * (S + (HELD ? 1 : S) + (p.dresidual ? S : 0));
-  if (threads == 0 || !ring_shape(stage_bytes, threads, nv * 16 / S, per_sm, stages)) return false;
-  blocks = static_cast<int>(std::min<long long>(p.T, static_cast<long long>(num_sms) * per_sm));
-  e = nv == 1   ? launch_ring<T, 1, HELD>(p, threads, blocks, stages, stage_bytes, st)
-      : nv == 2 ? launch_ring<T, 2, HELD>(p, threads, blocks, stages, stage_bytes, st)
-                : launch_ring<T, 4, HELD>(p, threads, blocks, stages, stage_bytes, st);
-  return true;
-}
-
-// Rows the ring does not take: of any alignment, with their values in registers
-// up to 8192 of them, else read twice.
-template <typename T, int VEC, bool HELD>
-cudaError_t launch_backward(const NormBackwardParams& p, int blocks, cudaStream_t st) {
-  const dim3 grid(blocks);
-  if constexpr (VEC == 1) {
-    const int nv = p.H <= 2048 ? 8 : 16;
-    if (p.H <= 512 * nv) {
-      const dim3 block(up32((p.H + nv - 1) / nv));
-      return nv == 8 ? launch_pdl(norm_backward_kernel<T, VEC, 8, HELD>, grid, block, 0, st, p)
-                     : launch_pdl(norm_backward_kernel<T, VEC, 16, HELD>, grid, block, 0, st, p);
-    }
+  const uint32_t H = p.H;  // (four bytes of 2^30 elements and more pass an int)
+  const int64_t stage_bytes =
+      ring_slot<ANY>(H * S) * (p.dresidual ? 2ll : 1ll) + ring_slot<ANY>(H * (HELD ? 1 : S));
+  auto blocks_of = [&](int each) {
+    return static_cast<int>(std::min<long long>(p.T, static_cast<long long>(num_sms) * each));
+  };
+  if (threads > 0 && ring_shape(stage_bytes, threads, ring_room(ANY, nv, nv * 16 / S), per_sm, stages)) {
+    blocks = blocks_of(per_sm);
+    return nv == 1   ? launch_ring<T, 1, HELD, ANY>(p, threads, blocks, stages, static_cast<int>(stage_bytes), st)
+           : nv == 2 ? launch_ring<T, 2, HELD, ANY>(p, threads, blocks, stages, static_cast<int>(stage_bytes), st)
+                     : launch_ring<T, 4, HELD, ANY>(p, threads, blocks, stages, static_cast<int>(stage_bytes), st);
   }
-  return launch_pdl(norm_backward_kernel<T, VEC, 0, HELD>, grid, dim3(512), 0, st, p);
+  blocks = blocks_of(2);
+  return launch_pdl(norm_backward_kernel<T, 16 / S, HELD, ANY>, dim3(blocks), dim3(512), 0, st, p);
 }
 
 // Whether rows (base, leading dimension in elements of `size` bytes) allow
@@ -573,22 +628,22 @@ cudaError_t forward_typed(const NormParams& p, int num_sms, cudaStream_t st) {
                    rows_fit(p.weight, 0, 1, 16) &&
                    (p.i8 ? rows_fit(p.y, p.ldy, 1, VEC) : rows_fit(p.y, p.ldy, S, 16));
   if (p.i8)
-    return vec ? launch_forward<T, VEC, true>(p, num_sms, st) : launch_forward<T, 1, true>(p, num_sms, st);
-  return vec ? launch_forward<T, VEC, false>(p, num_sms, st) : launch_forward<T, 1, false>(p, num_sms, st);
+    return vec ? launch_forward<T, VEC, true, false>(p, num_sms, st)
+               : launch_forward<T, VEC, true, true>(p, num_sms, st);
+  return vec ? launch_forward<T, VEC, false, false>(p, num_sms, st)
+             : launch_forward<T, VEC, false, true>(p, num_sms, st);
 }
 
 template <typename T, bool HELD>
 cudaError_t backward_held(const NormBackwardParams& p, int num_sms, int& blocks, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(T), S = sizeof(T);
-  const bool vec = p.H % VEC == 0 && rows_fit(p.dy, p.ldy, S, 16) &&
-                   (HELD ? rows_fit(p.h, p.ldh, 1, VEC) : rows_fit(p.h, p.ldh, S, 16)) &&
+  // (bulk copies are of 16 bytes, so that block rows' length is of 16 values)
+  const bool vec = p.H % (HELD ? 16 : VEC) == 0 && rows_fit(p.dy, p.ldy, S, 16) &&
+                   (HELD ? rows_fit(p.h, p.ldh, 1, 16) : rows_fit(p.h, p.ldh, S, 16)) &&
                    (!p.dresidual || rows_fit(p.dresidual, p.ldr, S, 16)) &&
                    rows_fit(p.dx, p.ldx, S, 16) && rows_fit(p.weight, 0, 1, 16);
-  cudaError_t e = cudaSuccess;
-  if (vec && (!HELD || rows_fit(p.h, p.ldh, 1, 16)) && try_ring<T, HELD>(p, num_sms, blocks, e, st))
-    return e;
-  blocks = norm_partial_rows(p.T, num_sms);
-  return vec ? launch_backward<T, VEC, HELD>(p, blocks, st) : launch_backward<T, 1, HELD>(p, blocks, st);
+  return vec ? launch_backward<T, HELD, false>(p, num_sms, blocks, st)
+             : launch_backward<T, HELD, true>(p, num_sms, blocks, st);
 }
 
 template <typename T>

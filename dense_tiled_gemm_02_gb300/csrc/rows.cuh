@@ -32,6 +32,153 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, VEC>& x) {
   *reinterpret_cast<Vec<T, VEC>*>(p) = x;
 }
 
+// ---------------------------------------------------------------- rows of any alignment
+// Rows whose length or place allows no vectors: a thread's VEC elements are read
+// as the aligned words around them, shifted together, and stored as aligned
+// words with the neighbouring lane's bytes in front, since an access for each
+// element is bound by the number of accesses (8525 x 7723 of fp16 to scaled rows
+// and back 283 us, this way 113; the norm of 8192 x 5001 of bf16 150 and 80 us, its
+// gradients 473 and 153).  What is left above the floor is instructions.
+template <typename T, int VEC>
+struct Around {
+  static constexpr int S = sizeof(T), BYTES = VEC * S, WORD = BYTES < 16 ? BYTES : 16;
+  static constexpr int N = BYTES / WORD, Q = WORD / 4;
+  uint32_t w[(N + 1) * Q];
+  uint32_t shift;
+};
+
+// Of the VEC elements from i on (with LEAD i may be negative), those of a row of
+// H: [from, to), to = 0 for none.
+struct Range {
+  int from, to;
+};
+template <int VEC, bool LEAD = false>
+__device__ __forceinline__ Range elements_at(int i, int H) {
+  return {LEAD ? max(0, -i) : 0, max(0, min(VEC, H - i))};
+}
+
+// Whether the words around the VEC elements at `at` lie within T rows of H
+// elements, ld apart.
+template <int VEC>
+__device__ __forceinline__ bool inside(long long at, long long T, long long ld, int H) {
+  return at >= VEC && at + 2 * VEC <= (T - 1) * ld + H;
+}
+
+// Elements `n` of those from p on, of which there are some; one by one where the
+// words around are not all the operand's.
+template <typename T, int VEC>
+__device__ __forceinline__ void fetch(Around<T, VEC>& x, const T* p, const Range& n, bool words) {
+  using A = Around<T, VEC>;
+  const uint32_t a = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & (A::WORD - 1);
+#pragma unroll
+  for (int j = 0; j < (A::N + 1) * A::Q; ++j) x.w[j] = 0u;
+  x.shift = words ? a : 0u;
+  if (words) {
+    const uint8_t* const from = reinterpret_cast<const uint8_t*>(p) - a;
+#pragma unroll
+    for (int k = 0; k <= A::N; ++k)
+      if (k * A::WORD < static_cast<int>(a) + n.to * A::S) {
+        const auto v = load_vec<uint32_t, A::Q>(reinterpret_cast<const uint32_t*>(from + k * A::WORD));
+#pragma unroll
+        for (int j = 0; j < A::Q; ++j) x.w[k * A::Q + j] = v.v[j];
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j >= n.from && j < n.to) {
+        using Bits = std::conditional_t<A::S == 4, uint32_t, std::conditional_t<A::S == 2, uint16_t, uint8_t>>;
+        const uint32_t bits = reinterpret_cast<const Bits*>(p)[j];
+        x.w[j * A::S / 4] |= bits << (j * A::S % 4 * 8);
+      }
+  }
+}
+
+// What was fetched; zeros for the other elements.  OFTEN: a branch passes by the
+// shift where there is none (which costs rows that nearly all have one a tenth).
+template <bool OFTEN, typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> shifted(const Around<T, VEC>& x, const Range& n) {
+  using A = Around<T, VEC>;
+  constexpr int W = (A::N + 1) * A::Q;
+  uint32_t w[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) w[j] = x.w[j];
+  if (!OFTEN || x.shift != 0u) {
+    if constexpr (A::Q >= 4) {
+#pragma unroll
+      for (int j = 0; j + 2 < W; ++j) w[j] = x.shift & 8u ? w[j + 2] : w[j];
+    }
+    if constexpr (A::Q >= 2) {
+#pragma unroll
+      for (int j = 0; j + 1 < W; ++j) w[j] = x.shift & 4u ? w[j + 1] : w[j];
+    }
+    if constexpr (A::S < 4) {
+#pragma unroll
+      for (int j = 0; j + 1 < W; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 8u * (x.shift & 3u));
+    }
+  }
+  Vec<T, VEC> o;
+  memcpy(&o, w, A::BYTES);
+  if (n.from > 0 || n.to < VEC) {
+    Vec<T, VEC> zeros;
+    memset(&zeros, 0, sizeof zeros);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j < n.from || j >= n.to) o.v[j] = zeros.v[j];
+  }
+  return o;
+}
+
+// Elements `n` of each lane's vector to p on, which is element i of a row.  All
+// lanes of a warp call; each one's elements follow those of the lane before, but
+// where a row begins.
+template <bool OFTEN, typename T, int VEC>
+__device__ __forceinline__ void store_shifted(T* p, int i, const Range& n, const Vec<T, VEC>& x) {
+  using A = Around<T, VEC>;
+  constexpr int N = A::N, Q = A::Q, WORD = A::WORD, S = A::S;
+  const int a = static_cast<int>(reinterpret_cast<uintptr_t>(p)) & (WORD - 1);
+  const int end = a + n.to * S;
+  uint32_t w[(N + 1) * Q];
+  memcpy(w + Q, &x, A::BYTES);
+  bool takes = false, given = false;
+  if (!OFTEN || !__all_sync(0xFFFFFFFFu, a == 0)) {
+    const int lane = threadIdx.x & 31;
+    // a lane with a whole word takes the bytes in front of its own into it
+    takes = lane > 0 && i >= VEC && end >= WORD && n.to > 0;
+    given = __shfl_down_sync(0xFFFFFFFFu, static_cast<int>(takes), 1) && lane < 31;
+#pragma unroll
+    for (int j = 0; j < Q; ++j) w[j] = __shfl_up_sync(0xFFFFFFFFu, w[N * Q + j], 1);
+    if constexpr (Q >= 4) {
+#pragma unroll
+      for (int j = (N + 1) * Q - 1; j >= 2; --j) w[j] = a & 8 ? w[j - 2] : w[j];
+    }
+    if constexpr (Q >= 2) {
+#pragma unroll
+      for (int j = (N + 1) * Q - 1; j >= 1; --j) w[j] = a & 4 ? w[j - 1] : w[j];
+    }
+    if constexpr (S < 4) {
+#pragma unroll
+      for (int j = (N + 1) * Q - 1; j >= Q; --j) w[j] = __funnelshift_l(w[j - 1], w[j], 8u * (a & 3));
+    }
+  }
+  const int begin = takes ? 0 : a + n.from * S;
+  uint8_t* const to = reinterpret_cast<uint8_t*>(p) - a;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (k * WORD >= begin && (k + 1) * WORD <= end) {
+      Vec<uint32_t, Q> v;
+#pragma unroll
+      for (int j = 0; j < Q; ++j) v.v[j] = w[(k + 1) * Q + j];
+      store_vec(reinterpret_cast<uint32_t*>(to + k * WORD), v);
+    }
+  // the elements of words that are not whole
+  const int head = (begin + WORD - 1) / WORD * WORD, tail = given ? end : end / WORD * WORD;
+  if (n.to > 0 && (begin < head || tail < end)) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j >= n.from && j < n.to && (a + j * S < head || a + j * S >= tail)) p[j] = x.v[j];
+  }
+}
+
 // The largest finite value of a type.
 template <typename T>
 __device__ __forceinline__ float largest() {
@@ -52,15 +199,19 @@ __device__ __forceinline__ void narrow_finite(float v, T& x) {
 // which fmaxf would let pass.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Sum (and largest) over the threads of a row: one warp, or `warps` of them
+// Sum and (TOP) largest over the threads of a row: one warp, or `warps` of them
 // with the partial results in `part`, which no later call may still be reading:
 // callers take two in turn.  In a fixed order, and the same in every thread.
+template <bool TOP = true>
 __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int warps, float2* part) {
+  auto over_warp = [&] {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  }
+    for (int d = 16; d > 0; d >>= 1) {
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      if constexpr (TOP) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    }
+  };
+  over_warp();
   if (warps == 1) return;
   const int lane = threadIdx.x & 31;
   if (lane == 0) part[threadIdx.x >> 5] = make_float2(sum, __uint_as_float(top));
@@ -68,11 +219,7 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int warps,
   const float2 x = lane < warps ? part[lane] : make_float2(0.f, 0.f);
   sum = x.x;
   top = __float_as_uint(x.y);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  }
+  over_warp();
 }
 
 // The largest magnitude of a vector, as the bits of an fp32 number.  Those of
@@ -107,19 +254,17 @@ __device__ __forceinline__ uint32_t nearest(float v, float inverse) {
 
 // The last bytes of n, or zeros.
 template <int VEC>
-__device__ __forceinline__ void store_bytes(int8_t* p, const uint32_t (&n)[VEC], bool zero) {
-  if constexpr (VEC == 1) {
-    *p = zero ? int8_t(0) : static_cast<int8_t>(n[0]);
-  } else {
-    Vec<uint32_t, VEC / 4> w;
+__device__ __forceinline__ Vec<int8_t, VEC> last_bytes(const uint32_t (&n)[VEC], bool zero) {
+  Vec<uint32_t, VEC / 4> w;
 #pragma unroll
-    for (int j = 0; j < VEC / 4; ++j) {
-      const uint32_t v = __byte_perm(__byte_perm(n[4 * j], n[4 * j + 1], 0x0040),
-                                     __byte_perm(n[4 * j + 2], n[4 * j + 3], 0x0040), 0x5410);
-      w.v[j] = zero ? 0u : v;
-    }
-    store_vec(reinterpret_cast<uint32_t*>(p), w);
+  for (int j = 0; j < VEC / 4; ++j) {
+    const uint32_t v = __byte_perm(__byte_perm(n[4 * j], n[4 * j + 1], 0x0040),
+                                   __byte_perm(n[4 * j + 2], n[4 * j + 3], 0x0040), 0x5410);
+    w.v[j] = zero ? 0u : v;
   }
+  Vec<int8_t, VEC> q;
+  memcpy(&q, &w, VEC);
+  return q;
 }
 
 // 2^23 + 128 + the integer j of a vector: its byte, sign flipped, as the last of
@@ -135,12 +280,7 @@ constexpr float BYTE_BIAS = 8388736.f;
 template <int VEC>
 __device__ __forceinline__ void integers(const Vec<int8_t, VEC>& q, float (&o)[VEC]) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    if constexpr (VEC % 4 == 0)
-      o[j] = from_byte(q, j) - BYTE_BIAS;
-    else
-      o[j] = static_cast<float>(q.v[j]);
-  }
+  for (int j = 0; j < VEC; ++j) o[j] = from_byte(q, j) - BYTE_BIAS;
 }
 
 // ---------------------------------------------------------------- scaled rows
@@ -159,11 +299,11 @@ __device__ __forceinline__ RowScale row_scale(float top, float unit) {
 }
 // The integers of VEC values (see nearest); 0 for a scale that is not finite.
 template <int VEC>
-__device__ __forceinline__ void store_row_integers(int8_t* p, const float (&v)[VEC], const RowScale& r) {
+__device__ __forceinline__ Vec<int8_t, VEC> row_integers(const float (&v)[VEC], const RowScale& r) {
   uint32_t n[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) n[j] = nearest(v[j] * r.pre, r.inv);
-  store_bytes(p, n, !(r.inv > 0.f));
+  return last_bytes(n, !(r.inv > 0.f));
 }
 
 // ---------------------------------------------------------------- block rows
@@ -189,11 +329,11 @@ __device__ __forceinline__ float block_inverse(uint32_t e) {
   return e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
 }
 template <int VEC>
-__device__ __forceinline__ void store_block_integers(int8_t* p, const float (&v)[VEC], float inverse) {
+__device__ __forceinline__ Vec<int8_t, VEC> block_integers(const float (&v)[VEC], float inverse) {
   uint32_t n[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) n[j] = nearest(v[j], inverse);
-  store_bytes(p, n, !(inverse > 0.f));
+  return last_bytes(n, !(inverse > 0.f));
 }
 
 // ---------------------------------------------------------------- items of rows

@@ -10,7 +10,8 @@
 // an item's row another 5).
 //
 // Measured (one GB300, 16384 x 4096 bf16, floor 30.1 us each way): block rows 30
-// us and back 33, scaled rows 29 and back 34.
+// us and back 33, scaled rows 29 and back 34; 16384 x 4095, whose rows are of any
+// alignment, 57 and 57, 58 and 51 (an access an element: 174 and 137, 94 and 132).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -26,12 +27,12 @@ namespace {
 constexpr int THREADS = DEAL_THREADS;
 
 // ---------------------------------------------------------------- block rows
-// LANES lanes to 32 values; VEC 1 (rows that do not allow vectors): a warp.
-template <typename T, int VEC>
+// LANES lanes to 32 values.  ANY: rows of any alignment.
+template <typename T, int VEC, bool ANY>
 __global__ void __launch_bounds__(THREADS)
     pack_blocks_kernel(const Rows8Params p, const Deal deal) {
   const int blocks = (p.H + ROW_BLOCK - 1) / ROW_BLOCK;
-  constexpr int LANES = ROW_BLOCK / VEC, U = 4;
+  constexpr int LANES = ROW_BLOCK / VEC, U = ANY ? 2 : 4;
   const Items all = block_items(p.T, deal, blockIdx.x);
   const Divisor& lanes = deal.lanes;
   pdl_wait();
@@ -39,38 +40,49 @@ __global__ void __launch_bounds__(THREADS)
   // (whole warps stay together: lanes past the last item load nothing but shuffle)
   for (uint32_t at0 = threadIdx.x; at0 - (threadIdx.x & 31) < all.n; at0 += U * THREADS) {
     Vec<T, VEC> x[U];
+    Around<T, VEC> around[ANY ? U : 1];
     long long row[U];
     int i[U];
-    bool ok[U];
+    Range n[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t at = all.at + at0 + u * THREADS, r = divide(at, lanes);
       row[u] = all.row + r;
       i[u] = static_cast<int>(at - r * lanes.d) * VEC;
-      ok[u] = at0 + u * THREADS < all.n && i[u] < p.H;
-      x[u] = Vec<T, VEC>{};
-      if (ok[u]) x[u] = load_vec<T, VEC>(static_cast<const T*>(p.X) + row[u] * p.ldx + i[u]);
+      n[u] = at0 + u * THREADS < all.n ? elements_at<VEC>(i[u], p.H) : Range{0, 0};
+      const long long from_at = row[u] * p.ldx + i[u];
+      const T* const from = static_cast<const T*>(p.X) + from_at;
+      if constexpr (ANY) {
+        if (n[u].to > 0) fetch(around[u], from, n[u], inside<VEC>(from_at, p.T, p.ldx, p.H));
+      } else {
+        x[u] = Vec<T, VEC>{};
+        if (n[u].to > 0) x[u] = load_vec<T, VEC>(from);
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if constexpr (ANY) x[u] = shifted<false>(around[u], n[u]);
       uint32_t top = vec_top(x[u]);
 #pragma unroll
       for (int d = LANES / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
       const uint32_t e = block_exponent(top, least_exponent<T>());
       const float inverse = block_inverse(e);
-      if (ok[u]) {
-        float v[VEC];
+      float v[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] = widen(x[u].v[j]);
-        store_block_integers(p.q_out + row[u] * p.ldq + i[u], v, inverse);
-        if (i[u] % ROW_BLOCK == 0)
-          static_cast<uint8_t*>(p.scales_out)[row[u] * blocks + i[u] / ROW_BLOCK] = e;
-      }
+      for (int j = 0; j < VEC; ++j) v[j] = widen(x[u].v[j]);
+      const auto q = block_integers(v, inverse);
+      int8_t* const to = p.q_out + row[u] * p.ldq + i[u];
+      if constexpr (ANY)
+        store_shifted<false>(to, i[u], n[u], q);
+      else if (n[u].to > 0)
+        store_vec(to, q);
+      if (n[u].to > 0 && i[u] % ROW_BLOCK == 0)
+        static_cast<uint8_t*>(p.scales_out)[row[u] * blocks + i[u] / ROW_BLOCK] = e;
     }
   }
 }
 
-template <typename T, int VEC, bool BLOCKS>
+template <typename T, int VEC, bool BLOCKS, bool ANY>
 __global__ void __launch_bounds__(THREADS)
     unpack_kernel(const Rows8Params p, const Deal deal) {
   const int blocks = (p.H + ROW_BLOCK - 1) / ROW_BLOCK;
@@ -79,25 +91,35 @@ __global__ void __launch_bounds__(THREADS)
   pdl_wait();
   pdl_trigger();
   constexpr int U = 2;
-  for (uint32_t at0 = threadIdx.x; at0 < all.n; at0 += U * THREADS) {
+  for (uint32_t at0 = threadIdx.x; at0 - (threadIdx.x & 31) < all.n; at0 += U * THREADS) {
     Vec<int8_t, VEC> q[U];
+    Around<int8_t, VEC> around[ANY ? U : 1];
     float step[U];
     T* to[U];
+    int i[U];
+    Range n[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t at = all.at + at0 + u * THREADS, r = divide(at, lanes);
       const long long row = all.row + r;
-      const int i = static_cast<int>(at - r * lanes.d) * VEC;
-      to[u] = static_cast<T*>(p.X_out) + row * p.ldx + i;
-      if (at0 + u * THREADS < all.n) {
-        q[u] = load_vec<int8_t, VEC>(p.q + row * p.ldq + i);
-        step[u] = BLOCKS ? block_step(static_cast<const uint8_t*>(p.scales)[row * blocks + i / ROW_BLOCK])
+      i[u] = static_cast<int>(at - r * lanes.d) * VEC;
+      n[u] = at0 + u * THREADS < all.n ? elements_at<VEC>(i[u], p.H) : Range{0, 0};
+      to[u] = static_cast<T*>(p.X_out) + row * p.ldx + i[u];
+      if (n[u].to > 0) {
+        const long long from_at = row * p.ldq + i[u];
+        const int8_t* const from = p.q + from_at;
+        if constexpr (ANY)
+          fetch(around[u], from, n[u], inside<VEC>(from_at, p.T, p.ldq, p.H));
+        else
+          q[u] = load_vec<int8_t, VEC>(from);
+        step[u] = BLOCKS ? block_step(static_cast<const uint8_t*>(p.scales)[row * blocks + i[u] / ROW_BLOCK])
                          : static_cast<const float*>(p.scales)[row];
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (at0 + u * THREADS < all.n) {
+      if (ANY || n[u].to > 0) {
+        if constexpr (ANY) q[u] = shifted<false>(around[u], n[u]);
         float v[VEC];
         integers(q[u], v);
         Vec<T, VEC> x;
@@ -108,7 +130,10 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
           for (int j = 0; j < VEC; ++j) narrow_finite(v[j] * step[u], x.v[j]);
         }
-        store_vec(to[u], x);
+        if constexpr (ANY)
+          store_shifted<false>(to[u], i[u], n[u], x);
+        else
+          store_vec(to[u], x);
       }
   }
 }
@@ -116,29 +141,47 @@ __global__ void __launch_bounds__(THREADS)
 // ---------------------------------------------------------------- scaled rows
 // A block (or, blockDim.x = 32, a warp) a row, whose threads hold NV vectors
 // each, or with NV = 0 (rows too long) read them again.
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, bool ANY>
 __global__ void __launch_bounds__(1024) pack_rows_kernel(const Rows8Params p) {
   __shared__ float2 part[32];
   const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int step = blockDim.x * VEC, first = threadIdx.x * VEC;
+  const int warp_first = (threadIdx.x & ~31) * VEC;  // whole warps stay together
   pdl_wait();
   pdl_trigger();
   if (row >= p.T) return;
   const T* const X = static_cast<const T*>(p.X) + row * p.ldx;
   constexpr int N = NV > 0 ? NV : 1;
   Vec<T, VEC> x[N];
+  Around<T, VEC> around[ANY ? N : 1];
   uint32_t top = 0u;
   float sum = 0.f;
-  auto largest_of = [&](const Vec<T, VEC>& v) { top = max(top, vec_top(v)); };
+  auto load = [&](int k, int i) {
+    const Range n = elements_at<VEC>(i, p.H);
+    if (n.to == 0) return;
+    if constexpr (ANY)
+      fetch(around[k], X + i, n, inside<VEC>(row * p.ldx + i, p.T, p.ldx, p.H));
+    else
+      x[k] = load_vec<T, VEC>(X + i);
+  };
+  auto settle = [&](int k, int i) {
+    if constexpr (ANY) x[k] = shifted<false>(around[k], elements_at<VEC>(i, p.H));
+  };
   if constexpr (NV > 0) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (first + k * step < p.H) x[k] = load_vec<T, VEC>(X + first + k * step);
+    for (int k = 0; k < NV; ++k) load(k, first + k * step);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (first + k * step < p.H) largest_of(x[k]);
+      if (first + k * step < p.H) {
+        settle(k, first + k * step);
+        top = max(top, vec_top(x[k]));
+      }
   } else {
-    for (int i = first; i < p.H; i += step) largest_of(load_vec<T, VEC>(X + i));
+    for (int i = first; i < p.H; i += step) {
+      load(0, i);
+      settle(0, i);
+      top = max(top, vec_top(x[0]));
+    }
   }
   row_reduce(sum, top, blockDim.x >> 5, part);
   const RowScale s = row_scale(__uint_as_float(top), 1.f);
@@ -147,28 +190,37 @@ __global__ void __launch_bounds__(1024) pack_rows_kernel(const Rows8Params p) {
     float f[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) f[j] = widen(v.v[j]);
-    store_row_integers(p.q_out + row * p.ldq + i, f, s);
+    const auto q = row_integers(f, s);
+    int8_t* const to = p.q_out + row * p.ldq + i;
+    if constexpr (ANY)
+      store_shifted<false>(to, i, elements_at<VEC>(i, p.H), q);
+    else if (i < p.H)
+      store_vec(to, q);
   };
   if constexpr (NV > 0) {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (first + k * step < p.H) store(x[k], first + k * step);
+      if (warp_first + k * step < p.H) store(x[k], first + k * step);
   } else {
-    for (int i = first; i < p.H; i += step) store(load_vec<T, VEC>(X + i), i);
+    for (int i = first, i0 = warp_first; i0 < p.H; i += step, i0 += step) {
+      load(0, i);
+      settle(0, i);
+      store(x[0], i);
+    }
   }
 }
 
 // ---------------------------------------------------------------- launches
-template <typename T, int VEC>
+template <typename T, int VEC, bool ANY>
 cudaError_t pack_as(const Rows8Params& p, int num_sms, cudaStream_t st) {
   if (p.block) {
     const int lanes = (p.H + ROW_BLOCK - 1) / ROW_BLOCK * (ROW_BLOCK / VEC);
     dim3 grid;
     const Deal deal = deal_of(p.T, lanes, num_sms, grid);
-    return launch_pdl(pack_blocks_kernel<T, VEC>, grid, dim3(THREADS), 0, st, p, deal);
+    return launch_pdl(pack_blocks_kernel<T, VEC, ANY>, grid, dim3(THREADS), 0, st, p, deal);
   }
   // few rows are spread over more threads
-  constexpr int MOST = VEC == 1 ? 8 : VEC == 16 ? 2 : 4;
+  constexpr int MOST = VEC == 16 || ANY ? 2 : 4;
   const int n = (p.H + VEC - 1) / VEC;
   int nv = p.T >= num_sms ? MOST : 1;
   while (nv > 1 && n <= 16 * nv) nv /= 2;
@@ -176,21 +228,23 @@ cudaError_t pack_as(const Rows8Params& p, int num_sms, cudaStream_t st) {
   const bool again = n > 1024 * nv;
   const int threads = again ? 1024 : (((n + nv - 1) / nv) + 31) / 32 * 32, rows = threads == 32 ? 4 : 1;
   const dim3 grid(static_cast<unsigned>((p.T + rows - 1) / rows)), block(threads, rows);
-  if (again) return launch_pdl(pack_rows_kernel<T, VEC, 0>, grid, block, 0, st, p);
-  if (nv == 1) return launch_pdl(pack_rows_kernel<T, VEC, 1>, grid, block, 0, st, p);
-  if constexpr (MOST == 8)
-    if (nv == 8) return launch_pdl(pack_rows_kernel<T, VEC, 8>, grid, block, 0, st, p);
+  if (again) return launch_pdl(pack_rows_kernel<T, VEC, 0, ANY>, grid, block, 0, st, p);
+  if (nv == 1) return launch_pdl(pack_rows_kernel<T, VEC, 1, ANY>, grid, block, 0, st, p);
   if constexpr (MOST >= 4)
-    if (nv == 4) return launch_pdl(pack_rows_kernel<T, VEC, 4>, grid, block, 0, st, p);
-  return launch_pdl(pack_rows_kernel<T, VEC, 2>, grid, block, 0, st, p);
+    if (nv == 4) return launch_pdl(pack_rows_kernel<T, VEC, 4, ANY>, grid, block, 0, st, p);
+  return launch_pdl(pack_rows_kernel<T, VEC, 2, ANY>, grid, block, 0, st, p);
 }
-template <typename T, int VEC>
+template <typename T, int VEC, bool ANY>
 cudaError_t unpack_as(const Rows8Params& p, int num_sms, cudaStream_t st) {
-  const int lanes = p.H / VEC;
+  const int lanes = (p.H + VEC - 1) / VEC;
   dim3 grid;
   const Deal deal = deal_of(p.T, lanes, num_sms, grid);
-  return p.block ? launch_pdl(unpack_kernel<T, VEC, true>, grid, dim3(THREADS), 0, st, p, deal)
-                 : launch_pdl(unpack_kernel<T, VEC, false>, grid, dim3(THREADS), 0, st, p, deal);
+  return p.block ? launch_pdl(unpack_kernel<T, VEC, true, ANY>, grid, dim3(THREADS), 0, st, p, deal)
+                 : launch_pdl(unpack_kernel<T, VEC, false, ANY>, grid, dim3(THREADS), 0, st, p, deal);
+}
+template <typename T, int VEC, bool ANY>
+cudaError_t either_way(const Rows8Params& p, bool pack, int num_sms, cudaStream_t st) {
+  return pack ? pack_as<T, VEC, ANY>(p, num_sms, st) : unpack_as<T, VEC, ANY>(p, num_sms, st);
 }
 
 template <typename T>
@@ -203,9 +257,9 @@ cudaError_t typed(const Rows8Params& p, bool pack, int num_sms, cudaStream_t st)
            reinterpret_cast<uintptr_t>(X) % bytes == 0 && reinterpret_cast<uintptr_t>(q) % vec == 0;
   };
   constexpr int HALF = 16 / sizeof(T);
-  if (fits(16, 16)) return pack ? pack_as<T, 16>(p, num_sms, st) : unpack_as<T, 16>(p, num_sms, st);
-  if (fits(HALF, 16)) return pack ? pack_as<T, HALF>(p, num_sms, st) : unpack_as<T, HALF>(p, num_sms, st);
-  return pack ? pack_as<T, 1>(p, num_sms, st) : unpack_as<T, 1>(p, num_sms, st);
+  if (fits(16, 16)) return either_way<T, 16, false>(p, pack, num_sms, st);
+  if (fits(HALF, 16)) return either_way<T, HALF, false>(p, pack, num_sms, st);
+  return either_way<T, 32 / sizeof(T), true>(p, pack, num_sms, st);
 }
 
 cudaError_t launch(const Rows8Params& p, bool pack, int num_sms, cudaStream_t st) {

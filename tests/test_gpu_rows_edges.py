@@ -332,3 +332,105 @@ def test_tensors_other_than_planned_are_refused():
         s.product.run(s.y8, s.s, s.W, s.ws, offsets_of([8]), s.D)
     with pytest.raises(ValueError, match="planned without C"):
         s.grad.run(s.q, s.e, s.dD, None, s.dW, s.dW)
+
+
+WIDTHS = [1, 2, 5, 7, 8, 9, 15, 17, 23, 31, 33, 40, 47, 255, 257, 511, 1023, 2047, 2051, 4099, 8191]
+
+
+def framed(shape, dtype, offset):
+    """A tensor from element `offset` of a buffer of 77s, and that buffer."""
+    n = shape[0] * shape[1]
+    buf = torch.full((n + offset + 40,), 77, device="cuda").to(dtype)
+    return buf[offset:offset + n].view(shape), buf
+
+
+def kept(t, buf, offset):
+    """Whether the buffer around the tensor is as it was."""
+    return bool((buf[:offset] == 77).all()) and bool((buf[offset + t.numel():] == 77).all())
+
+
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,offset", [(1, 0), (2, 3), (9, 1), (40, 6)])
+def test_rows8_of_any_width(H, dtype, T, offset):
+    X, _ = framed((T, H), dtype, offset)
+    X.copy_(rnd((T, H), dtype, H, 3.0))
+    q, qbuf = framed((T, H), torch.int8, offset + 5)
+    back, bbuf = framed((T, H), dtype, offset + 1)
+    E = torch.empty((T, -(-H // 32)), dtype=torch.uint8, device="cuda")
+    q_ref, e_ref, v_ref = (t.cuda() for t in blocks_ref(X))
+    op = pkg.Rows8.like(X, q, E)
+    op.pack(X, q, E)
+    assert torch.equal(q, q_ref) and torch.equal(E, e_ref) and kept(q, qbuf, offset + 5)
+    op2 = pkg.Rows8.like(back, q, E)
+    op2.unpack(q, E, back)
+    assert torch.equal(back.double(), v_ref) and kept(back, bbuf, offset + 1)
+    s = torch.empty(T, device="cuda")
+    op3 = pkg.Rows8.like(X, q, s)
+    op3.pack(X, q, s)
+    top = X.double().abs().amax(1)
+    # two roundings of a scale; five of a ratio of at most 127
+    near(s, top / 127, 2 * U * top / 127)
+    ratio = 127 * X.double() / top[:, None]
+    assert float((q.double() - ratio).abs().max()) <= 0.5 + 127 * 6 * U
+    assert kept(q, qbuf, offset + 5)
+    for o in (op, op2, op3):
+        done(o)
+
+
+@pytest.mark.parametrize("H", WIDTHS + [16385, 33333])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,offset", [(1, 0), (3, 5), (50, 1)])
+@pytest.mark.parametrize("in_8_bits", [False, True])
+def test_norm_of_any_width(H, dtype, T, offset, in_8_bits):
+    """Forward and backward, h over x and dx over dresidual."""
+    x, xbuf = framed((T, H), dtype, offset)
+    x.copy_(rnd((T, H), dtype, 1, 2.0))
+    res, _ = framed((T, H), dtype, offset + 2)
+    res.copy_(rnd((T, H), dtype, 2))
+    w = rnd((H,), dtype, 3)
+    y, ybuf = framed((T, H), dtype, offset + 3)
+    rstd, dw = torch.empty(T, device="cuda"), torch.empty(H, device="cuda")
+    h_ref, r_ref, y_ref = norm_ref(x, res, w)
+    op = pkg.RmsNorm.like(x, w, y, residual=res, h=x, eps=EPS)
+    op.run(x, w, y, residual=res, h=x, rstd=rstd)
+    assert torch.equal(x, h_ref) and kept(x, xbuf, offset) and kept(y, ybuf, offset + 3)
+    near(rstd, r_ref, (H + 5) * U * r_ref)
+    near(y, y_ref, (H + 8) * U * y_ref.abs())
+    dy = rnd((T, H), dtype, 4)
+    dx, dbuf = framed((T, H), dtype, offset + 1)
+    dx.copy_(rnd((T, H), dtype, 5))
+    dres = dx.clone()
+    if in_8_bits:
+        q, e, h = held(T, H, 7)
+        q8, _ = framed((T, H), torch.int8, offset)
+        q8.copy_(q)
+        op.backward(dy, q8, w, rstd, dx, dw, dresidual=dx, exponents=e)
+    else:
+        h = h_ref
+        op.backward(dy, x, w, rstd, dx, dw, dresidual=dx)
+    dx_ref, size, dw_ref, dw_size = backward_ref(dy, h, w, rstd, dres)
+    near(dx, dx_ref, (H + 12) * U * size, "dx")
+    near(dw, dw_ref, (T + 4) * U * dw_size, "dweight")
+    assert kept(dx, dbuf, offset + 1)
+    done(op)
+
+
+@pytest.mark.parametrize("H", [7, 257, 1001, 16385])
+def test_norm_to_8_bits_of_any_width(H):
+    T, offset = 40, 3
+    x, _ = framed((T, H), F16, offset)
+    x.copy_(rnd((T, H), F16, 1, 2.0))
+    w = rnd((H,), F16, 3)
+    y, ybuf = framed((T, H), torch.int8, offset)
+    s = torch.empty(T, device="cuda")
+    op = pkg.RmsNorm.like(x, w, y, scales=s, eps=EPS)
+    op.run(x, w, y, scales=s)
+    done(op)
+    _, _, y_ref = norm_ref(x, None, w)
+    top = y_ref.abs().amax(1)
+    near(s, top / 127, (H + 9) * U * top / 127)
+    hw = x.double() * w.double()
+    ratio = 127 * hw / hw.abs().amax(1, keepdim=True)
+    assert float((y.double() - ratio).abs().max()) <= 0.5 + 127 * 6 * U
+    assert kept(y, ybuf, offset)
