@@ -747,7 +747,8 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
 // ---------------------------------------------------------------- copies of rows
 // 16 values an item.  A last unit that K ends in is padded with whatever
 // follows: the tensor maps end at K.  Up to two jobs a launch (one after the
-// other they take 3 us more of 4096 x 4096 x 4096).
+// other they take 3 us more of 4096 x 4096 x 4096), and two items a thread, one
+// after the other (four, all in flight: 5 us more of 8192 x 8192 x 8192).
 struct CopyJob {
   const int8_t* src;
   uint8_t* dst;
@@ -759,41 +760,29 @@ struct CopyJob {
 
 template <bool WIDEN>
 __global__ void __launch_bounds__(DEAL_THREADS) i8_copy_kernel(const CopyJob first, const CopyJob second) {
-  constexpr int U = 4;
   const bool two = blockIdx.x >= first.blocks;
   const CopyJob& job = two ? second : first;
   const Items all = block_items(job.rows, job.deal, blockIdx.x - (two ? first.blocks : 0u));
   pdl_wait();
   pdl_trigger();
-  for (uint32_t at0 = threadIdx.x; at0 < all.n; at0 += U * DEAL_THREADS) {
-    uint4 w[U];
-    uint8_t* to[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t at = all.at + at0 + u * DEAL_THREADS, r = divide(at, job.deal.lanes);
-      const long long row = all.row + r;
-      const int k = static_cast<int>(at - r * job.deal.lanes.d) * 16;
-      const int8_t* const from = job.src + row * job.ld_src + k;
-      to[u] = job.dst + (WIDEN ? 2 : 1) * (row * job.ld_dst + k);
-      if (at0 + u * DEAL_THREADS < all.n)
-        w[u] = job.aligned ? *reinterpret_cast<const uint4*>(from) : load16_at(from, min(16, job.cols - k));
+  for (uint32_t at0 = threadIdx.x; at0 < all.n; at0 += DEAL_THREADS) {
+    const uint32_t at = all.at + at0, r = divide(at, job.deal.lanes);
+    const long long row = all.row + r;
+    const int k = static_cast<int>(at - r * job.deal.lanes.d) * 16;
+    const int8_t* const from = job.src + row * job.ld_src + k;
+    const uint4 w = job.aligned ? *reinterpret_cast<const uint4*>(from) : load16_at(from, min(16, job.cols - k));
+    uint4* const to = reinterpret_cast<uint4*>(job.dst + (WIDEN ? 2 : 1) * (row * job.ld_dst + k));
+    if constexpr (WIDEN) {
+      uint4 a, b;
+      widen4(w.x, a.x, a.y);
+      widen4(w.y, a.z, a.w);
+      widen4(w.z, b.x, b.y);
+      widen4(w.w, b.z, b.w);
+      to[0] = a;
+      to[1] = b;
+    } else {
+      to[0] = w;
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (at0 + u * DEAL_THREADS < all.n) {
-        uint4* const d = reinterpret_cast<uint4*>(to[u]);
-        if constexpr (WIDEN) {
-          uint4 a, b;
-          widen4(w[u].x, a.x, a.y);
-          widen4(w[u].y, a.z, a.w);
-          widen4(w[u].z, b.x, b.y);
-          widen4(w[u].w, b.z, b.w);
-          d[0] = a;
-          d[1] = b;
-        } else {
-          d[0] = w[u];
-        }
-      }
   }
 }
 
@@ -808,7 +797,7 @@ CopyJob job_of(const I8Copy& c, int num_sms) {
   j.cols = c.cols;
   j.aligned = c.cols % 16 == 0 && c.ld_src % 16 == 0 && reinterpret_cast<uintptr_t>(c.src) % 16 == 0;
   dim3 grid;
-  j.deal = deal_of(c.rows, (c.cols + 15) / 16, num_sms, grid);
+  j.deal = deal_of(c.rows, (c.cols + 15) / 16, 2, num_sms, grid);
   j.blocks = grid.x;
   return j;
 }

@@ -374,10 +374,10 @@ __device__ __forceinline__ Items block_items(long long T, const Deal& d, uint32_
   return {row, at, min(d.chunk, d.lanes.d - at)};
 }
 
-// Four items a thread, fewer where that leaves SMs without work.  (A part is a
+// `items` a thread, fewer where that leaves SMs without work.  (A part is a
 // multiple of DEAL_THREADS.)
-inline Deal deal_of(long long T, int lanes, int num_sms, dim3& grid) {
-  uint32_t n = 4 * DEAL_THREADS;
+inline Deal deal_of(long long T, int lanes, int items, int num_sms, dim3& grid) {
+  uint32_t n = items * DEAL_THREADS;
   while (n > DEAL_THREADS && T * lanes < 2ll * num_sms * n) n /= 2;
   const uint32_t parts = (lanes + n - 1) / n;
   const int rows = parts > 1 ? 1 : static_cast<int>(n / lanes);

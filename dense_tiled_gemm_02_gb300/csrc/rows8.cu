@@ -1,17 +1,20 @@
 // rows8.cu -- rows to 8 bits and back: blocks of 32 values with a power of two,
 // and whole rows with one fp32 scale.
 //
-// Bound by HBM: 16 values a thread and turn (16-byte accesses on both sides:
-// with 8 of a 16-bit type, 8-byte ones on the 8-bit side, unpacking takes 44
-// instead of 33 us), several turns in flight; two lanes share a block's exponent
-// and find its largest magnitude by a shuffle.  Integers are made and read by
-// additions in the last place and byte permutes, since conversion instructions,
-// at a quarter of the rate, bounded the first form (40 us; 64-bit divisions for
-// an item's row another 5).
+// Bound by HBM: 16 values a thread and turn, 16-byte accesses on both sides
+// (with 8 of a 16-bit type, 8-byte ones on the 8-bit side, unpacking takes 36
+// instead of 34.6 us).  Packing has four turns in flight (two: 36 us instead of
+// 30), unpacking takes two, one after the other (four, two in flight: 34.6 instead
+// of 31.5; all in flight: 40).  Two lanes share a block's exponent and find its
+// largest magnitude by a shuffle.  Integers are made and read by additions in
+// the last place and byte permutes, since conversion instructions, at a quarter
+// of the rate, bounded the first form (40 us; 64-bit divisions for an item's row
+// another 5).
 //
-// Measured (one GB300, 16384 x 4096 bf16, floor 30.1 us each way): block rows 30
-// us and back 33, scaled rows 29 and back 34; 16384 x 4095, whose rows are of any
-// alignment, 57 and 57, 58 and 51 (an access an element: 174 and 137, 94 and 132).
+// Measured (one GB300, 16384 x 4096 bf16, floor 30.1 us each way): block rows 30.4
+// us and back 31.5, scaled rows 30.8 and back 31.2; 16384 x 4095, whose rows are
+// of any alignment, 57 and 53, 59 and 52 (an access an element: 174 and 137, 94
+// and 132).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -90,51 +93,39 @@ __global__ void __launch_bounds__(THREADS)
   const Divisor& lanes = deal.lanes;
   pdl_wait();
   pdl_trigger();
-  constexpr int U = 2;
-  for (uint32_t at0 = threadIdx.x; at0 - (threadIdx.x & 31) < all.n; at0 += U * THREADS) {
-    Vec<int8_t, VEC> q[U];
-    Around<int8_t, VEC> around[ANY ? U : 1];
-    float step[U];
-    T* to[U];
-    int i[U];
-    Range n[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t at = all.at + at0 + u * THREADS, r = divide(at, lanes);
-      const long long row = all.row + r;
-      i[u] = static_cast<int>(at - r * lanes.d) * VEC;
-      n[u] = at0 + u * THREADS < all.n ? elements_at<VEC>(i[u], p.H) : Range{0, 0};
-      to[u] = static_cast<T*>(p.X_out) + row * p.ldx + i[u];
-      if (n[u].to > 0) {
-        const long long from_at = row * p.ldq + i[u];
-        const int8_t* const from = p.q + from_at;
-        if constexpr (ANY)
-          fetch(around[u], from, n[u], inside<VEC>(from_at, p.T, p.ldq, p.H));
-        else
-          q[u] = load_vec<int8_t, VEC>(from);
-        step[u] = BLOCKS ? block_step(static_cast<const uint8_t*>(p.scales)[row * blocks + i[u] / ROW_BLOCK])
-                         : static_cast<const float*>(p.scales)[row];
-      }
+  for (uint32_t at0 = threadIdx.x; at0 - (threadIdx.x & 31) < all.n; at0 += THREADS) {
+    const uint32_t at = all.at + at0, r = divide(at, lanes);
+    const long long row = all.row + r;
+    const int i = static_cast<int>(at - r * lanes.d) * VEC;
+    const Range n = at0 < all.n ? elements_at<VEC>(i, p.H) : Range{0, 0};
+    Vec<int8_t, VEC> q{};
+    Around<int8_t, VEC> around;
+    float step = 0.f;
+    if (n.to > 0) {
+      const long long from_at = row * p.ldq + i;
+      if constexpr (ANY)
+        fetch(around, p.q + from_at, n, inside<VEC>(from_at, p.T, p.ldq, p.H));
+      else
+        q = load_vec<int8_t, VEC>(p.q + from_at);
+      step = BLOCKS ? block_step(static_cast<const uint8_t*>(p.scales)[row * blocks + i / ROW_BLOCK])
+                    : static_cast<const float*>(p.scales)[row];
     }
+    if constexpr (ANY) q = shifted<false>(around, n);
+    float v[VEC];
+    integers(q, v);
+    Vec<T, VEC> x;
+    if (step < largest<T>() / 256.f) {  // nothing can round past the finite values
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (ANY || n[u].to > 0) {
-        if constexpr (ANY) q[u] = shifted<false>(around[u], n[u]);
-        float v[VEC];
-        integers(q[u], v);
-        Vec<T, VEC> x;
-        if (step[u] < largest<T>() / 256.f) {  // nothing can round past the finite values
+      for (int j = 0; j < VEC; ++j) narrow(v[j] * step, x.v[j]);
+    } else {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) narrow(v[j] * step[u], x.v[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) narrow_finite(v[j] * step[u], x.v[j]);
-        }
-        if constexpr (ANY)
-          store_shifted<false>(to[u], i[u], n[u], x);
-        else
-          store_vec(to[u], x);
-      }
+      for (int j = 0; j < VEC; ++j) narrow_finite(v[j] * step, x.v[j]);
+    }
+    T* const to = static_cast<T*>(p.X_out) + row * p.ldx + i;
+    if constexpr (ANY)
+      store_shifted<false>(to, i, n, x);
+    else if (n.to > 0)
+      store_vec(to, x);
   }
 }
 
@@ -216,7 +207,7 @@ cudaError_t pack_as(const Rows8Params& p, int num_sms, cudaStream_t st) {
   if (p.block) {
     const int lanes = (p.H + ROW_BLOCK - 1) / ROW_BLOCK * (ROW_BLOCK / VEC);
     dim3 grid;
-    const Deal deal = deal_of(p.T, lanes, num_sms, grid);
+    const Deal deal = deal_of(p.T, lanes, 4, num_sms, grid);
     return launch_pdl(pack_blocks_kernel<T, VEC, ANY>, grid, dim3(THREADS), 0, st, p, deal);
   }
   // few rows are spread over more threads
@@ -238,7 +229,7 @@ template <typename T, int VEC, bool ANY>
 cudaError_t unpack_as(const Rows8Params& p, int num_sms, cudaStream_t st) {
   const int lanes = (p.H + VEC - 1) / VEC;
   dim3 grid;
-  const Deal deal = deal_of(p.T, lanes, num_sms, grid);
+  const Deal deal = deal_of(p.T, lanes, 2, num_sms, grid);
   return p.block ? launch_pdl(unpack_kernel<T, VEC, true, ANY>, grid, dim3(THREADS), 0, st, p, deal)
                  : launch_pdl(unpack_kernel<T, VEC, false, ANY>, grid, dim3(THREADS), 0, st, p, deal);
 }
