@@ -83,7 +83,9 @@ struct Cfg {
 };
 
 // ---------------------------------------------------------------- kernel
-// SCALED (rows form, no C): D[r, f] times x_scales[r] and the expert's w_scales[f].
+// SCALED (rows form, no C): D[r, f] times x_scales[r] and the expert's w_scales[f],
+// two multiplications of the fp32 sums on their way to the store (8192 x 8192 x
+// 8192 548 us, as without).
 template <int CG, int QT, int STAGES, int DT, bool SCALED>
 __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmX128,

@@ -20,7 +20,23 @@
 // goes with it, so that the converters, who see the stage filled, know the slot
 // free.  The converters' way through a stage is a chain of latencies (wait,
 // load, convert, store, wait, arrive: about 600 cycles of which the instructions
-// are a third), so two groups of warps take the stages in turn.
+// are a third), so two groups of warps take the stages in turn.  A third group, no
+// loads from shared memory at all, halves of a stage a group and waits that spin
+// changed the time by less than a twentieth.
+//
+// Fewer tiles than SMs: clusters of 2 to 8 CTAs take a tile each, a part of K a
+// CTA, and add up through distributed shared memory.
+//
+// Measured (one GB300, us, the floor in brackets; X's widening included): 64 x
+// 8192 x 8192 20.5 (10.3), 64 x 4096 x 4096 11.6 (2.6), 512 x 8192 x 8192 55 (35),
+// 2048 x 8192 x 8192 185 (141), 1024 rows over 40 of 64 experts of 4096 x 2048 74
+// (51).  What bounds it: with few rows the two launches, the first loads and the
+// join (9 us around 11.5 of streaming); with many the converters (0.7-0.8 of the
+// tensor rate).  From 6144 rows an expert both operands are widened in HBM and go
+// through grouped.cu's pairs instead: 8192 x 8192 x 8192 609-626 (564) against 711.
+// Not faster: X widened here as well (64 x 8192 x 8192 27 by the converters, 38 by
+// the epilogue's warps); CTA pairs with the weights in tensor memory (8192^3 911,
+// an arrival on the other CTA's barrier takes several times a local one's time).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

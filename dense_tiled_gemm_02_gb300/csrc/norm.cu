@@ -4,10 +4,17 @@
 //   h = x + residual,  r = 1 / sqrt(mean h^2 + eps),  y = h r w
 //   dx = r (w dy - h r^2 / H sum(w dy h)) + dresidual,  dw = sum over rows of dy h r
 //
-// Bound by HBM: each row is read once and stays in its threads' registers.
-// The 8-bit form needs the largest |y| too, which is r max |h w|: known with
-// the sum of squares, so that one reduction serves both, and r falls out of the
-// integers y / scale = 127 h w / max |h w|.
+// Bound by HBM: each row is read once and stays in its threads' registers (the
+// gradients': in shared memory).  The 8-bit form needs the largest |y| too, which
+// is r max |h w|: known with the sum of squares, so that one reduction serves
+// both, and r falls out of the integers y / scale = 127 h w / max |h w|.
+//
+// Measured (one GB300, 16384 x 4096 bf16 with a residual, us, the floor in
+// brackets): 79 (80.3), to 8 bits 81 (70.3); the gradients 91 (80.3), from block
+// rows 89 (70.6) of which 3 are the last sum of dweight.  A row's gradients held
+// in registers between the passes, without the ring, 170 from block rows: a block
+// that waits for its row's sum has nothing in flight.  16 x 4096 to 8 bits: 2.5
+// in a graph; a call's host side takes 5.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -404,8 +404,11 @@ GEMM_API int gemm_trace_set(gemm_handle_t h, uint64_t* dev_buf);
  * operator or of another device than the current one),
  * GEMM_ERR_MISALIGNED or GEMM_ERR_CUDA.
  *
- * GEMM_FORCE_PLAN (read by the create calls, for tests and tuning) takes one
- * more key: wide=0|1, the grouped product's single CTAs or CTA pairs.
+ * GEMM_FORCE_PLAN (read by the create calls, for tests and tuning) takes more
+ * keys: wide=0|1, the grouped product's single CTAs or CTA pairs, and the 8-bit
+ * product's form of widened operands; tiles=0|1 (its form for few rows or its
+ * tiles), tall=0|1 (tiles of 64 or 128 rows), csk=0 (no clusters that share a
+ * tile).
  *
  * Experts are numbered 0 .. E-1, E <= GEMM_MAX_EXPERTS.  Rows sorted by
  * expert are described by `offsets`, E + 1 int32 values in device memory:
@@ -424,7 +427,8 @@ typedef struct gemm_op* gemm_op_t;
 
 /* gemm_op_status: synchronise stream, then return and clear the handle's
  * device status word: GEMM_OK, GEMM_ERR_DEVICE_TIMEOUT (a bounded device-side
- * wait of a grouped product expired) or GEMM_ERR_INVALID_ARG (offsets or row
+ * wait of a grouped product, of an 8-bit product or of a norm's backward pass
+ * expired) or GEMM_ERR_INVALID_ARG (offsets or row
  * indices out of range); GEMM_ERR_CUDA if the synchronisation fails.  After a
  * timeout the outputs of the handle's calls are undefined until this has
  * reported it. */
@@ -441,8 +445,8 @@ GEMM_API int64_t gemm_op_workspace_bytes(gemm_op_t op);
  * full length. */
 GEMM_API int gemm_op_plan_string(gemm_op_t op, char* buf, size_t n);
 
-/* gemm_op_debug_set: the test hook of gemm_debug_set, for the grouped
- * product's ring (the other operators wait for nothing and ignore it).
+/* gemm_op_debug_set: the test hook of gemm_debug_set, for the rings of the
+ * grouped products and of the 8-bit products' tiles (the others ignore it).
  * GEMM_DEBUG_SKIP_ONE_FILL: only the first CTA or CTA pair of the next run
  * leaves its first stage unfilled. */
 #define GEMM_DEBUG_SKIP_ONE_FILL 2
@@ -673,10 +677,11 @@ GEMM_API int gemm_rows8_grad_run(gemm_op_t op, const int8_t* q, const uint8_t* E
  * offsets may be NULL (all R rows); otherwise they group the rows as above,
  * and rows of no expert are not written.  W is 16-byte aligned where ldw is a
  * multiple of 16 (else GEMM_ERR_MISALIGNED); other rows of W, when there are
- * more than a few of X, are copied to aligned ones on each call.  The sums are
- * exact as long as they stay below 2^24 (always up to K = 1024), and beyond that off by at most
- * K * 2^-24 of the sum of magnitudes; scaled in fp32 and rounded once.
- * K < 2^17.
+ * more than a few of X, are copied to aligned ones on each call.  The handle's
+ * workspace holds X in fp16, and for many rows W too (2 bytes a weight).  The
+ * sums are exact as long as they stay below 2^24 (always up to K = 1024), and
+ * beyond that off by at most K * 2^-24 of the sum of magnitudes; scaled in fp32
+ * and rounded once.  K < 2^17.
  */
 typedef struct {
   int32_t E;
