@@ -667,8 +667,15 @@ cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t st) {
                             : forward_typed<__half>(p, num_sms, st);
 }
 
-int norm_partial_rows(long long T, int num_sms) {
-  return static_cast<int>(std::min<long long>(T, static_cast<long long>(num_sms) * BACKWARD_BLOCKS));
+int norm_partial_rows(long long T, int H, int type, int num_sms) {
+  int nv;
+  const int threads = type == T_F32 ? ring_threads<float>(H, nv) : ring_threads<__half>(H, nv);
+  const int sums = nv * (type == T_F32 ? 4 : 8);
+  int blocks = 2;  // rows too long for the ring
+  if (threads > 0)
+    for (const bool any : {false, true})
+      blocks = std::max(blocks, std::min(BACKWARD_BLOCKS, ring_room(any, nv, sums) / threads));
+  return static_cast<int>(std::min<long long>(T, static_cast<long long>(num_sms) * blocks));
 }
 
 cudaError_t launch_norm_backward(const NormBackwardParams& p, int num_sms, cudaStream_t st) {

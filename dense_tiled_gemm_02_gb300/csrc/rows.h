@@ -44,8 +44,9 @@ struct NormBackwardParams {
   float* partial;     // norm_partial_rows() x H
   uint32_t* status;
 };
-// Blocks of the backward kernel, each of which leaves a row of partial sums of dweight.
-int norm_partial_rows(long long T, int num_sms);
+// Blocks of the backward kernel, at most, each of which leaves a row of partial
+// sums of dweight.
+int norm_partial_rows(long long T, int H, int type, int num_sms);
 cudaError_t launch_norm_backward(const NormBackwardParams& p, int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- rows to 8 bits (rows8.cu)

@@ -46,7 +46,10 @@ int gemm_norm_create(gemm_op_t* out, const gemm_norm_desc_t* desc) {
   cudaGetLastError();
   // partial sums of dweight; a norm out in 8 bits has no backward pass
   const size_t partial =
-      d.y_type == GEMM_I8 ? 0 : sizeof(float) * norm_partial_rows(d.T, std::max(sms, 1)) * static_cast<size_t>(d.H);
+      d.y_type == GEMM_I8
+          ? 0
+          : sizeof(float) * static_cast<size_t>(d.H) *
+                norm_partial_rows(d.T, static_cast<int>(d.H), d.type, std::max(sms, 1));
   gemm_op* op = nullptr;
   const int rc = make_op(Kind::kNorm, partial, 0, 0, &op);
   if (rc != GEMM_OK) return rc;

@@ -434,3 +434,26 @@ def test_norm_to_8_bits_of_any_width(H):
     ratio = 127 * hw / hw.abs().amax(1, keepdim=True)
     assert float((y.double() - ratio).abs().max()) <= 0.5 + 127 * 6 * U
     assert kept(y, ybuf, offset)
+
+
+@pytest.mark.parametrize("H", [64, 1024, 1028, 2048, 4096, 8192, 8200, 16384, 16392])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_norm_backward_of_as_many_rows_as_blocks_take(H, dtype, offset):
+    """More rows than blocks, so that every block's partial sums are in use, and
+    those of a handle beside it stay what they are."""
+    T = 2000
+    x, _ = framed((T, H), dtype, offset)
+    x.copy_(rnd((T, H), dtype, 1))
+    w, dy = rnd((H,), dtype, 2), rnd((T, H), dtype, 3)
+    rstd = rnd((T,), F32, 4).abs() + 0.5
+    dx, dw, dw2 = torch.empty_like(dy), torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+    ops = [pkg.RmsNorm.like(x, w, torch.empty_like(x), eps=EPS) for _ in range(2)]
+    ops[0].backward(dy, x, w, rstd, dx, dw)
+    ops[1].backward(dy, x, w, rstd, dx, dw2)
+    for o in ops:
+        done(o)
+    dx_ref, size, dw_ref, dw_size = backward_ref(dy, x, w, rstd, None)
+    near(dx, dx_ref, (H + 12) * U * size, "dx")
+    near(dw, dw_ref, (T + 4) * U * dw_size, "dweight")
+    assert torch.equal(dw, dw2)
