@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
       if (i < p.H) row_sums<T, VEC, I8, ANY, KEEP>(p, h[0], i, sum, top, kept[0]);
     }
   }
-  row_reduce<I8>(sum, top, warps, part);
+  row_reduce<true, I8>(sum, top, warps, part);
   const float r = 1.f / sqrtf(sum / static_cast<float>(p.H) + p.eps);
   const RowScale q = I8 ? row_scale(__uint_as_float(top), r) : RowScale{};
   if (threadIdx.x == 0) {
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardPa
         if (p.dweight && (!ANY || i + j < p.H)) mine[i + j] = fmaf(t, r, mine[i + j]);
       }
     }
-    row_reduce<false>(sum, top, warps, part[turn]);
+    row_reduce<true, false>(sum, top, warps, part[turn]);
     const float c = r * r * (sum / static_cast<float>(p.H));
     for (int i = first, i0 = warp_first; i0 < p.H; i += step, i0 += step) {
       Vec<T, VEC> res{};
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
         }
       }
     if (warps == 1) __syncwarp();
-    row_reduce<false>(sum, top, warps, part[turn]);
+    row_reduce<true, false>(sum, top, warps, part[turn]);
     if (*const_cast<volatile int*>(&abort_flag)) break;
     // every thread is past its second pass over the previous row: its stage
     // takes the row after those under way
@@ -589,15 +589,22 @@ bool ring_shape(int64_t stage_bytes, int threads, int room, int& blocks, int& st
   return false;
 }
 
-template <typename T, int NV, bool HELD, bool ANY>
-cudaError_t launch_ring(const NormBackwardParams& p, int threads, int blocks, int stages,
-                        int stage_bytes, cudaStream_t st) {
-  auto* const kernel = norm_backward_ring_kernel<T, NV, HELD, ANY>;
-  const int bytes = stages * stage_bytes;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(blocks), dim3(threads), bytes, st, p, stages);
+// What a launch of the ring kernels needs once, for rows of H elements.
+template <typename T, int NV>
+cudaError_t allow_ring() {
+  for (auto* const kernel : {norm_backward_ring_kernel<T, NV, false, false>, norm_backward_ring_kernel<T, NV, false, true>,
+                             norm_backward_ring_kernel<T, NV, true, false>, norm_backward_ring_kernel<T, NV, true, true>}) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+template <typename T>
+cudaError_t prepare_typed(int H) {
+  int nv;
+  if (ring_threads<T>(H, nv) == 0) return cudaSuccess;
+  return nv == 1 ? allow_ring<T, 1>() : nv == 2 ? allow_ring<T, 2>() : allow_ring<T, 4>();
 }
 
 template <typename T, bool HELD, bool ANY>
@@ -613,9 +620,11 @@ cudaError_t launch_backward(const NormBackwardParams& p, int num_sms, int& block
   };
   if (threads > 0 && ring_shape(stage_bytes, threads, ring_room(ANY, nv, nv * 16 / S), per_sm, stages)) {
     blocks = blocks_of(per_sm);
-    return nv == 1   ? launch_ring<T, 1, HELD, ANY>(p, threads, blocks, stages, static_cast<int>(stage_bytes), st)
-           : nv == 2 ? launch_ring<T, 2, HELD, ANY>(p, threads, blocks, stages, static_cast<int>(stage_bytes), st)
-                     : launch_ring<T, 4, HELD, ANY>(p, threads, blocks, stages, static_cast<int>(stage_bytes), st);
+    auto* const kernel = nv == 1   ? norm_backward_ring_kernel<T, 1, HELD, ANY>
+                         : nv == 2 ? norm_backward_ring_kernel<T, 2, HELD, ANY>
+                                   : norm_backward_ring_kernel<T, 4, HELD, ANY>;
+    return launch_pdl(kernel, dim3(blocks), dim3(threads), stages * static_cast<size_t>(stage_bytes), st, p,
+                      stages);
   }
   blocks = blocks_of(2);
   return launch_pdl(norm_backward_kernel<T, 16 / S, HELD, ANY>, dim3(blocks), dim3(512), 0, st, p);
@@ -665,6 +674,12 @@ cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t st) {
   return p.type == T_F32    ? forward_typed<float>(p, num_sms, st)
          : p.type == T_BF16 ? forward_typed<__nv_bfloat16>(p, num_sms, st)
                             : forward_typed<__half>(p, num_sms, st);
+}
+
+cudaError_t prepare_norm_backward(int H, int type) {
+  return type == T_F32    ? prepare_typed<float>(H)
+         : type == T_BF16 ? prepare_typed<__nv_bfloat16>(H)
+                          : prepare_typed<__half>(H);
 }
 
 int norm_partial_rows(long long T, int H, int type, int num_sms) {

@@ -66,6 +66,7 @@ struct gemm_op {
   bool wide = false;
   bool tiles = false;  // i8: on the tensor cores (wide, or tiles of tile_rows rows)
   int tile_rows = 0, split = 1;
+  CUtensorMap map_x{}, map_x32{}, map_w{};  // i8: of the workspace's operands
   int units = 0;
   int grid = 0;  // route: blocks
   gemm_op* inner = nullptr;  // rows8_grad: the grouped product it ends in

@@ -199,15 +199,15 @@ __device__ __forceinline__ void narrow_finite(float v, T& x) {
 // which fmaxf would let pass.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Sum and (TOP) largest over the threads of a row: one warp, or `warps` of them
+// (SUM) sum and (TOP) largest over the threads of a row: one warp, or `warps` of them
 // with the partial results in `part`, which no later call may still be reading:
 // callers take two in turn.  In a fixed order, and the same in every thread.
-template <bool TOP = true>
+template <bool SUM, bool TOP>
 __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int warps, float2* part) {
   auto over_warp = [&] {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      if constexpr (SUM) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
       if constexpr (TOP) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     }
   };

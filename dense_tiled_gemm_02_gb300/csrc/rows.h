@@ -47,6 +47,8 @@ struct NormBackwardParams {
 // Blocks of the backward kernel, at most, each of which leaves a row of partial
 // sums of dweight.
 int norm_partial_rows(long long T, int H, int type, int num_sms);
+// Once, before any of the launches.
+cudaError_t prepare_norm_backward(int H, int type);
 cudaError_t launch_norm_backward(const NormBackwardParams& p, int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- rows to 8 bits (rows8.cu)

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(1024) pack_rows_kernel(const Rows8Params p) {
       top = max(top, vec_top(x[0]));
     }
   }
-  row_reduce(sum, top, blockDim.x >> 5, part);
+  row_reduce<false, true>(sum, top, blockDim.x >> 5, part);
   const RowScale s = row_scale(__uint_as_float(top), 1.f);
   if (threadIdx.x == 0) static_cast<float*>(p.scales_out)[row] = s.scale;
   auto store = [&](const Vec<T, VEC>& v, int i) {

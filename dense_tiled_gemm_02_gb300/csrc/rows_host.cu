@@ -53,6 +53,11 @@ int gemm_norm_create(gemm_op_t* out, const gemm_norm_desc_t* desc) {
   gemm_op* op = nullptr;
   const int rc = make_op(Kind::kNorm, partial, 0, 0, &op);
   if (rc != GEMM_OK) return rc;
+  if (d.y_type != GEMM_I8 && prepare_norm_backward(static_cast<int>(d.H), d.type) != cudaSuccess) {
+    cudaGetLastError();
+    gemm_op_destroy(op);
+    return GEMM_ERR_CUDA;
+  }
   op->norm = d;
   std::snprintf(op->plan, sizeof op->plan, "norm T=%lld H=%lld residual=%d out=%s",
                 static_cast<long long>(d.T), static_cast<long long>(d.H), d.residual,
@@ -339,6 +344,17 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
       return GEMM_ERR_CUDA;
     }
   }
+  if (tiles) {
+    uint8_t* const ws = static_cast<uint8_t*>(op->ws);
+    const int64_t w_rows = d.E * d.N;
+    if (!encode_rows(&op->map_x, ws, ws_ldx, d.K, d.R, 0, BK, wide ? 128 : rows) ||
+        !encode_rows(&op->map_x32, ws, ws_ldx, d.K, d.R, 0, BK, 32) ||
+        (wide && !encode_rows(&op->map_w, ws + x_bytes, ws_ldw, d.K, w_rows, 0, BK, 128)) ||
+        (copy_w && !wide && !encode_bytes(&op->map_w, ws + x_bytes, ws_ldw, d.K, w_rows))) {
+      gemm_op_destroy(op);
+      return GEMM_ERR_CUDA;
+    }
+  }
   op->tiles = tiles;
   op->wide = wide;
   op->tile_rows = rows;
@@ -369,19 +385,14 @@ int run_i8_tiles(gemm_op_t op, const int8_t* X, const float* x_scales, const int
   const int K = static_cast<int>(d.K);
   const int64_t w_rows = d.E * d.N;
   uint8_t* const ws = static_cast<uint8_t*>(op->ws);
-  uint16_t* const wx = reinterpret_cast<uint16_t*>(ws);
-  const void* w = op->copy_b ? ws + op->ws_b_off : static_cast<const void*>(W);
-  const I8Copy copy_x = {X, d.ldx, wx, op->ws_lda, d.R, K};
+  const I8Copy copy_x = {X, d.ldx, ws, op->ws_lda, d.R, K};
   const I8Copy copy_w = {W, d.ldw, ws + op->ws_b_off, op->ws_ldb, w_rows, K};
   int rc = launched(launch_i8_widen(copy_x, wide ? copy_w : I8Copy{}, op->num_sms, st));
   if (rc == GEMM_OK && op->copy_b && !wide) rc = launched(launch_i8_copy(copy_w, op->num_sms, st));
   if (rc != GEMM_OK) return rc;
-  CUtensorMap wm{}, x{}, x32{}, dm{};
-  if (!(wide ? encode_rows(&wm, w, op->ws_ldb, d.K, w_rows, 0, BK, 128)
-             : encode_bytes(&wm, w, op->ws_ldb, d.K, w_rows)) ||
-      !encode_rows(&x, wx, op->ws_lda, d.K, d.R, 0, BK, wide ? 128 : op->tile_rows) ||
-      !encode_rows(&x32, wx, op->ws_lda, d.K, d.R, 0, BK, 32))
-    return GEMM_ERR_CUDA;
+  // (the maps of what the caller owns; the others are the handle's)
+  CUtensorMap wm{}, dm{};
+  if (!op->copy_b && !encode_bytes(&wm, W, op->ws_ldb, d.K, w_rows)) return GEMM_ERR_CUDA;
   GroupedParams p{};
   p.E = d.E;
   p.R = static_cast<int>(d.R);
@@ -391,7 +402,7 @@ int run_i8_tiles(gemm_op_t op, const int8_t* X, const float* x_scales, const int
   p.offsets = offsets;
   p.d_type = d.d_type;
   p.d_vec = is_16bit(d.d_type) && d.ldd % 8 == 0 && aligned(D, 16);
-  p.d_tma = p.d_vec && d.N % 8 == 0;
+  p.d_tma = p.d_vec && d.N % 8 == 0 && op->split == 1;  // (clusters' threads store)
   if (p.d_tma && !encode_rows(&dm, D, d.ldd, d.N, d.R, 1, 64, 32)) return GEMM_ERR_CUDA;
   p.ldd = d.ldd;
   p.D = D;
@@ -403,8 +414,10 @@ int run_i8_tiles(gemm_op_t op, const int8_t* X, const float* x_scales, const int
   op->debug_flags = 0;
   p.x_scales = x_scales;
   p.w_scales = w_scales;
-  return launched(wide ? launch_scaled(wm, x, x32, dm, p, op->units, st)
-                       : launch_i8_tiles(op->tile_rows, wm, x, x32, dm, p, op->units, op->split, st));
+  const CUtensorMap& w = op->copy_b ? op->map_w : wm;
+  return launched(wide ? launch_scaled(w, op->map_x, op->map_x32, dm, p, op->units, st)
+                       : launch_i8_tiles(op->tile_rows, w, op->map_x, op->map_x32, dm, p, op->units,
+                                         op->split, st));
 }
 
 }  // namespace
