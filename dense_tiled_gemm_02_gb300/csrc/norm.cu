@@ -79,8 +79,10 @@ using WordsOf = std::conditional_t<ANY, Around<T, VEC>, Vec<T, VEC>>;
 
 template <typename T, int VEC>
 __device__ __forceinline__ void add_residual(Vec<T, VEC>& h, const Vec<T, VEC>& r) {
+  float v[VEC];
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) narrow(widen(h.v[j]) + widen(r.v[j]), h.v[j]);
+  for (int j = 0; j < VEC; ++j) v[j] = widen(h.v[j]) + widen(r.v[j]);
+  h = narrowed<T, VEC>(v);
 }
 
 template <typename T, int VEC, bool ANY>
@@ -102,10 +104,10 @@ __device__ __forceinline__ void store_y(const NormParams& p, long long row, cons
     for (int j = 0; j < VEC; ++j) v[j] = KEEP ? kept[j] : widen(h.v[j]) * w[j];
     store_row<int8_t, VEC, ANY>(static_cast<int8_t*>(p.y) + row * p.ldy + i, i, p.H, row_integers(v, q));
   } else {
-    Vec<T, VEC> y;
+    float v[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) narrow(widen(h.v[j]) * r * (KEEP ? kept[j] : w[j]), y.v[j]);
-    store_row<T, VEC, ANY>(static_cast<T*>(p.y) + row * p.ldy + i, i, p.H, y);
+    for (int j = 0; j < VEC; ++j) v[j] = widen(h.v[j]) * r * (KEEP ? kept[j] : w[j]);
+    store_row<T, VEC, ANY>(static_cast<T*>(p.y) + row * p.ldy + i, i, p.H, narrowed<T, VEC>(v));
   }
 }
 
@@ -230,14 +232,13 @@ template <typename T, int VEC>
 __device__ __forceinline__ Vec<T, VEC> dx_of(const float (&dy)[VEC], const float (&h)[VEC],
                                              const float (&w)[VEC], float r, float c,
                                              const Vec<T, VEC>& res, bool residual) {
-  Vec<T, VEC> o;
+  float v[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
-    float v = r * (dy[j] * w[j] - h[j] * c);
-    if (residual) v += widen(res.v[j]);
-    narrow(v, o.v[j]);
+    v[j] = r * (dy[j] * w[j] - h[j] * c);
+    if (residual) v[j] += widen(res.v[j]);
   }
-  return o;
+  return narrowed<T, VEC>(v);
 }
 
 // Threads of an SM that the ring kernels' registers are for: by the sums of
@@ -260,8 +261,7 @@ __device__ __forceinline__ void widen_h(const Vec<T, VEC>& v, float, float (&h)[
 }
 template <int VEC>
 __device__ __forceinline__ void widen_h(const Vec<int8_t, VEC>& v, float step, float (&h)[VEC]) {
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) h[j] = fmaf(from_byte(v, j), step, step * -BYTE_BIAS);
+  times_step<true>(v, step, h);
 }
 
 // Rows too long for the kernel below.  Blocks take rows in turn and read each
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardPa
       }
     }
     row_reduce<true, false>(sum, top, warps, part[turn]);
-    const float c = r * r * (sum / static_cast<float>(p.H));
+    const float c = r * (r * (sum / static_cast<float>(p.H)));  // (r r may underflow)
     for (int i = first, i0 = warp_first; i0 < p.H; i += step, i0 += step) {
       Vec<T, VEC> res{};
       if (i < p.H) {
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
       const long long next = row + static_cast<long long>(stages - 1) * gridDim.x;
       if (next < p.T) load_row(next, s == 0 ? stages - 1 : s - 1);
     }
-    const float c = r * r * (sum / static_cast<float>(p.H));
+    const float c = r * (r * (sum / static_cast<float>(p.H)));  // (r r may underflow)
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = first + k * step;

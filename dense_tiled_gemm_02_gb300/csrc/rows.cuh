@@ -187,12 +187,33 @@ __device__ __forceinline__ float largest() {
   return __uint_as_float(0x7F7FFFFFu);
 }
 
-// Rounded to T; what is beyond the finite values becomes the largest of them,
-// NaN stays (no comparison with it holds).
-template <typename T>
-__device__ __forceinline__ void narrow_finite(float v, T& x) {
-  if (fabsf(v) > largest<T>()) v = copysignf(largest<T>(), v);
-  narrow(v, x);
+// What is beyond the finite values becomes the largest of them, NaN stays (no
+// comparison with it holds).
+__device__ __forceinline__ float finite(float v, float most) {
+  return fabsf(v) > most ? copysignf(most, v) : v;
+}
+
+// Rounded to T, two at a time: one instruction for both, and no byte permutes to
+// put them together.
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> narrowed(const float (&v)[VEC]) {
+  Vec<T, VEC> o;
+  if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o.v[j] = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) {
+      if constexpr (std::is_same_v<T, __half>) {
+        const __half2 p = __floats2half2_rn(v[j], v[j + 1]);
+        memcpy(&o.v[j], &p, 4);
+      } else {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v[j], v[j + 1]);
+        memcpy(&o.v[j], &p, 4);
+      }
+    }
+  }
+  return o;
 }
 
 // Magnitudes are compared as integers: NaN then counts as above infinity,
@@ -276,13 +297,6 @@ __device__ __forceinline__ float from_byte(const Vec<int8_t, VEC>& v, int j) {
 }
 constexpr float BYTE_BIAS = 8388736.f;
 
-// The integers of a vector.
-template <int VEC>
-__device__ __forceinline__ void integers(const Vec<int8_t, VEC>& q, float (&o)[VEC]) {
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) o[j] = from_byte(q, j) - BYTE_BIAS;
-}
-
 // ---------------------------------------------------------------- scaled rows
 // From the largest magnitude of a row: v * pre * inv are its integers, and
 // scale * integer its values times `unit`.  Where 127 / top would overflow, v
@@ -327,6 +341,19 @@ __device__ __forceinline__ float block_step(uint32_t e) {
 }
 __device__ __forceinline__ float block_inverse(uint32_t e) {
   return e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
+}
+// The integers of a vector times step.  POWER: a power of two (or NaN), of which
+// the bias is an exact multiple, so that one operation does it; where that is finite.
+template <bool POWER, int VEC>
+__device__ __forceinline__ void times_step(const Vec<int8_t, VEC>& q, float step, float (&o)[VEC]) {
+  if (POWER && step < 0x1p100f) {
+    const float bias = step * -BYTE_BIAS;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] = fmaf(from_byte(q, j), step, bias);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] = (from_byte(q, j) - BYTE_BIAS) * step;
+  }
 }
 template <int VEC>
 __device__ __forceinline__ Vec<int8_t, VEC> block_integers(const float (&v)[VEC], float inverse) {

@@ -112,15 +112,12 @@ __global__ void __launch_bounds__(THREADS)
     }
     if constexpr (ANY) q = shifted<false>(around, n);
     float v[VEC];
-    integers(q, v);
-    Vec<T, VEC> x;
-    if (step < largest<T>() / 256.f) {  // nothing can round past the finite values
+    times_step<BLOCKS>(q, step, v);
+    if (!(step < largest<T>() / 256.f)) {  // else nothing can round past the finite values
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) narrow(v[j] * step, x.v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) narrow_finite(v[j] * step, x.v[j]);
+      for (int j = 0; j < VEC; ++j) v[j] = finite(v[j], largest<T>());
     }
+    const Vec<T, VEC> x = narrowed<T, VEC>(v);
     T* const to = static_cast<T*>(p.X_out) + row * p.ldx + i;
     if constexpr (ANY)
       store_shifted<false>(to, i, n, x);

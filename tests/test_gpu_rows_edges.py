@@ -457,3 +457,32 @@ def test_norm_backward_of_as_many_rows_as_blocks_take(H, dtype, offset):
     near(dx, dx_ref, (H + 12) * U * size, "dx")
     near(dw, dw_ref, (T + 4) * U * dw_size, "dweight")
     assert torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("H", [64, 1001, 1024, 40000])
+@pytest.mark.parametrize("dtype,low,high", [(BF16, 225, 249), (F32, 225, 249), (BF16, 1, 12), (F16, 100, 130)])
+def test_norm_backward_from_steps_at_the_ends_of_the_range(H, dtype, low, high):
+    """Block rows whose exponents lie near the ends: with h r of about 1, as the
+    forward pass leaves it, no intermediate value may leave fp32's range."""
+    T = 5
+    q = ints((T, H), 1, -127, 128)
+    E = ints((T, -(-H // 32)), 2, 0, 4).to(torch.uint8)
+    E += torch.linspace(low, high - 4, T, device="cuda").round().to(torch.uint8)[:, None]
+    h = q.double() * torch.exp2(E.cpu().double() - 127).cuda().repeat_interleave(32, 1)[:, :H]
+    rstd = (1 / torch.sqrt((h * h).mean(1))).float()
+    w, dy = rnd((H,), dtype, 3), rnd((T, H), dtype, 4, 2.0 ** -10)
+    dx, dw = torch.empty_like(dy), torch.empty(H, device="cuda")
+    op = pkg.RmsNorm.like(dy, w, torch.empty_like(dy), eps=EPS)
+    op.backward(dy, q, w, rstd, dx, dw, exponents=E)
+    done(op)
+    dx_ref, size, dw_ref, dw_size = backward_ref(dy, h, w, rstd, None)
+    # (where values are below fp32's normal range, a rounding is 2^-150 instead
+    # of relative: 12 of them, times r at most 2^126 where h is that small)
+    tiny = 12 * 2.0 ** -150 * rstd.double()[:, None].clamp_min(1.0) * (1 + h.abs())
+    inf = torch.finfo(dtype).max
+    fits = dx_ref.abs() < inf
+    near(torch.where(fits, dx, torch.zeros_like(dx)), torch.where(fits, dx_ref, 0.0),
+         torch.where(fits, (H + 12) * U * size + tiny, 0.0), "dx")
+    # a term's dy h may be below the normal range, too: off by at most 2^-150
+    # there, which r then multiplies (of h of about 2^-118 and r of 2^118, 2^-32)
+    near(dw, dw_ref, (T + 4) * U * dw_size + float(rstd.double().sum()) * 2.0 ** -150, "dweight")
