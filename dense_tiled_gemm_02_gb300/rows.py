@@ -22,6 +22,7 @@ from .experts import (_new_zeros, _on_one_device, _Op, _plan_of, _Planned, _row_
                       _stack_stride, _type)
 
 BLOCK = 32  # values that share a power of two
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (none without CUDA)
 
 
 def _blocks(n: int) -> int:
@@ -54,6 +55,10 @@ def _given(plan, t, what: str):
     if (plan is None) != (t is None):
         raise ValueError(f"planned {'without' if plan is None else 'with'} {what}")
     return None if t is None else plan.pointer(t)
+
+
+# The methods that enqueue write out what _Op._call does: handing it the pointers
+# costs a fifteenth of the smallest calls.
 
 
 class RmsNorm(_Op):
@@ -101,11 +106,14 @@ class RmsNorm(_Op):
 
     def run(self, x, weight, y, scales=None, residual=None, h=None, rstd=None, stream=None) -> None:
         """Enqueue the norm; rstd (T fp32), if given, is what `backward` needs."""
-        self._call("gemm_norm_run", stream, self._x.pointer(x),
-                   _given(self._residual, residual, "residual"), self._weight.pointer(weight),
-                   _given(self._h, h, "h"), self._y.pointer(y),
-                   _given(self._scales, scales, "scales"),
-                   None if rstd is None else self._rstd.pointer(rstd))
+        stream = _current(self._index) if stream is None else getattr(stream, "cuda_stream", stream)
+        rc = self._lib.gemm_norm_run(
+            self.handle, self._x.pointer(x), _given(self._residual, residual, "residual"),
+            self._weight.pointer(weight), _given(self._h, h, "h"), self._y.pointer(y),
+            _given(self._scales, scales, "scales"),
+            None if rstd is None else self._rstd.pointer(rstd), stream)
+        if rc != _gemm.GEMM_OK:
+            raise _gemm.GemmError(rc, "gemm_norm_run")
 
     def backward(self, dy, h, weight, rstd, dx, dweight=None, dresidual=None, exponents=None,
                  stream=None) -> None:
@@ -115,13 +123,16 @@ class RmsNorm(_Op):
         if self._scales is not None:
             raise ValueError("planned for an int8 y, which has no gradient")
         rows = (self._h8 if exponents is not None else self._x if self._h is None else self._h)
-        self._call("gemm_norm_backward", stream, self._y.pointer(dy), rows.pointer(h),
-                   None if exponents is None else self._exponents.pointer(exponents),
-                   self._weight.pointer(weight), self._rstd.pointer(rstd),
-                   None if dresidual is None else
-                   (self._x if self._h is None else self._h).pointer(dresidual),
-                   self._x.pointer(dx),
-                   None if dweight is None else self._dweight.pointer(dweight))
+        stream = _current(self._index) if stream is None else getattr(stream, "cuda_stream", stream)
+        rc = self._lib.gemm_norm_backward(
+            self.handle, self._y.pointer(dy), rows.pointer(h),
+            None if exponents is None else self._exponents.pointer(exponents),
+            self._weight.pointer(weight), self._rstd.pointer(rstd),
+            None if dresidual is None else
+            (self._x if self._h is None else self._h).pointer(dresidual),
+            self._x.pointer(dx), None if dweight is None else self._dweight.pointer(dweight), stream)
+        if rc != _gemm.GEMM_OK:
+            raise _gemm.GemmError(rc, "gemm_norm_backward")
 
 
 class Rows8(_Op):
@@ -156,13 +167,19 @@ class Rows8(_Op):
 
     def pack(self, X, q, scales, stream=None) -> None:
         """Enqueue q and scales from X."""
-        self._call("gemm_rows8_pack", stream, self._X.pointer(X), self._q.pointer(q),
-                   self._scales.pointer(scales))
+        stream = _current(self._index) if stream is None else getattr(stream, "cuda_stream", stream)
+        rc = self._lib.gemm_rows8_pack(self.handle, self._X.pointer(X), self._q.pointer(q),
+                                       self._scales.pointer(scales), stream)
+        if rc != _gemm.GEMM_OK:
+            raise _gemm.GemmError(rc, "gemm_rows8_pack")
 
     def unpack(self, q, scales, X, stream=None) -> None:
         """Enqueue X from q and scales."""
-        self._call("gemm_rows8_unpack", stream, self._q.pointer(q), self._scales.pointer(scales),
-                   self._X.pointer(X))
+        stream = _current(self._index) if stream is None else getattr(stream, "cuda_stream", stream)
+        rc = self._lib.gemm_rows8_unpack(self.handle, self._q.pointer(q),
+                                         self._scales.pointer(scales), self._X.pointer(X), stream)
+        if rc != _gemm.GEMM_OK:
+            raise _gemm.GemmError(rc, "gemm_rows8_unpack")
 
 
 class Rows8Grad(_Op):
@@ -231,9 +248,13 @@ class I8Gemm(_Op):
 
     def run(self, X, x_scales, W, w_scales, offsets, D, stream=None) -> None:
         """Enqueue the products."""
-        self._call("gemm_i8_run", stream, self._X.pointer(X), self._x_scales.pointer(x_scales),
-                   self._W.pointer(W), self._w_scales.pointer(w_scales),
-                   _given(self._offsets, offsets, "offsets"), self._D.pointer(D))
+        stream = _current(self._index) if stream is None else getattr(stream, "cuda_stream", stream)
+        rc = self._lib.gemm_i8_run(
+            self.handle, self._X.pointer(X), self._x_scales.pointer(x_scales), self._W.pointer(W),
+            self._w_scales.pointer(w_scales), _given(self._offsets, offsets, "offsets"),
+            self._D.pointer(D), stream)
+        if rc != _gemm.GEMM_OK:
+            raise _gemm.GemmError(rc, "gemm_i8_run")
 
 
 def i8_matmul(X, x_scales, W, w_scales, offsets=None, out_dtype=torch.bfloat16, D=None,
