@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
 }
 
 // ---------------------------------------------------------------- copies of rows
-// 16 values an item.  A last unit that K ends in is padded with whatever
+// 16 values an item, as they are or widened to fp16.  A last unit that K ends in is padded with whatever
 // follows: the tensor maps end at K.  Up to two jobs a launch (one after the
 // other they take 3 us more of 4096 x 4096 x 4096), and two items a thread, one
 // after the other (four, all in flight: 5 us more of 8192 x 8192 x 8192).
@@ -770,11 +770,11 @@ struct CopyJob {
   uint8_t* dst;
   long long ld_src, ld_dst, rows;
   int cols, aligned;  // rows of src are 16-byte multiples apart and start so
+  bool widen;
   unsigned blocks;
   Deal deal;
 };
 
-template <bool WIDEN>
 __global__ void __launch_bounds__(DEAL_THREADS) i8_copy_kernel(const CopyJob first, const CopyJob second) {
   const bool two = blockIdx.x >= first.blocks;
   const CopyJob& job = two ? second : first;
@@ -787,8 +787,8 @@ __global__ void __launch_bounds__(DEAL_THREADS) i8_copy_kernel(const CopyJob fir
     const int k = static_cast<int>(at - r * job.deal.lanes.d) * 16;
     const int8_t* const from = job.src + row * job.ld_src + k;
     const uint4 w = job.aligned ? *reinterpret_cast<const uint4*>(from) : load16_at(from, min(16, job.cols - k));
-    uint4* const to = reinterpret_cast<uint4*>(job.dst + (WIDEN ? 2 : 1) * (row * job.ld_dst + k));
-    if constexpr (WIDEN) {
+    uint4* const to = reinterpret_cast<uint4*>(job.dst + (job.widen ? 2 : 1) * (row * job.ld_dst + k));
+    if (job.widen) {
       uint4 a, b;
       widen4(w.x, a.x, a.y);
       widen4(w.y, a.z, a.w);
@@ -811,18 +811,12 @@ CopyJob job_of(const I8Copy& c, int num_sms) {
   j.ld_dst = c.ld_dst;
   j.rows = c.rows;
   j.cols = c.cols;
+  j.widen = c.widen;
   j.aligned = c.cols % 16 == 0 && c.ld_src % 16 == 0 && reinterpret_cast<uintptr_t>(c.src) % 16 == 0;
   dim3 grid;
   j.deal = deal_of(c.rows, (c.cols + 15) / 16, 2, num_sms, grid);
   j.blocks = grid.x;
   return j;
-}
-
-template <bool WIDEN>
-cudaError_t copy_rows(const I8Copy& first, const I8Copy& second, int num_sms, cudaStream_t st) {
-  const CopyJob a = job_of(first, num_sms), b = job_of(second, num_sms);
-  if (a.blocks + b.blocks == 0) return cudaSuccess;
-  return launch_pdl(i8_copy_kernel<WIDEN>, dim3(a.blocks + b.blocks), dim3(DEAL_THREADS), 0, st, a, b);
 }
 
 // ---------------------------------------------------------------- launches
@@ -898,11 +892,10 @@ cudaError_t launch_i8_tiles(int rows, const CUtensorMap& w, const CUtensorMap& x
                               : launch_typed<T_F16>(rows, w, x, x32, d, p, units, split, st);
 }
 
-cudaError_t launch_i8_copy(const I8Copy& c, int num_sms, cudaStream_t st) {
-  return copy_rows<false>(c, I8Copy{}, num_sms, st);
-}
-cudaError_t launch_i8_widen(const I8Copy& first, const I8Copy& second, int num_sms, cudaStream_t st) {
-  return copy_rows<true>(first, second, num_sms, st);
+cudaError_t launch_i8_copies(const I8Copy& first, const I8Copy& second, int num_sms, cudaStream_t st) {
+  const CopyJob a = job_of(first, num_sms), b = job_of(second, num_sms);
+  if (a.blocks + b.blocks == 0) return cudaSuccess;
+  return launch_pdl(i8_copy_kernel, dim3(a.blocks + b.blocks), dim3(DEAL_THREADS), 0, st, a, b);
 }
 
 }  // namespace gb300

@@ -14,7 +14,7 @@
 // rows 89 (70.6) of which 3 are the last sum of dweight.  A row's gradients held
 // in registers between the passes, without the ring, 170 from block rows: a block
 // that waits for its row's sum has nothing in flight.  16 x 4096 to 8 bits: 2.5
-// in a graph; a call's host side takes 5.4.
+// in a graph; a call's host side takes 5.0.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -253,15 +253,17 @@ __host__ __device__ constexpr uint32_t ring_slot(uint32_t bytes) {
   return ANY ? (bytes + 15u) / 16u * 16u + 16u : bytes;
 }
 
-// VEC values of h: of type T, or of block rows with this exponent's step.
+// VEC values of h, of block rows in steps: the step is a power of two, which the
+// factors r and c of a whole vector take instead, exactly.
 template <typename T, int VEC>
-__device__ __forceinline__ void widen_h(const Vec<T, VEC>& v, float, float (&h)[VEC]) {
+__device__ __forceinline__ void widen_h(const Vec<T, VEC>& v, float (&h)[VEC]) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) h[j] = widen(v.v[j]);
 }
 template <int VEC>
-__device__ __forceinline__ void widen_h(const Vec<int8_t, VEC>& v, float step, float (&h)[VEC]) {
-  times_step<true>(v, step, h);
+__device__ __forceinline__ void widen_h(const Vec<int8_t, VEC>& v, float (&h)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) h[j] = from_byte(v, j) - BYTE_BIAS;
 }
 
 // Rows too long for the kernel below.  Blocks take rows in turn and read each
@@ -297,11 +299,12 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardPa
         return load_vec<E, VEC>(base + row * ld + i);
       }
     };
-    float dy[VEC], h[VEC], w[VEC];
+    float dy[VEC], h[VEC], w[VEC], hstep = 1.f;
     auto load_row = [&](int i) {
       const auto dyv = load(static_cast<const T*>(p.dy), p.ldy, i);
       const auto hv = load(static_cast<const HT*>(p.h), p.ldh, i);
-      widen_h(hv, HELD ? block_step(p.E[row * blocks + i / ROW_BLOCK]) : 1.f, h);
+      widen_h(hv, h);
+      if constexpr (HELD) hstep = block_step(p.E[row * blocks + i / ROW_BLOCK]);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) dy[j] = widen(dyv.v[j]);
       load_weight<T, VEC, ANY>(p.weight, w32, i, p.H, w);
@@ -310,12 +313,15 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardPa
     uint32_t top = 0u;
     for (int i = first; i < p.H; i += step) {
       load_row(i);
+      const float rh = r * hstep;
+      float vec = 0.f;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float t = dy[j] * h[j];
-        sum = fmaf(t, w[j], sum);
-        if (p.dweight && (!ANY || i + j < p.H)) mine[i + j] = fmaf(t, r, mine[i + j]);
+        vec = fmaf(t, w[j], vec);
+        if (p.dweight && (!ANY || i + j < p.H)) mine[i + j] = fmaf(t, rh, mine[i + j]);
       }
+      sum = fmaf(vec, hstep, sum);
     }
     row_reduce<true, false>(sum, top, warps, part[turn]);
     const float c = r * (r * (sum / static_cast<float>(p.H)));  // (r r may underflow)
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardPa
         if (p.dresidual) res = load(static_cast<const T*>(p.dresidual), p.ldr, i);
       }
       store_row<T, VEC, ANY>(static_cast<T*>(p.dx) + row * p.ldx + i, i, p.H,
-                             dx_of(dy, h, w, r, c, res, p.dresidual != nullptr));
+                             dx_of(dy, h, w, r, c * hstep, res, p.dresidual != nullptr));
     }
   }
 }
@@ -335,10 +341,11 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardPa
 // keeps the next rows of its turn in a ring in shared memory (bulk copies: dy, h
 // and dresidual of a row are one stage), so that what is in flight does not
 // depend on registers or on where a block is between its two passes over a row.
-// The passes read the stage twice.  With ANY the copies are of the aligned words
-// around a row, less those that are not all the operand's, whose bytes the copying
-// thread stores.
-template <typename T, int NV, bool HELD, bool ANY>
+// The passes read the stage twice.  With LEAD (ANY, and 8-bit rows that are VEC
+// apart, but not 16) the copies are of the aligned words around a row, less those
+// that are not all the operand's, whose bytes the copying thread stores (for all
+// 8-bit rows: 98 us instead of 89 for 16384 x 4096).
+template <typename T, int NV, bool HELD, bool ANY, bool LEAD>
 __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(sizeof(T))))
     norm_backward_ring_kernel(const NormBackwardParams p, const int stages) {
   constexpr int VEC = 16 / sizeof(T);
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
   const int warps = blockDim.x >> 5;
   const int step = blockDim.x * VEC, first = threadIdx.x * VEC;
   const int warp_first = (threadIdx.x & ~31) * VEC;  // whole warps store
-  const uint32_t dy_bytes = ring_slot<ANY>(p.H * sizeof(T)), h_bytes = ring_slot<ANY>(p.H * sizeof(HT));
+  const uint32_t dy_bytes = ring_slot<ANY>(p.H * sizeof(T)), h_bytes = ring_slot<LEAD>(p.H * sizeof(HT));
   const uint32_t stage_bytes = dy_bytes + h_bytes + (p.dresidual ? dy_bytes : 0u);
   const uint32_t bar0 = smem_u32(bars);
   if (threadIdx.x == 0) {
@@ -364,7 +371,7 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
   __syncthreads();
   // bytes of a row's first word that are not its own
   auto lead = [&](const void* row) {
-    return ANY ? static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) : 0;
+    return LEAD ? static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) : 0;
   };
   // lane l of the first warp copies operand l: dy, h, dresidual
   const int operands = p.dresidual ? 3 : 2;
@@ -378,7 +385,7 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
     const uint32_t bar = bar0 + 8 * s;
     uint8_t* const to = ring + s * stage_bytes + slot;
     const uint8_t* const from = base + row * stride;
-    if constexpr (ANY) {
+    if constexpr (LEAD) {
       const int a = lead(from), end = a + length;
       // the words that are all the operand's: bytes [w0, w1) of the slot
       const int w0 = row * stride >= a ? 0 : 16;
@@ -458,18 +465,21 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
       if (first + k * step < p.H) {
         float h[VEC];
         const auto hk = load(hrow, first + k * step);
-        widen_h(hk, scale[k], h);
+        widen_h(hk, h);
         const auto dy = load(dyrow, first + k * step);
         if constexpr (KEEP) {
           hv[k] = hk;
           dyv[k] = dy;
         }
+        const float rh = HELD ? r * scale[k] : r;
+        float vec = HELD ? 0.f : sum;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           const float t = widen(dy.v[j]) * h[j];
-          dw[k][j] = fmaf(t, r, dw[k][j]);
-          sum = fmaf(t, w[k][j], sum);
+          dw[k][j] = fmaf(t, rh, dw[k][j]);
+          vec = fmaf(t, w[k][j], vec);
         }
+        sum = HELD ? fmaf(vec, scale[k], sum) : vec;
       }
     if (warps == 1) __syncwarp();
     row_reduce<true, false>(sum, top, warps, part[turn]);
@@ -488,14 +498,14 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
         float h[VEC], d[VEC];
         Vec<T, VEC> res{};
         if (i < p.H) {
-          widen_h(KEEP ? hv[k] : load(hrow, i), scale[k], h);
+          widen_h(KEEP ? hv[k] : load(hrow, i), h);
           const auto dy = KEEP ? dyv[k] : load(dyrow, i);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) d[j] = widen(dy.v[j]);
           if (p.dresidual) res = load(resrow, i);
         }
         store_row<T, VEC, ANY>(static_cast<T*>(p.dx) + row * p.ldx + i, i, p.H,
-                               dx_of(d, h, w[k], r, c, res, p.dresidual != nullptr));
+                               dx_of(d, h, w[k], r, HELD ? c * scale[k] : c, res, p.dresidual != nullptr));
       }
     }
     if (++s == stages) {
@@ -519,7 +529,9 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
 }
 
 // dweight: the blocks' partial sums, 32 columns a block, added up by 32 warps
-// in turn and then in warp order.
+// in turn and then in warp order.  Eight loads in flight, a last batch's past the
+// end of its last row again (predicated away instead, 16 of them take 5 us more for
+// 1216 rows; a loop unrolled four times 1).
 __global__ void __launch_bounds__(1024)
     norm_dweight_kernel(const float* partial, int rows, int H, float* dweight) {
   __shared__ float part[32][33];
@@ -528,8 +540,13 @@ __global__ void __launch_bounds__(1024)
   pdl_trigger();
   float sum = 0.f;
   if (i < H) {
-#pragma unroll 4
-    for (int r = threadIdx.y; r < rows; r += 32) sum += partial[static_cast<long long>(r) * H + i];
+    for (int r0 = threadIdx.y; r0 < rows; r0 += 32 * 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = partial[static_cast<long long>(min(r0 + 32 * u, rows - 1)) * H + i];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum += r0 + 32 * u < rows ? v[u] : 0.f;
+    }
   }
   part[threadIdx.y][threadIdx.x] = sum;
   __syncthreads();
@@ -592,8 +609,10 @@ bool ring_shape(int64_t stage_bytes, int threads, int room, int& blocks, int& st
 // What a launch of the ring kernels needs once, for rows of H elements.
 template <typename T, int NV>
 cudaError_t allow_ring() {
-  for (auto* const kernel : {norm_backward_ring_kernel<T, NV, false, false>, norm_backward_ring_kernel<T, NV, false, true>,
-                             norm_backward_ring_kernel<T, NV, true, false>, norm_backward_ring_kernel<T, NV, true, true>}) {
+  for (auto* const kernel :
+       {norm_backward_ring_kernel<T, NV, false, false, false>, norm_backward_ring_kernel<T, NV, false, true, true>,
+        norm_backward_ring_kernel<T, NV, true, false, false>, norm_backward_ring_kernel<T, NV, true, false, true>,
+        norm_backward_ring_kernel<T, NV, true, true, true>}) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES);
     if (e != cudaSuccess) return e;
@@ -607,22 +626,22 @@ cudaError_t prepare_typed(int H) {
   return nv == 1 ? allow_ring<T, 1>() : nv == 2 ? allow_ring<T, 2>() : allow_ring<T, 4>();
 }
 
-template <typename T, bool HELD, bool ANY>
+template <typename T, bool HELD, bool ANY, bool LEAD>
 cudaError_t launch_backward(const NormBackwardParams& p, int num_sms, int& blocks, cudaStream_t st) {
   constexpr int S = sizeof(T);
   int nv, per_sm, stages;
   const int threads = ring_threads<T>(p.H, nv);
   const uint32_t H = p.H;  // (four bytes of 2^30 elements and more pass an int)
   const int64_t stage_bytes =
-      ring_slot<ANY>(H * S) * (p.dresidual ? 2ll : 1ll) + ring_slot<ANY>(H * (HELD ? 1 : S));
+      ring_slot<ANY>(H * S) * (p.dresidual ? 2ll : 1ll) + ring_slot<LEAD>(H * (HELD ? 1 : S));
   auto blocks_of = [&](int each) {
     return static_cast<int>(std::min<long long>(p.T, static_cast<long long>(num_sms) * each));
   };
   if (threads > 0 && ring_shape(stage_bytes, threads, ring_room(ANY, nv, nv * 16 / S), per_sm, stages)) {
     blocks = blocks_of(per_sm);
-    auto* const kernel = nv == 1   ? norm_backward_ring_kernel<T, 1, HELD, ANY>
-                         : nv == 2 ? norm_backward_ring_kernel<T, 2, HELD, ANY>
-                                   : norm_backward_ring_kernel<T, 4, HELD, ANY>;
+    auto* const kernel = nv == 1   ? norm_backward_ring_kernel<T, 1, HELD, ANY, LEAD>
+                         : nv == 2 ? norm_backward_ring_kernel<T, 2, HELD, ANY, LEAD>
+                                   : norm_backward_ring_kernel<T, 4, HELD, ANY, LEAD>;
     return launch_pdl(kernel, dim3(blocks), dim3(threads), stages * static_cast<size_t>(stage_bytes), st, p,
                       stages);
   }
@@ -653,13 +672,15 @@ cudaError_t forward_typed(const NormParams& p, int num_sms, cudaStream_t st) {
 template <typename T, bool HELD>
 cudaError_t backward_held(const NormBackwardParams& p, int num_sms, int& blocks, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(T), S = sizeof(T);
-  // (bulk copies are of 16 bytes, so that block rows' length is of 16 values)
-  const bool vec = p.H % (HELD ? 16 : VEC) == 0 && rows_fit(p.dy, p.ldy, S, 16) &&
-                   (HELD ? rows_fit(p.h, p.ldh, 1, 16) : rows_fit(p.h, p.ldh, S, 16)) &&
+  const bool vec = p.H % VEC == 0 && rows_fit(p.dy, p.ldy, S, 16) &&
+                   (HELD ? rows_fit(p.h, p.ldh, 1, VEC) : rows_fit(p.h, p.ldh, S, 16)) &&
                    (!p.dresidual || rows_fit(p.dresidual, p.ldr, S, 16)) &&
                    rows_fit(p.dx, p.ldx, S, 16) && rows_fit(p.weight, 0, 1, 16);
-  return vec ? launch_backward<T, HELD, false>(p, num_sms, blocks, st)
-             : launch_backward<T, HELD, true>(p, num_sms, blocks, st);
+  if (!vec) return launch_backward<T, HELD, true, true>(p, num_sms, blocks, st);
+  if constexpr (HELD)  // bulk copies are of 16 bytes
+    if (p.H % 16 != 0 || !rows_fit(p.h, p.ldh, 1, 16))
+      return launch_backward<T, HELD, false, true>(p, num_sms, blocks, st);
+  return launch_backward<T, HELD, false, false>(p, num_sms, blocks, st);
 }
 
 template <typename T>

@@ -103,8 +103,9 @@ struct I8Copy {
   void* dst;
   long long ld_dst, rows;
   int cols;
+  bool widen;  // to fp16
 };
-cudaError_t launch_i8_copy(const I8Copy& c, int num_sms, cudaStream_t st);
-cudaError_t launch_i8_widen(const I8Copy& first, const I8Copy& second, int num_sms, cudaStream_t st);
+// Both (a job without rows is none) in one launch.
+cudaError_t launch_i8_copies(const I8Copy& first, const I8Copy& second, int num_sms, cudaStream_t st);
 
 }  // namespace gb300

@@ -385,10 +385,9 @@ int run_i8_tiles(gemm_op_t op, const int8_t* X, const float* x_scales, const int
   const int K = static_cast<int>(d.K);
   const int64_t w_rows = d.E * d.N;
   uint8_t* const ws = static_cast<uint8_t*>(op->ws);
-  const I8Copy copy_x = {X, d.ldx, ws, op->ws_lda, d.R, K};
-  const I8Copy copy_w = {W, d.ldw, ws + op->ws_b_off, op->ws_ldb, w_rows, K};
-  int rc = launched(launch_i8_widen(copy_x, wide ? copy_w : I8Copy{}, op->num_sms, st));
-  if (rc == GEMM_OK && op->copy_b && !wide) rc = launched(launch_i8_copy(copy_w, op->num_sms, st));
+  const I8Copy copy_x = {X, d.ldx, ws, op->ws_lda, d.R, K, true};
+  const I8Copy copy_w = {W, d.ldw, ws + op->ws_b_off, op->ws_ldb, w_rows, K, wide};
+  const int rc = launched(launch_i8_copies(copy_x, op->copy_b ? copy_w : I8Copy{}, op->num_sms, st));
   if (rc != GEMM_OK) return rc;
   // (the maps of what the caller owns; the others are the handle's)
   CUtensorMap wm{}, dm{};
