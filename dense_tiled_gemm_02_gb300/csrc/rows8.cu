@@ -129,8 +129,11 @@ __global__ void __launch_bounds__(THREADS)
 // ---------------------------------------------------------------- scaled rows
 // A block (or, blockDim.x = 32, a warp) a row, whose threads hold NV vectors
 // each, or with NV = 0 (rows too long) read them again.
+// Registers: what 1024 threads have; those that hold fp32 of any alignment keep to
+// 48, at which five blocks of 256 threads fit an SM (52, four: 91 us instead of 77
+// for 16384 x 4095).
 template <typename T, int VEC, int NV, bool ANY>
-__global__ void __launch_bounds__(1024) pack_rows_kernel(const Rows8Params p) {
+__global__ void __maxnreg__(ANY && sizeof(T) == 4 ? 48 : 64) pack_rows_kernel(const Rows8Params p) {
   __shared__ float2 part[32];
   const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int step = blockDim.x * VEC, first = threadIdx.x * VEC;

@@ -601,9 +601,10 @@ GEMM_API int gemm_w4_run(gemm_op_t op, const void* X, const uint8_t* W, const vo
  *   rstd[t] = 1 / sqrt(mean_i h[t, i]^2 + eps)
  *   y[t, i] = h[t, i] * rstd[t] * weight[i]
  * y_type type: y rounded once.  y_type I8: scaled rows, scales[t] = max_i
- * |y[t, i]| / 127 and q the nearest integers (ties to even); a row of zeros
- * has scale 0, a row in which y is not finite a scale that is not finite, and
- * q 0.  weight: H values of type or F32.  rstd (T fp32) may be NULL.  Sums are
+ * |y[t, i]| / 127 and q the integers nearest to 127 p / max |p|, ties to even, of
+ * the row's p = h weight, both products and quotients rounded to fp32; a row of
+ * zeros has scale 0, a row in which y is not finite a scale that is not finite,
+ * and q 0.  weight: H values of type or F32.  rstd (T fp32) may be NULL.  Sums are
  * fp32.  h may be x or residual itself (of the same leading dimension);
  * nothing else may overlap.
  * gemm_norm_backward (y_type = type): from dy (laid out like y) and what
@@ -635,8 +636,9 @@ GEMM_API int gemm_norm_backward(gemm_op_t op, const void* dy, const void* h, con
  * 127 steps (at least 2^-127, of fp16 rows 2^-24), q the nearest integers, ties
  * to even; a block with a value that is not finite gets the byte 255 and comes
  * back as NaN.  block 0: scaled rows, scales T fp32, as gemm_norm_run makes
- * them.  pack reads X and writes q and scales, unpack the reverse; what rounds
- * past type's largest finite value comes back as that.
+ * them of p = X (of 16-bit types, q is the nearest to the exact quotient).
+ * pack reads X and writes q and scales, unpack the reverse; what rounds past
+ * type's largest finite value comes back as that.
  */
 typedef struct {
   int64_t T, H;
