@@ -58,15 +58,15 @@ __device__ __forceinline__ void load_weight(const void* w, bool f32, int i, int 
 }
 
 // A row's sum of squares and (I8) largest |h w|; if KEEP with what the store needs
-// of the weights: h w, or w.
-template <typename T, int VEC, bool I8, bool ANY, bool KEEP>
-__device__ __forceinline__ void row_sums(const NormParams& p, const Vec<T, VEC>& h, int i,
+// of the weights: h w, or w.  SCALED (here and below): of h times `by`.
+template <typename T, int VEC, bool I8, bool ANY, bool KEEP, bool SCALED>
+__device__ __forceinline__ void row_sums(const NormParams& p, const Vec<T, VEC>& h, int i, float by,
                                          float& sum, uint32_t& top, float (&kept)[VEC]) {
   float w[VEC];
   if constexpr (I8 || KEEP) load_weight<T, VEC, ANY>(p.weight, p.weight_type == T_F32, i, p.H, w);
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
-    const float v = widen(h.v[j]);
+    const float v = SCALED ? widen(h.v[j]) * by : widen(h.v[j]);
     sum = fmaf(v, v, sum);
     if constexpr (I8) top = max(top, magnitude(v * w[j]));
     if constexpr (KEEP) kept[j] = I8 ? v * w[j] : w[j];
@@ -93,20 +93,22 @@ __device__ __forceinline__ void store_row(T* p, int i, int H, const Vec<T, VEC>&
     store_vec(p, x);
 }
 
-template <typename T, int VEC, bool I8, bool ANY, bool KEEP>
+template <typename T, int VEC, bool I8, bool ANY, bool KEEP, bool SCALED>
 __device__ __forceinline__ void store_y(const NormParams& p, long long row, const Vec<T, VEC>& h,
-                                        int i, float r, const RowScale& q, const float (&kept)[VEC]) {
+                                        int i, float by, float r, const RowScale& q,
+                                        const float (&kept)[VEC]) {
+  auto value = [&](int j) { return SCALED ? widen(h.v[j]) * by : widen(h.v[j]); };
   float w[VEC];
   if (!KEEP && i < p.H) load_weight<T, VEC, ANY>(p.weight, p.weight_type == T_F32, i, p.H, w);
   if constexpr (I8) {
     float v[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = KEEP ? kept[j] : widen(h.v[j]) * w[j];
-    store_row<int8_t, VEC, ANY>(static_cast<int8_t*>(p.y) + row * p.ldy + i, i, p.H, row_integers(v, q));
+    for (int j = 0; j < VEC; ++j) v[j] = KEEP ? kept[j] : value(j) * w[j];
+    store_row<int8_t, VEC, ANY>(static_cast<int8_t*>(p.y) + row * p.ldy + i, i, p.H, row_integers<SCALED>(v, q));
   } else {
     float v[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = widen(h.v[j]) * r * (KEEP ? kept[j] : w[j]);
+    for (int j = 0; j < VEC; ++j) v[j] = value(j) * r * (KEEP ? kept[j] : w[j]);
     store_row<T, VEC, ANY>(static_cast<T*>(p.y) + row * p.ldy + i, i, p.H, narrowed<T, VEC>(v));
   }
 }
@@ -119,7 +121,7 @@ __device__ __forceinline__ void store_y(const NormParams& p, long long row, cons
 // shifted.
 template <typename T, int VEC, int NV, bool I8, bool ANY>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
-  __shared__ float2 part[MAX_WARPS];
+  __shared__ float2 part[2][MAX_WARPS];
   const int warps = blockDim.x >> 5;
   const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
   pdl_wait();
@@ -188,9 +190,6 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
         for (int k = 0; k < NV; ++k) h[k] = settle(x[k], first + k * step);
       }
     }
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (first + k * step < p.H) row_sums<T, VEC, I8, ANY, KEEP>(p, h[k], first + k * step, sum, top, kept[k]);
   } else {
     for (int i = first, i0 = warp_first; i0 < p.H; i += step, i0 += step) {
       Words v;
@@ -201,30 +200,80 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
         add_residual(h[0], settle(v, i));
         store_row<T, VEC, ANY>(hout + i, i, p.H, h[0]);
       }
-      if (i < p.H) row_sums<T, VEC, I8, ANY, KEEP>(p, h[0], i, sum, top, kept[0]);
+      if (i < p.H) row_sums<T, VEC, I8, ANY, KEEP, false>(p, h[0], i, 1.f, sum, top, kept[0]);
     }
   }
-  row_reduce<true, I8>(sum, top, warps, part);
-  const float r = 1.f / sqrtf(sum / static_cast<float>(p.H) + p.eps);
-  const RowScale q = I8 ? row_scale(__uint_as_float(top), r) : RowScale{};
-  if (threadIdx.x == 0) {
-    if (p.rstd) p.rstd[row] = r;
-    if constexpr (I8) p.scales[row] = q.scale;
-  }
-  if constexpr (NV > 0) {
+  // f(h, i, kept) for all of this thread's vectors in the row, or (whole_warps) its
+  // warp's.  NV = 0: h's or x's row again (with ANY a thread reads what its warp's
+  // lanes and, one word at either end, other warps stored before the barrier of
+  // the sum).
+  auto each = [&](bool whole_warps, auto f) {
+    if constexpr (NV > 0) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if ((ANY ? warp_first : first) + k * step < p.H)
-        store_y<T, VEC, I8, ANY, KEEP>(p, row, h[k], first + k * step, r, q, kept[k]);
-  } else {
-    // h's or x's row again (with ANY a thread reads what its warp's lanes and, one
-    // word at either end, other warps stored before the barrier of the sum)
-    for (int i = first, i0 = warp_first; i0 < p.H; i += step, i0 += step) {
-      Words v;
-      load(p.residual ? p.h : p.x, p.residual ? p.ldh : p.ldx, i, v);
-      store_y<T, VEC, I8, ANY, KEEP>(p, row, settle(v, i), i, r, q, kept[0]);
+      for (int k = 0; k < NV; ++k)
+        if ((whole_warps ? warp_first : first) + k * step < p.H) f(h[k], first + k * step, kept[k]);
+    } else {
+      for (int i = first, i0 = warp_first; (whole_warps ? i0 : i) < p.H; i += step, i0 += step) {
+        Words v;
+        load(p.residual ? p.h : p.x, p.residual ? p.ldh : p.ldx, i, v);
+        f(settle(v, i), i, kept[0]);
+      }
     }
+  };
+  if constexpr (NV > 0)
+    each(false, [&](const Vec<T, VEC>& v, int i, float(&k)[VEC]) {
+      row_sums<T, VEC, I8, ANY, KEEP, false>(p, v, i, 1.f, sum, top, k);
+    });
+  row_reduce<true, I8>(sum, top, warps, part[0]);
+  auto finish = [&](auto scaled, float by, float r, float rstd) {  // r: of h times `by`
+    const RowScale q = I8 ? row_scale(__uint_as_float(top), r) : RowScale{};
+    if (threadIdx.x == 0) {
+      if (p.rstd) p.rstd[row] = rstd;
+      if constexpr (I8) p.scales[row] = q.scale;
+    }
+    each(ANY || NV == 0, [&](const Vec<T, VEC>& v, int i, const float(&k)[VEC]) {
+      store_y<T, VEC, I8, ANY, KEEP, decltype(scaled)::value>(p, row, v, i, by, r, q, k);
+    });
+  };
+  // Squares of values beyond 2^64 overflow, those below 2^-50 underflow (which
+  // matters where eps is as small), and so may h w: then once more with h times
+  // a power of two that brings its largest magnitude to one.  (Not fp16 by itself.)
+  float by = 1.f, r = 0.f, rstd = 0.f;
+  uint32_t most = 0u;
+  if (!(sum < INFINITY) || (sum < 0x1p-90f && p.eps < 0x1p-100f) ||
+      (I8 && (top < RowScale::LEAST || top > RowScale::MOST))) {
+    each(false, [&](const Vec<T, VEC>& v, int, const float(&)[VEC]) { most = max(most, vec_top(v)); });
+    float none = 0.f;
+    row_reduce<false, true>(none, most, warps, part[1]);
   }
+  const bool scaled = most != 0u && most < 0x7F800000u;  // (the same for all of a row's threads)
+  if (scaled) {
+    const uint32_t up = min(253u, max(1u, 254u - (most >> 23)));
+    by = __uint_as_float(up << 23);
+    sum = 0.f;
+    top = 0u;
+    each(false, [&](const Vec<T, VEC>& v, int i, float(&k)[VEC]) {
+      row_sums<T, VEC, I8, ANY, KEEP, true>(p, v, i, by, sum, top, k);
+    });
+    row_reduce<true, I8>(sum, top, warps, part[0]);
+    const float eps = p.eps * by * by;
+    if (eps < 0x1p40f) {
+      r = 1.f / sqrtf(sum / static_cast<float>(p.H) + eps);
+      rstd = r * by;
+    } else {  // the squares are nothing beside eps
+      rstd = 1.f / sqrtf(p.eps);
+      r = rstd * __uint_as_float((254u - up) << 23);
+    }
+  } else {
+    r = rstd = 1.f / sqrtf(sum / static_cast<float>(p.H) + p.eps);
+  }
+  // (for rows that are read again, one loop for both: 173 us instead of 148 with two
+  // for 2048 x 40000 bf16 with a residual; for those in registers, two: 54 us instead
+  // of 58 with one for 16384 x 4096 bf16 to 8 bits)
+  if (NV == 0 || scaled)
+    finish(std::true_type{}, by, r, rstd);
+  else
+    finish(std::false_type{}, by, r, rstd);
 }
 
 // ---------------------------------------------------------------- backward
@@ -314,17 +363,15 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardPa
     for (int i = first; i < p.H; i += step) {
       load_row(i);
       const float rh = r * hstep;
-      float vec = 0.f;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float t = dy[j] * h[j];
-        vec = fmaf(t, w[j], vec);
-        if (p.dweight && (!ANY || i + j < p.H)) mine[i + j] = fmaf(t, rh, mine[i + j]);
+        const float t = dy[j] * (h[j] * rh);
+        sum = fmaf(t, w[j], sum);
+        if (p.dweight && (!ANY || i + j < p.H)) mine[i + j] += t;
       }
-      sum = fmaf(vec, hstep, sum);
     }
     row_reduce<true, false>(sum, top, warps, part[turn]);
-    const float c = r * (r * (sum / static_cast<float>(p.H)));  // (r r may underflow)
+    const float c = sum / static_cast<float>(p.H);
     for (int i = first, i0 = warp_first; i0 < p.H; i += step, i0 += step) {
       Vec<T, VEC> res{};
       if (i < p.H) {
@@ -332,7 +379,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardPa
         if (p.dresidual) res = load(static_cast<const T*>(p.dresidual), p.ldr, i);
       }
       store_row<T, VEC, ANY>(static_cast<T*>(p.dx) + row * p.ldx + i, i, p.H,
-                             dx_of(dy, h, w, r, c * hstep, res, p.dresidual != nullptr));
+                             dx_of(dy, h, w, r, r * hstep * c, res, p.dresidual != nullptr));
     }
   }
 }
@@ -471,15 +518,17 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
           hv[k] = hk;
           dyv[k] = dy;
         }
+        // (h r is about 1 whatever h is, dy h may be anything: h times its vector's r,
+        // or of at most 127 steps the vector's sum)
         const float rh = HELD ? r * scale[k] : r;
         float vec = HELD ? 0.f : sum;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float t = widen(dy.v[j]) * h[j];
-          dw[k][j] = fmaf(t, rh, dw[k][j]);
+          const float t = widen(dy.v[j]) * (HELD ? h[j] : h[j] * rh);
+          dw[k][j] = HELD ? fmaf(t, rh, dw[k][j]) : dw[k][j] + t;
           vec = fmaf(t, w[k][j], vec);
         }
-        sum = HELD ? fmaf(vec, scale[k], sum) : vec;
+        sum = HELD ? fmaf(vec, rh, sum) : vec;
       }
     if (warps == 1) __syncwarp();
     row_reduce<true, false>(sum, top, warps, part[turn]);
@@ -490,7 +539,7 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
       const long long next = row + static_cast<long long>(stages - 1) * gridDim.x;
       if (next < p.T) load_row(next, s == 0 ? stages - 1 : s - 1);
     }
-    const float c = r * (r * (sum / static_cast<float>(p.H)));  // (r r may underflow)
+    const float c = sum / static_cast<float>(p.H);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = first + k * step;
@@ -505,7 +554,7 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
           if (p.dresidual) res = load(resrow, i);
         }
         store_row<T, VEC, ANY>(static_cast<T*>(p.dx) + row * p.ldx + i, i, p.H,
-                               dx_of(d, h, w[k], r, HELD ? c * scale[k] : c, res, p.dresidual != nullptr));
+                               dx_of(d, h, w[k], r, HELD ? r * scale[k] * c : r * c, res, p.dresidual != nullptr));
       }
     }
     if (++s == stages) {

@@ -328,15 +328,18 @@ __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
 // scale * integer its values times `unit`.  inv + low is 127 / top / pre to twice
 // fp32's bits, so that what is in the middle of two integers (top / 2 always is)
 // comes out there and goes to the even one: by the reciprocal's 24 bits alone
-// every second tie went astray.  pre keeps all of them in the normal range.  A
-// scale that is not finite has integers of 0.
+// every second tie went astray.  pre keeps all of them in the normal range, 1 for a
+// top between LEAST and MOST.  A scale that is not finite has integers of 0.
 struct RowScale {
   float scale, pre, inv, low;
+  static constexpr uint32_t LEAST = (127u - 100u) << 23, MOST = (127u + 100u) << 23;  // (bits)
 };
 __device__ __forceinline__ RowScale row_scale(float top, float unit) {
   RowScale r;
   r.scale = top * unit / 127.f;
-  r.pre = top < 0x1p-100f ? 0x1p80f : top > 0x1p100f ? 0x1p-80f : 1.f;
+  r.pre = top < __uint_as_float(RowScale::LEAST)  ? 0x1p80f
+          : top > __uint_as_float(RowScale::MOST) ? 0x1p-80f
+                                                  : 1.f;
   const float t = top * r.pre;
   const bool some = top > 0.f && magnitude(r.scale) < 0x7F800000u;
   r.inv = some ? 127.f / t : 0.f;
@@ -350,7 +353,8 @@ __device__ __forceinline__ RowScale row_scale(float top, float unit) {
 // with are multiples of v's last place, above 2^-11 v).  The same in 24 bits would
 // take a second look at what rounds to a middle: by pairs 49 us instead of 31.6 for
 // 16384 x 4096 bf16, in which middles are common, and the norm's 89 instead of 84.6.
-template <int VEC>
+// PRE: pre may not be 1.
+template <bool PRE, int VEC>
 __device__ __forceinline__ Vec<int8_t, VEC> row_integers(const float (&v)[VEC], const RowScale& r) {
   uint32_t n[VEC];
   float a[VEC];
@@ -358,7 +362,7 @@ __device__ __forceinline__ Vec<int8_t, VEC> row_integers(const float (&v)[VEC], 
                  integers = pair_of(INTEGERS, INTEGERS);
 #pragma unroll
   for (int j = 0; j < VEC; ++j) a[j] = v[j];
-  if (r.pre != 1.f) {  // (the same for a row's threads, and rare)
+  if (PRE && r.pre != 1.f) {  // (the same for a row's threads, and rare)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) a[j] *= r.pre;
   }

@@ -181,7 +181,7 @@ __global__ void __maxnreg__(ANY && sizeof(T) == 4 ? 48 : 64) pack_rows_kernel(co
     float f[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) f[j] = widen(v.v[j]);
-    const auto q = row_integers(f, s);
+    const auto q = row_integers<true>(f, s);
     int8_t* const to = p.q_out + row * p.ldq + i;
     if constexpr (ANY)
       store_shifted<false>(to, i, elements_at<VEC>(i, p.H), q);

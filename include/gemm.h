@@ -605,8 +605,10 @@ GEMM_API int gemm_w4_run(gemm_op_t op, const void* X, const uint8_t* W, const vo
  * the row's p = h weight, both products and quotients rounded to fp32; a row of
  * zeros has scale 0, a row in which y is not finite a scale that is not finite,
  * and q 0.  weight: H values of type or F32.  rstd (T fp32) may be NULL.  Sums are
- * fp32.  h may be x or residual itself (of the same leading dimension);
- * nothing else may overlap.
+ * fp32; of rows whose squares would leave fp32's range they are those of h times a
+ * power of two, so that y is right for any finite h (rstd in fp32 is infinite for
+ * rows of less than 2^-127 on average, which takes an eps of 0).  h may be x or
+ * residual itself (of the same leading dimension); nothing else may overlap.
  * gemm_norm_backward (y_type = type): from dy (laid out like y) and what
  * arrives at h by the residual, dresidual (like h, NULL for zero),
  *   dx = rstd (weight dy - h rstd^2 / H sum_j dy_j weight_j h_j) + dresidual

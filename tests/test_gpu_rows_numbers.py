@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import dense_tiled_gemm_02_gb300 as pkg
-from test_gpu_rows import (BF16, EPS, F16, F32, done, rnd, strided)
+from test_gpu_rows import (BF16, EPS, F16, F32, U, backward_ref, done, near, rnd, strided)
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,141 @@ def test_norm_to_the_nearest_integers(T, H, dtype, weights, pad):
     op.run(x, w, y, scales=scales)
     done(op)
     assert torch.equal(y.cpu(), nearest_integers(x.cpu().float() * w.cpu().float()))
+
+
+# ---------------------------------------------------------------- norm at the ends of the range
+def norm_of_any_size(h, w, eps):
+    """(rstd, y) in 64 bits."""
+    h = h.double()
+    rstd = 1 / torch.sqrt((h * h).mean(1) + eps)
+    return rstd, h * rstd[:, None] * w.double()
+
+
+# a row's size, as the exponent of two; at the last of them rstd is below fp32's normal range
+SIZES = [-126, -120, -80, -64, -50, -40, 40, 60, 64, 70, 100, 120, 126]
+RANGE_WIDTHS = [64, 1001, 2048, 4096, 8200, 40000, 40001]
+
+
+def rows_of_sizes(H, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.rand((len(SIZES), H), generator=g) + 0.5) * torch.where(
+        torch.rand((len(SIZES), H), generator=g) < 0.5, 1.0, -1.0)
+    return (x * torch.exp2(torch.tensor(SIZES, dtype=torch.float64))[:, None]).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("H", RANGE_WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("eps", [0.0, EPS, 2.0 ** -100, 1e30])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_norm_of_rows_of_any_size(H, dtype, eps, with_residual):
+    """Neither the squares nor their sum leave fp32's range unseen."""
+    x, w = rows_of_sizes(H, dtype, H), rnd((H,), dtype, 3)
+    res = torch.zeros_like(x) if with_residual else None
+    h = torch.empty_like(x) if with_residual else None
+    y, rstd = torch.empty_like(x), torch.empty(len(SIZES), device="cuda")
+    op = pkg.RmsNorm.like(x, w, y, residual=res, h=h, eps=eps)
+    op.run(x, w, y, residual=res, h=h, rstd=rstd)
+    done(op)
+    r_ref, y_ref = norm_of_any_size(x, w, op.desc.eps)
+    if with_residual:
+        assert torch.equal(h, x)
+    # (rstd's least step is 2^-149, half of it what h multiplies)
+    near(rstd, r_ref, (H + 8) * U * r_ref, "rstd")
+    near(y, y_ref, (H + 12) * U * y_ref.abs() + 2.0 ** -150 * (x.double() * w.double()).abs(), "y")
+
+
+@pytest.mark.parametrize("H", RANGE_WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("eps", [0.0, EPS])
+@pytest.mark.parametrize("size", [-100, -60, 0, 60, 100])
+def test_norm_to_8_bits_of_rows_and_weights_of_any_size(H, dtype, eps, size):
+    """h w may leave fp32's range where y does not."""
+    x, w = rows_of_sizes(H, dtype, H), (rnd((H,), F32, 3) * 2.0 ** size).to(dtype)
+    y, scales = torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(len(x), device="cuda")
+    op = pkg.RmsNorm.like(x, w, y, scales=scales, eps=eps)
+    op.run(x, w, y, scales=scales)
+    done(op)
+    r_ref, y_ref = norm_of_any_size(x, w, op.desc.eps)
+    top = y_ref.abs().amax(1)
+    # two roundings of what may be below the normal range, then divided by 127
+    near(scales, top / 127, (H + 12) * U * top / 127 + 2 * 2.0 ** -150, "scales")
+    ratio = 127 * y_ref / top[:, None]
+    assert float((y.double() - ratio).abs().max()) <= 0.5 + 127 * 3 * U
+
+
+@pytest.mark.parametrize("H", [64, 1001, 4096, 40001])
+@pytest.mark.parametrize("dtype,size", [(BF16, -128), (BF16, -133), (F32, -128), (F32, -140), (F32, -149)])
+def test_norm_of_rows_below_the_normal_range(H, dtype, size):
+    """rstd is infinite in fp32, y is not."""
+    g = torch.Generator().manual_seed(H)
+    x = torch.randint(-3, 4, (5, H), generator=g).double() * 2.0 ** size
+    x[:, 0] = 2.0 ** size
+    x, w = x.to(dtype).cuda(), rnd((H,), dtype, 3)
+    y, rstd = torch.empty_like(x), torch.empty(5, device="cuda")
+    op = pkg.RmsNorm.like(x, w, y, eps=0.0)
+    op.run(x, w, y, rstd=rstd)
+    done(op)
+    r_ref, y_ref = norm_of_any_size(x, w, 0.0)
+    near(y, y_ref, (H + 12) * U * y_ref.abs(), "y")
+    fits = r_ref < torch.finfo(F32).max
+    near(rstd[fits], r_ref[fits], (H + 8) * U * r_ref[fits], "rstd")
+    assert bool(torch.isinf(rstd[~fits]).all())
+    y, scales = torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(5, device="cuda")
+    op = pkg.RmsNorm.like(x, w, y, scales=scales, eps=0.0)
+    op.run(x, w, y, scales=scales)
+    done(op)
+    near(scales, y_ref.abs().amax(1) / 127, (H + 12) * U * y_ref.abs().amax(1) / 127, "scales")
+
+
+def test_norm_of_zeros_and_what_is_not_finite_beside_large_rows():
+    H = 320
+    x = rows_of_sizes(H, BF16, 1)
+    x[1], x[3, 7], x[9, 5], x[11, 300] = 0, float("inf"), float("nan"), float("-inf")
+    w = rnd((H,), BF16, 2)
+    y, rstd = torch.empty_like(x), torch.empty(len(x), device="cuda")
+    op = pkg.RmsNorm.like(x, w, y, eps=0.0)
+    op.run(x, w, y, rstd=rstd)
+    done(op)
+    r_ref, y_ref = norm_of_any_size(x, w, 0.0)
+    assert torch.equal(torch.isnan(y), torch.isnan(y_ref))  # (of zeros: 0 / 0)
+    assert torch.equal(torch.isinf(rstd), torch.isinf(r_ref))
+    assert torch.equal(rstd == 0, r_ref == 0)
+    y, scales = torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(len(x), device="cuda")
+    op = pkg.RmsNorm.like(x, w, y, scales=scales, eps=EPS)
+    op.run(x, w, y, scales=scales)
+    done(op)
+    bad = [3, 9, 11]
+    assert torch.isfinite(scales).logical_not().nonzero().flatten().tolist() == bad
+    assert not y[bad].any() and not y[1].any() and float(scales[1]) == 0
+
+
+@pytest.mark.parametrize("H", [64, 1001, 4096, 8200, 16392, 40001])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kept", ["rows", "8 bits"])
+def test_norm_gradients_of_rows_of_any_size(H, dtype, kept):
+    """The forward pass's own rstd, from rows or from their 8 bits."""
+    x, w = rows_of_sizes(H, dtype, H), rnd((H,), dtype, 3)
+    T = len(x)
+    dy, dres = rnd((T, H), dtype, 4), rnd((T, H), dtype, 5)
+    y, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty(H, device="cuda")
+    op = pkg.RmsNorm.like(x, w, y, eps=0.0)
+    op.run(x, w, y, rstd=rstd)
+    rows, exponents, h = x, None, x.double()
+    if kept == "8 bits":
+        rows, exponents = pkg.Rows8.empty(x)
+        pkg.Rows8.like(x, rows, exponents).pack(x, rows, exponents)
+        step = torch.exp2(exponents.cpu().double() - 127).cuda().repeat_interleave(32, 1)[:, :H]
+        h = rows.double() * step
+    op.backward(dy, rows, w, rstd, dx, dw, dresidual=dres, exponents=exponents)
+    done(op)
+    dx_ref, size, dw_ref, dw_size = backward_ref(dy, h, w, rstd, dres)
+    # below the normal range a rounding is 2^-150 instead of relative: of h r, whose
+    # error w dy and the sum over the row pass on, and of r times what it multiplies
+    r = rstd.double()[:, None]
+    low = 4 * 2.0 ** -150 * (1 + r * (1 + (dy.double() * w.double()).abs().amax(1, keepdim=True)) * 8)
+    fits = (dx_ref.abs() + size) < torch.finfo(dtype).max
+    near(torch.where(fits, dx, torch.zeros_like(dx)), torch.where(fits, dx_ref, 0.0),
+         torch.where(fits, (H + 12) * U * size + low, 0.0), "dx")
+    near(dw, dw_ref, (T + 4) * U * dw_size + T * 2.0 ** -140, "dweight")
+    assert bool(torch.isfinite(dw).all())
