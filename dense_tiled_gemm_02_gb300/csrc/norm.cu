@@ -31,7 +31,6 @@ constexpr int MAX_WARPS = 32;
 constexpr int BACKWARD_BLOCKS = 8;  // per SM, at most
 constexpr int RING_MOST = 4;        // stages of a block's ring
 constexpr int RING_BYTES = 212 * 1024;  // of all blocks of an SM
-constexpr uint64_t RING_TIMEOUT_NS = 2000000000ull;
 
 // VEC weights of the rows' type or of fp32, from column i; with ANY of any
 // alignment, from columns before the row's as well, and zeros outside it.
@@ -449,7 +448,9 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
       bulk_load_1d(smem_u32(to), from, length, bar);
     }
   };
-  for (int s = 0; s < stages; ++s) {
+  const bool skip = (p.debug_flags & DBG_SKIP_FIRST_FILL) ||
+                    ((p.debug_flags & DBG_SKIP_ONE_FILL) && blockIdx.x == 0);
+  for (int s = skip ? 1 : 0; s < stages; ++s) {  // test hook: the wait for the first row expires
     const long long row = blockIdx.x + static_cast<long long>(s) * gridDim.x;
     if (row < p.T) load_row(row, s);
   }
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
     prefetch(row + gridDim.x);
     // (a thread that gives up raises the flag before the barrier in row_reduce,
     // after which all see it)
-    bounded_wait(bar0 + 8 * s, ph, &abort_flag, p.status, STATUS_TIMEOUT, RING_TIMEOUT_NS);
+    bounded_wait(bar0 + 8 * s, ph, &abort_flag, p.status, STATUS_TIMEOUT, p.timeout_ns);
     const uint8_t* const stage = ring + s * stage_bytes;
     const T* const dyrow = reinterpret_cast<const T*>(
         stage + lead(static_cast<const T*>(p.dy) + row * p.ldy));
@@ -570,10 +571,13 @@ __global__ void __launch_bounds__(ring_room(ANY, NV, NV * 16 / static_cast<int>(
       for (int j = 0; j < VEC; ++j)
         if (first + k * step + (ANY ? j : 0) < p.H) mine[first + k * step + j] = dw[k][j];
   }
-  // after a wait that ran out: copies still under way land before the block leaves
+  // After a wait that ran out, at this block's row number m: copies under way land
+  // before the block leaves (of rows m to m + stages - 2, at the first one more).
   if (row < p.T && threadIdx.x == 0) {
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    const long long m = (row - blockIdx.x) / gridDim.x;
+    for (long long n = m; n < m + stages - (m > 0); ++n)
+      if (blockIdx.x + n * gridDim.x < p.T && !(skip && n == 0))
+        drain_wait(bar0 + 8 * static_cast<uint32_t>(n % stages), static_cast<uint32_t>(n / stages) & 1u, 200000000ull);
   }
 }
 

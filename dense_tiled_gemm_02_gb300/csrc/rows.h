@@ -43,6 +43,8 @@ struct NormBackwardParams {
   float* dweight;     // may be null
   float* partial;     // norm_partial_rows() x H
   uint32_t* status;
+  unsigned long long timeout_ns;
+  int debug_flags;
 };
 // Blocks of the backward kernel, at most, each of which leaves a row of partial
 // sums of dweight.

@@ -137,6 +137,9 @@ int gemm_norm_backward(gemm_op_t op, const void* dy, const void* h, const uint8_
   p.dweight = dweight;
   p.partial = static_cast<float*>(op->ws);
   p.status = op->status;
+  p.timeout_ns = op->timeout_ns;
+  p.debug_flags = op->debug_flags;
+  op->debug_flags = 0;
   return launched(launch_norm_backward(p, op->num_sms, st));
 }
 

@@ -446,9 +446,9 @@ GEMM_API int64_t gemm_op_workspace_bytes(gemm_op_t op);
 GEMM_API int gemm_op_plan_string(gemm_op_t op, char* buf, size_t n);
 
 /* gemm_op_debug_set: the test hook of gemm_debug_set, for the rings of the
- * grouped products and of the 8-bit products' tiles (the others ignore it).
- * GEMM_DEBUG_SKIP_ONE_FILL: only the first CTA or CTA pair of the next run
- * leaves its first stage unfilled. */
+ * grouped products, of the 8-bit products' tiles and of a norm's backward pass
+ * (the others ignore it).  GEMM_DEBUG_SKIP_ONE_FILL: only the first CTA or CTA
+ * pair of the next run leaves its first stage unfilled. */
 #define GEMM_DEBUG_SKIP_ONE_FILL 2
 GEMM_API int gemm_op_debug_set(gemm_op_t op, int flags, uint64_t timeout_ns);
 

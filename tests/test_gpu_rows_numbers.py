@@ -223,3 +223,36 @@ def test_norm_gradients_of_rows_of_any_size(H, dtype, kept):
          torch.where(fits, (H + 12) * U * size + low, 0.0), "dx")
     near(dw, dw_ref, (T + 4) * U * dw_size + T * 2.0 ** -140, "dweight")
     assert bool(torch.isfinite(dw).all())
+
+
+# ---------------------------------------------------------------- the gradients' wait
+@pytest.mark.parametrize("flag", [pkg.GEMM_DEBUG_SKIP_FIRST_FILL, pkg.GEMM_DEBUG_SKIP_ONE_FILL])
+@pytest.mark.parametrize("T,H", [(3, 64), (2000, 256), (700, 1001), (5000, 4096)])
+@pytest.mark.parametrize("in_8_bits", [False, True])
+@pytest.mark.parametrize("with_dresidual", [False, True])
+def test_norm_gradients_after_a_timeout(flag, T, H, in_8_bits, with_dresidual):
+    """A wait that runs out is reported, and the next call starts afresh."""
+    x, w, dy = rnd((T, H), BF16, 1), rnd((H,), BF16, 2), rnd((T, H), BF16, 3)
+    dres = rnd((T, H), BF16, 4) if with_dresidual else None
+    rstd, dx, dw = rnd((T,), F32, 5).abs() + 0.5, torch.empty_like(x), torch.empty(H, device="cuda")
+    rows, exponents = x, None
+    if in_8_bits:
+        rows, exponents = pkg.Rows8.empty(x)
+        pkg.Rows8.like(x, rows, exponents).pack(x, rows, exponents)
+    op = pkg.RmsNorm.like(x, w, torch.empty_like(x), eps=EPS)
+
+    def run():
+        op.backward(dy, rows, w, rstd, dx, dw, dresidual=dres, exponents=exponents)
+        return op.status()
+
+    assert run() == pkg.GEMM_OK
+    first = dx.clone(), dw.clone()
+    for timeout_ns in (1_000_000, 10_000_000):
+        op.debug_set(flag, timeout_ns)
+        assert run() == pkg.GEMM_ERR_DEVICE_TIMEOUT
+        op.debug_set(0)
+        dx.fill_(7.0)
+        dw.fill_(7.0)
+        assert run() == pkg.GEMM_OK
+        assert torch.equal(dx, first[0]) and torch.equal(dw, first[1])
+    op.close()
