@@ -219,11 +219,10 @@ __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel
       if (rb + m < r1 && n0 + n < p.N) {
         int v = 0;
         for (int y = 0; y < warps; ++y) v += red[y][n][m];
-        const float scale =
-            o == threadIdx.x
-                ? first_x * first_w
-                : p.x_scales[rb + m] * p.w_scales[static_cast<long long>(e) * p.N + n0 + n];
-        store_d(p.D, p.d_type, (rb + m) * p.ldd + n0 + n, static_cast<float>(v) * scale);
+        const bool first = o == threadIdx.x;
+        const float sx = first ? first_x : p.x_scales[rb + m];
+        const float sw = first ? first_w : p.w_scales[static_cast<long long>(e) * p.N + n0 + n];
+        store_d(p.D, p.d_type, (rb + m) * p.ldd + n0 + n, static_cast<float>(v) * sx * sw);
       }
     }
   }

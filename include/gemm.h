@@ -684,8 +684,10 @@ GEMM_API int gemm_rows8_grad_run(gemm_op_t op, const int8_t* q, const uint8_t* E
  * more than a few of X, are copied to aligned ones on each call.  The handle's
  * workspace holds X in fp16, and for many rows W too (2 bytes a weight).  The
  * sums are exact as long as they stay below 2^24 (always up to K = 1024), and
- * beyond that off by at most K * 2^-24 of the sum of magnitudes; scaled in fp32
- * and rounded once.  K < 2^17.
+ * beyond that off by at most K * 2^-24 of the sum of magnitudes (a few rows' are
+ * rounded once, so that D may differ in its last bits by how many rows there are).
+ * In fp32 they are multiplied by the row's scale, then by the output's, and rounded
+ * once to D's type.  K < 2^17.
  */
 typedef struct {
   int32_t E;

@@ -14,7 +14,9 @@ import pytest
 import torch
 
 import dense_tiled_gemm_02_gb300 as pkg
-from test_gpu_rows import (BF16, EPS, F16, F32, U, backward_ref, done, near, rnd, strided)
+from gpu_helpers import forced_plan
+from test_gpu_rows import (BF16, EPS, F16, F32, HALF_STEP, PLANS, TINY, U, backward_ref, done, ints,
+                           near, offsets_of, rnd, strided)
 
 pytestmark = pytest.mark.gpu
 
@@ -256,3 +258,40 @@ def test_norm_gradients_after_a_timeout(flag, T, H, in_8_bits, with_dresidual):
         assert run() == pkg.GEMM_OK
         assert torch.equal(dx, first[0]) and torch.equal(dw, first[1])
     op.close()
+
+
+# ---------------------------------------------------------------- scales of a product
+@pytest.mark.parametrize("counts", [[1], [8], [20], [70], [3, 0, 40, 9]])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_i8_scales_the_same_in_every_form(counts, out):
+    """The sum times the row's scale, then times the output's: where the scales'
+    product would leave fp32's range, and the same bits in every form."""
+    R, K, N, E = sum(counts), 1000, 136, len(counts)
+    off = offsets_of(counts) if E > 1 else None
+    X, W = ints((R, K), 1), ints((E, N, K), 2)
+    X[0] = 0  # a sum of zero
+    pairs = torch.tensor([(1e-25, 1e-18), (1e20, 1e25), (3e-20, 2e-24), (0.01, 0.02)])
+    xs = pairs[torch.arange(R) % 4, 0].cuda() * (1 + rnd((R,), F32, 3).abs())
+    ws = pairs[torch.arange(N) % 4, 1].cuda() * (1 + rnd((E, N), F32, 4).abs())
+    got = []
+    for plan in PLANS:
+        D = torch.empty((R, N), dtype=out, device="cuda")
+        with forced_plan(plan):
+            op = pkg.I8Gemm.like(X, xs, W, ws, off, D)
+        op.run(X, xs, W, ws, off, D)
+        done(op)
+        got.append(D)
+    at = 0
+    for e, n in enumerate(counts):
+        r = slice(at, at + n)
+        sums = X[r].double() @ W[e].double().t()
+        first = (sums.float() * xs[r, None]).double()  # the sums are exact
+        ref = first * ws[e].double()
+        fits = ref.abs() < torch.finfo(out).max
+        d = got[0][r].double()
+        off_by = (d - ref).abs() - (U * ref.abs() + 2.0 ** -150) * 2 - HALF_STEP[out] * ref.abs() - TINY[out]
+        assert not bool((off_by[fits] > 0).any())
+        assert not d[sums == 0].any()
+        at += n
+    for D, plan in zip(got[1:], PLANS[1:]):
+        assert torch.equal(D, got[0]), plan
