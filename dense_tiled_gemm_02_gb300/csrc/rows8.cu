@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(THREADS)
     if constexpr (ANY) q = shifted<false>(around, n);
     float v[VEC];
     times_step<BLOCKS>(q, step, v);
-    if (!(step < largest<T>() / 256.f)) {  // else nothing can round past the finite values
+    if (!(fabsf(step) < largest<T>() / 256.f)) {  // else nothing can round past the finite values
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[j] = finite(v[j], largest<T>());
     }

@@ -89,6 +89,24 @@ def test_norm_to_the_nearest_integers(T, H, dtype, weights, pad):
     assert torch.equal(y.cpu(), nearest_integers(x.cpu().float() * w.cpu().float()))
 
 
+# ---------------------------------------------------------------- scaled rows back
+def test_scaled_rows_back_from_scales_of_either_sign():
+    """What rounds past the largest finite value comes back as that, by negative
+    scales too."""
+    for dtype in (F16, BF16, F32):
+        top = torch.finfo(dtype).max
+        s = torch.tensor([1.0, -1.0, 0.01, -0.01, 0.0, -0.0, 1e-3, -1e-3], device="cuda") * top
+        q = ints((8, 96), 3, -127, 128)
+        q[:, 0], q[:, 1] = 127, -127
+        X = torch.empty((8, 96), dtype=dtype, device="cuda")
+        op = pkg.Rows8.like(X, q, s)
+        op.unpack(q, s, X)
+        done(op)
+        want = (q.double() * s.double()[:, None]).clamp(-top, top)
+        assert bool(torch.isfinite(X).all())
+        near(X, want, U * want.abs())
+
+
 # ---------------------------------------------------------------- norm at the ends of the range
 def norm_of_any_size(h, w, eps):
     """(rstd, y) in 64 bits."""
