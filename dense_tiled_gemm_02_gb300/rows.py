@@ -190,12 +190,13 @@ class Rows8Grad(_Op):
         """Plan for A (R x K) as block rows q and exponents, B (R x N) of a
         16-bit type and D (E, K, N); offsets None for E = 1."""
         R, K = q.shape
-        E, N = D.shape[0], B.shape[1]
         ldq = _int8_rows(q, (R, K), "q")
         _packed(exponents, (R, _blocks(K)), torch.uint8, "exponents")
-        if B.dim() != 2 or B.shape[0] != R or D.dim() != 3 or tuple(D.shape) != (E, K, N):
+        if (B.dim() != 2 or B.shape[0] != R or D.dim() != 3 or
+                tuple(D.shape[1:]) != (K, B.shape[1])):
             raise ValueError(f"q {tuple(q.shape)} and B {tuple(B.shape)} do not give D "
                              f"{tuple(D.shape)}")
+        E, N = D.shape[0], B.shape[1]
         _check_offsets(offsets, E)
         if C is not None and (C.shape != D.shape or C.dtype != D.dtype):
             raise ValueError("C must have D's shape and type")
