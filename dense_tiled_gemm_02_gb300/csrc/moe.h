@@ -54,29 +54,6 @@ __device__ __forceinline__ int2 expert_rows(const int* offsets, int e, int R, ui
   return r;
 }
 
-// The y-th expert that has rows, or -1 (every thread of the block calls it).
-__device__ __forceinline__ int nth_expert(const int* offsets, int E, int R, uint32_t* status, int y) {
-  __shared__ uint32_t words[32];
-  const int nw = (E + 31) / 32;
-  for (int e0 = threadIdx.x & ~31; e0 < 32 * nw; e0 += blockDim.x) {
-    const int e = e0 + (threadIdx.x & 31);
-    bool any = false;
-    if (e < E) {
-      const int2 r = expert_rows(offsets, e, R, status);
-      any = r.y > r.x;
-    }
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, any);
-    if ((threadIdx.x & 31) == 0) words[e0 / 32] = b;
-  }
-  __syncthreads();
-  for (int i = 0; i < nw; ++i) {
-    const int n = __popc(words[i]);
-    if (y < n) return 32 * i + __fns(words[i], 0, y + 1);
-    y -= n;
-  }
-  return -1;
-}
-
 // ---------------------------------------------------------------- routing (route.cu)
 struct RouteParams {
   int T, E, k, type, normalize;

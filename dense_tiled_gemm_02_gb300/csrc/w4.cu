@@ -139,6 +139,29 @@ __device__ __forceinline__ void store_d(void* d, int type, long long i, float v)
     static_cast<__half*>(d)[i] = __float2half_rn(v);
 }
 
+// The y-th expert that has rows, or -1 (every thread of the block calls it).
+__device__ __forceinline__ int nth_expert(const W4Params& p, int y) {
+  __shared__ uint32_t words[32];
+  const int nw = (p.E + 31) / 32;
+  for (int e0 = threadIdx.x & ~31; e0 < 32 * nw; e0 += blockDim.x) {
+    const int e = e0 + (threadIdx.x & 31);
+    bool any = false;
+    if (e < p.E) {
+      const int2 r = expert_rows(p.offsets, e, p.R, p.status);
+      any = r.y > r.x;
+    }
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, any);
+    if ((threadIdx.x & 31) == 0) words[e0 / 32] = b;
+  }
+  __syncthreads();
+  for (int i = 0; i < nw; ++i) {
+    const int n = __popc(words[i]);
+    if (y < n) return 32 * i + __fns(words[i], 0, y + 1);
+    y -= n;
+  }
+  return -1;
+}
+
 constexpr int RT = 2;  // 16-row weight tiles a warp takes against one X
 
 // NT: 8-token tiles.
@@ -162,7 +185,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps<NT>, SM_WARPS / kMaxWarps<NT>)
   pdl_trigger();
   int e = 0, r0 = 0, r1 = p.R;
   if (p.offsets) {
-    e = p.E > 1 ? nth_expert(p.offsets, p.E, p.R, p.status, blockIdx.y) : 0;
+    e = p.E > 1 ? nth_expert(p, blockIdx.y) : 0;
     if (e < 0) return;
     const int2 r = expert_rows(p.offsets, e, p.R, p.status);
     r0 = r.x;
