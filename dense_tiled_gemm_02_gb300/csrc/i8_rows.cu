@@ -109,16 +109,16 @@ __device__ __forceinline__ int3 nth_pass(const int* offsets, int E, int R, uint3
   return make_int3(found[0], found[1], found[2]);
 }
 
-// RT 16-row weight tiles a warp takes against NT tiles of 8 rows; U steps in
-// flight.  ALIGNED: rows of X and W are 16-byte multiples apart and start so.
-template <int RT, int NT, bool ALIGNED>
+// 16 rows of weights against NT tiles of 8 rows of X; U steps in flight.  ALIGNED:
+// rows of X and W are 16-byte multiples apart and start so.
+template <int NT, bool ALIGNED>
 __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel(const I8RowsParams p) {
-  constexpr int U = RT == 1 ? 4 : 2;
-  __shared__ int red[SM_WARPS][16 * RT][8 * NT + 1];
+  constexpr int U = 4;
+  __shared__ int red[SM_WARPS][16][8 * NT + 1];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int tiles = (p.N + 16 * RT - 1) / (16 * RT);  // passes one after another, tiles fastest
-  const int pass = blockIdx.x / tiles, n0 = (blockIdx.x - pass * tiles) * 16 * RT;
+  const int tiles = (p.N + 15) / 16;  // passes one after another, tiles fastest
+  const int pass = blockIdx.x / tiles, n0 = (blockIdx.x - pass * tiles) * 16;
   if (!p.offsets && p.K <= warps * U * STEP) {
     // The weights on their way to L2 while the kernel before this one ends
     // (nothing is read before that), where a warp has a single run of them:
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel
     // is in the way, 1 x 8192 x 8192: 14.9 -> 16.8.)
     const int n = n0 + g, k = warp * U * STEP + 128 * t;
 #pragma unroll
-    for (int i = 0; i < 2 * RT; ++i)
+    for (int i = 0; i < 2; ++i)
       if (128 * t < U * STEP && k < p.K && n + 8 * i < p.N) prefetch_l2(p.W + (n + 8 * i) * p.ldw + k);
   }
   pdl_wait();
@@ -144,35 +144,33 @@ __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel
   const int left = p.N - n0 - g;
   const int8_t* const w0 =
       p.W + (static_cast<long long>(e) * p.N + n0 + (left > 0 ? g : 0)) * p.ldw + 16 * t;
-  auto rows_on = [&](int i, int h) { return 16 * i + 8 * h < left ? 16 * i + 8 * h : 0; };
+  auto rows_on = [&](int h) { return 8 * h < left ? 8 * h : 0; };
   const int steps = (p.K + STEP - 1) / STEP;
   {
-    int acc[RT][NT][4] = {};
+    int acc[NT][4] = {};
     // the scales of the first output this thread will store, on their way
     // beside the sums (not multiplied here: that would wait for them)
     float first_x = 0.f, first_w = 0.f;
     {
-      const int n = threadIdx.x % (16 * RT), m = threadIdx.x / (16 * RT);
+      const int n = threadIdx.x % 16, m = threadIdx.x / 16;
       if (m < 8 * NT && rb + m < r1 && n0 + n < p.N) {
         first_x = p.x_scales[rb + m];
         first_w = p.w_scales[static_cast<long long>(e) * p.N + n0 + n];
       }
     }
     for (int s0 = warp * U; s0 < steps; s0 += warps * U) {
-      uint4 w[RT][2][U], x[NT][U];
+      uint4 w[2][U], x[NT][U];
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int h = 0; h < 2; ++h) {
+        const int8_t* const src = w0 + rows_on(h) * p.ldw + s0 * STEP;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int8_t* const src = w0 + rows_on(i, h) * p.ldw + s0 * STEP;
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int k = (s0 + u) * STEP + 16 * t;
-            w[i][h][u] = make_uint4(0u, 0u, 0u, 0u);
-            if (k < p.K)
-              w[i][h][u] = ALIGNED ? load16(src + u * STEP) : load16_at(src + u * STEP, min(16, p.K - k));
-          }
+        for (int u = 0; u < U; ++u) {
+          const int k = (s0 + u) * STEP + 16 * t;
+          w[h][u] = make_uint4(0u, 0u, 0u, 0u);
+          if (k < p.K)
+            w[h][u] = ALIGNED ? load16(src + u * STEP) : load16_at(src + u * STEP, min(16, p.K - k));
         }
+      }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int r = rb + 8 * j + g;
@@ -197,25 +195,19 @@ __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma_s8(acc[i][j], w[i][0][u].x, w[i][1][u].x, w[i][0][u].y, w[i][1][u].y, x[j][u].x,
-                   x[j][u].y);
-            mma_s8(acc[i][j], w[i][0][u].z, w[i][1][u].z, w[i][0][u].w, w[i][1][u].w, x[j][u].z,
-                   x[j][u].w);
-          }
+        for (int j = 0; j < NT; ++j) {
+          mma_s8(acc[j], w[0][u].x, w[1][u].x, w[0][u].y, w[1][u].y, x[j][u].x, x[j][u].y);
+          mma_s8(acc[j], w[0][u].z, w[1][u].z, w[0][u].w, w[1][u].w, x[j][u].z, x[j][u].w);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          red[warp][16 * i + g + 8 * (q >> 1)][8 * j + 2 * t + (q & 1)] = acc[i][j][q];
+      for (int q = 0; q < 4; ++q)
+        red[warp][g + 8 * (q >> 1)][8 * j + 2 * t + (q & 1)] = acc[j][q];
     __syncthreads();
-    for (int o = threadIdx.x; o < 16 * RT * 8 * NT; o += blockDim.x) {
-      const int n = o % (16 * RT), m = o / (16 * RT);
+    for (int o = threadIdx.x; o < 16 * 8 * NT; o += blockDim.x) {
+      const int n = o % 16, m = o / 16;
       if (rb + m < r1 && n0 + n < p.N) {
         int v = 0;
         for (int y = 0; y < warps; ++y) v += red[y][n][m];
@@ -228,9 +220,9 @@ __global__ void __launch_bounds__(32 * SM_WARPS, NT == 1 ? 2 : 1) i8_rows_kernel
   }
 }
 
-template <int RT, int NT, bool ALIGNED>
+template <int NT, bool ALIGNED>
 cudaError_t launch_as(const I8RowsParams& p, cudaStream_t st) {
-  const int tiles = (p.N + 16 * RT - 1) / (16 * RT);
+  const int tiles = (p.N + 15) / 16;
   // passes: at most one that is not full for each expert with rows
   const int experts = p.offsets ? std::min(p.E, p.R) : 1;
   const int passes = p.offsets ? experts + p.R / (8 * NT) : (p.R + 8 * NT - 1) / (8 * NT);
@@ -239,13 +231,13 @@ cudaError_t launch_as(const I8RowsParams& p, cudaStream_t st) {
   while (warps < SM_WARPS && 2 * warps <= steps / 2 &&
          static_cast<long long>(tiles) * experts * warps < SM_WARPS * p.num_sms)
     warps *= 2;
-  return launch_pdl(i8_rows_kernel<RT, NT, ALIGNED>, dim3(static_cast<unsigned>(static_cast<long long>(tiles) * passes)), dim3(32 * warps), 0, st, p);
+  return launch_pdl(i8_rows_kernel<NT, ALIGNED>, dim3(static_cast<unsigned>(static_cast<long long>(tiles) * passes)), dim3(32 * warps), 0, st, p);
 }
 
 template <bool ALIGNED>
 cudaError_t launch_rows(const I8RowsParams& p, cudaStream_t st) {
   const int rows = p.E > 1 ? (p.R + p.E - 1) / p.E : p.R;
-  return rows <= 8 ? launch_as<1, 1, ALIGNED>(p, st) : launch_as<1, 2, ALIGNED>(p, st);
+  return rows <= 8 ? launch_as<1, ALIGNED>(p, st) : launch_as<2, ALIGNED>(p, st);
 }
 
 }  // namespace

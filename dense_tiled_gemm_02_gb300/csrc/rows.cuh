@@ -423,8 +423,9 @@ __device__ __forceinline__ Vec<int8_t, VEC> block_integers(const float (&v)[VEC]
 // ---------------------------------------------------------------- items of rows
 constexpr int DEAL_THREADS = 128;  // of a block whose threads take items in turn
 
-// n / d for n < 2^31, by a multiplication (a 64-bit division would take longer
-// than the rest of an item).
+// n / d for n < 2^31, by a multiplication and a shift: the division by an invariant
+// integer of Granlund and Montgomery (1994), m = floor(2^32 (2^s - d) / d) + 1 with
+// 2^s >= d the least (a 64-bit division would take longer than the rest of an item).
 struct Divisor {
   uint32_t d, m, s;
 };
