@@ -298,13 +298,18 @@ int gemm_i8_create(gemm_op_t* out, const gemm_i8_desc_t* desc) {
   // 0.33 us a million weights and pass, against 6.5 and 0.19 of the tiles (16
   // rows of 4096 x 4096 8.4 and 10.9 us, of 8192 x 8192 23.7 and 19.0; 32 of
   // 1024 x 4096 5.3 and 7.6, of 4096 x 4096 14.4 and 10.9).  Tiles of 128 rows
-  // against the wide form: 4096 rows of 8192 x 8192 359 and 361 us, 8192 rows
-  // 716 and 623.
+  // against the wide form, N x K: 4096 rows of 8192 x 8192 363 and 362 us, 6144 of
+  // 4096 x 4096 147 and 141, 8192 of 8192 x 8192 714 and 625, of 8192 x 1024 108 and
+  // 89.  That is with at least four of the wide form's tiles for each of its CTA
+  // pairs: with fewer its last round costs more than the converters do (8192 rows of
+  // 2048 x 2048 59 and 70, of 256 x 8192 78 and 89, of 1024 x 8192 147 and 164;
+  // 16384 of 1024 x 8192 are an exception, 263 and 242).
   const bool some = d.K > 0 && d.R > 0 && d.N > 0;
   const int64_t mean = (d.R + d.E - 1) / d.E, passes = (mean + 15) / 16;
   const double weights = static_cast<double>(d.E) * d.N * d.K;
   const bool few = mean <= 8 || (passes <= 2 && (0.33 * passes - 0.19) * weights < 4.5e6);
-  const bool wide = some && planned("wide", d.R >= 6144ll * d.E);
+  const int64_t wide_tiles = d.E * ((mean + 255) / 256) * ((d.N + 255) / 256);
+  const bool wide = some && planned("wide", d.R >= 6144ll * d.E && wide_tiles >= 4ll * (sms / 2));
   const bool tiles = wide || (some && planned("tiles", !few));
   const int rows = wide ? 0 : planned("tall", mean > 64) ? 128 : 64;
   // X in fp16; W in fp16 (wide), or a copy where the TMA unit cannot read its

@@ -313,3 +313,21 @@ def test_i8_scales_the_same_in_every_form(counts, out):
         at += n
     for D, plan in zip(got[1:], PLANS[1:]):
         assert torch.equal(D, got[0]), plan
+
+
+# ---------------------------------------------------------------- forms of a product
+@pytest.mark.parametrize("E,R,N,K,form", [
+    (1, 8, 4096, 4096, "rows"), (1, 64, 4096, 4096, "tiles"), (1, 4096, 4096, 1024, "tiles"),
+    (1, 8192, 256, 2048, "tiles"), (1, 8192, 2048, 512, "tiles"), (1, 8192, 8192, 256, "wide"),
+    (8, 49152, 512, 256, "wide"), (8, 49152, 128, 256, "tiles"), (64, 64, 512, 256, "rows"),
+])
+def test_i8_form_by_rows_and_outputs(E, R, N, K, form):
+    """Both operands are widened where there are many rows and tiles enough for all SMs."""
+    X = torch.zeros((R, K), dtype=torch.int8, device="cuda")
+    W = torch.zeros((E, N, K), dtype=torch.int8, device="cuda")
+    xs, ws = torch.ones(R, device="cuda"), torch.ones((E, N), device="cuda")
+    off = offsets_of([R // E] * E) if E > 1 else None
+    D = torch.empty((R, N), dtype=BF16, device="cuda")
+    op = pkg.I8Gemm.like(X, xs, W, ws, off, D)
+    assert f"form={form} " in op.plan()
+    op.close()
