@@ -17,7 +17,7 @@
 //
 // Measured (one GB300, us, the floor in brackets): 1 x 4096 x 4096 4.6 (2.5),
 // 1 x 8192 x 8192 14.7 (10.0), 8 x 8192 x 8192 14.7, 16 rows 23.9; 64 rows over
-// 40 of 64 experts of 4096 x 2048 54.6 (50.3: 6.2 TB/s of weights).  Below that a
+// 40 of 64 experts of 4096 x 2048 55 (50.3: 6.1 TB/s of weights).  Below that a
 // launch, one trip to HBM and the sum over warps bound it (1 x 1024 x 4096 2.4,
 // 0.6).  An expert with most of the rows has its weights read, from L2, by every
 // pass of 8: 64 rows on 2 of 64 experts 16.3 (2.6), 512 on one 70 (4.4); the host

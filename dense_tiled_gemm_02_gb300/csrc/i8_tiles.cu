@@ -34,7 +34,8 @@
 // join (9 us around 11.5 of streaming); with many the converters (0.7-0.8 of the
 // tensor rate).  From 6144 rows an expert, with tiles enough for all pairs, both
 // operands are widened in HBM and go through grouped.cu's pairs instead: 8192 x
-// 8192 x 8192 609-626 (564) against 711.
+// 8192 x 8192 609-626 (564) against 711, 665 after seconds under the power cap.  W
+// off the 16-byte grid is copied on each call: 64 x 8192 x 8191 43 (10.3).
 // Not faster: X widened here as well (64 x 8192 x 8192 27 by the converters, 38 by
 // the epilogue's warps); CTA pairs with the weights in tensor memory (8192^3 911,
 // an arrival on the other CTA's barrier takes several times a local one's time).

@@ -9,12 +9,17 @@
 // is r max |h w|: known with the sum of squares, so that one reduction serves
 // both, and r falls out of the integers y / scale = 127 h w / max |h w|.
 //
-// Measured (one GB300, 16384 x 4096 bf16 with a residual, us, the floor in
-// brackets): 79 (80.3), to 8 bits 81 (70.3); the gradients 91 (80.3), from block
-// rows 89 (70.6) of which 3 are the last sum of dweight.  A row's gradients held
-// in registers between the passes, without the ring, 170 from block rows: a block
-// that waits for its row's sum has nothing in flight.  16 x 4096 to 8 bits: 2.5
-// in a graph; a call's host side takes 5.0.
+// Measured (one GB300, 16384 x 4096 bf16 with a residual, us, in brackets the bytes
+// at a copy's rate, which the forward pass beats because up to an L2 of what it
+// writes goes to HBM after its end): 79 (80.3), to 8 bits 80 (70.3); the gradients
+// 92 (80.3), from block rows 91 (70.6), of which 3 are the last sum of dweight; in
+// fp32 154 (160.6), 125 (130.5), and the gradients of 8192 rows 86 (80.3).  Rows
+// longer than the registers hold are read twice (2048 x 40000 bf16 149 (98), to 8
+// bits 182 (86)), the gradients' past the ring, too (2048 x 20000 bf16 164 (49),
+// 4096 x 16384 fp32 282 (161)).  A row's gradients held in registers between the
+// passes, without the ring, 170 from block rows: a block that waits for its row's
+// sum has nothing in flight.  16 x 4096 to 8 bits: 2.5 in a graph; a call's host
+// side takes 5.0.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

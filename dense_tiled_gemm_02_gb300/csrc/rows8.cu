@@ -11,10 +11,10 @@
 // of the rate, bounded the first form (40 us; 64-bit divisions for an item's row
 // another 5).
 //
-// Measured (one GB300, 16384 x 4096 bf16, floor 30.1 us each way): block rows 30.4
-// us and back 31.5, scaled rows 30.8 and back 31.2; 16384 x 4095, whose rows are
-// of any alignment, 57 and 53, 59 and 52 (an access an element: 174 and 137, 94
-// and 132).
+// Measured (one GB300, 16384 x 4096 bf16, floor 30.1 us each way): block rows 30.6
+// us and back 31.9, scaled rows 31.5 and back 31.9; in fp32 (50.2) 49 and 69, 48
+// and 69; 16384 x 4095, whose rows are of any alignment, 57 and 53, 60 and 52 (an
+// access an element: 174 and 137, 94 and 132), scaled rows in fp32 84 and 66.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
