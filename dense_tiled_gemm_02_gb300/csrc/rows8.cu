@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(THREADS)
 // A block (or, blockDim.x = 32, a warp) a row, whose threads hold NV vectors
 // each, or with NV = 0 (rows too long) read them again.
 // Registers: what 1024 threads have; those that hold fp32 of any alignment keep to
-// 48, at which five blocks of 256 threads fit an SM (52, four: 91 us instead of 77
-// for 16384 x 4095).
+// 48, at which five blocks of 256 threads fit an SM (16384 x 4095 84 us; with 52, so
+// that four fit, 91).
 template <typename T, int VEC, int NV, bool ANY>
 __global__ void __maxnreg__(ANY && sizeof(T) == 4 ? 48 : 64) pack_rows_kernel(const Rows8Params p) {
   __shared__ float2 part[32];
